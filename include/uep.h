@@ -16,7 +16,8 @@
  *     these calls; work is enqueued on `stream` (a hipStream_t; NULL = the null
  *     stream) and ordered with the caller's other work on that stream.
  *   - Integer arrays are int32, row-major, with the shapes given below.
- *     bf16 data is passed as raw uint16 bits and moved bit for bit.
+ *     bf16 data is passed as raw uint16 bits and moved bit for bit; calls with a
+ *     dtype argument take void pointers to UEP_F32 or UEP_BF16 elements.
  *   - Geometry: R virtual EP ranks, T tokens per rank, K routing slots per token,
  *     E logical experts, home(e) = e / (E / R) for the routed experts.  A physical
  *     instance id is i = r * inst_per_rank + j (rank r, local slot j); instance
@@ -63,8 +64,14 @@ enum {
   UEP_ERR_BAD_QUOTA = 16,   /* negative quota, or quota on an unused instance */
   UEP_ERR_COVER = 32,       /* a bucket position not covered by the transfer plan */
   UEP_ERR_LP = 64,          /* LPLB: an expert with load but no instance */
-  UEP_ERR_ROW_RANGE = 128   /* a dest_row entry outside [-1, out_rows) */
+  UEP_ERR_ROW_RANGE = 128,  /* a dest_row entry outside [-1, out_rows) */
+  UEP_ERR_LOGIT = 256,      /* a router logit (or logit's bias) that is NaN or +infinity */
+  UEP_ERR_GRAD = 512,       /* AdamW: a gradient element that is not finite */
+  UEP_ERR_PLAN = 1024       /* AdamW: not a plan for this call, or a step below 1 */
 };
+
+/* element types of the calls that take more than one */
+enum { UEP_F32 = 0, UEP_BF16 = 1 };
 
 /* Library version string and a static text for a status code (host). */
 const char* uep_version(void);
@@ -443,6 +450,177 @@ uep_status uep_lplb_plan(const int32_t* topk_ids, int32_t R, int32_t T, int32_t 
 uep_status uep_lplb_sample(const int32_t* topk_ids, int32_t R, int32_t T, int32_t K,
                            const void* lp, const float* x, uint64_t seed, uint64_t layer,
                            int32_t* dest_inst, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_gate -- the router gate: top-k expert ids and combine weights from the logits.
+ * [UEP] section "在 Gate 之后获取当前层真实负载": the path starts where the Gate has run;
+ * this is that Gate, so that a layer goes from router logits to the load matrix
+ * (topk_ids) and the combine (gate_w) without leaving the library.
+ *   scores     softmax: s_e = exp(l_e) / sum_j exp(l_j);  sigmoid: s_e = 1/(1 + exp(-l_e))
+ *   selection  the K largest of l_e (softmax) or of s_e + bias_e (sigmoid), in descending
+ *              order, ties to the lowest expert id
+ *   weights    w_k = scale * s_k, or with renorm scale * s_k / sum over the selected s
+ *              (all weights 0 if that sum is 0)
+ * Only finite logits are eligible (and enter the softmax's sum): -infinity, of the logit
+ * or of the bias, masks an expert; NaN and +infinity do too and are flagged.  A token with fewer than K eligible experts
+ * gets id -1 and weight 0 in the remaining slots.
+ *
+ *   logits     [R][T][E]  in   dtype UEP_F32 or UEP_BF16
+ *   bias       [E] fp32   in   optional, sigmoid only: enters the selection, not the weights
+ *   batch_size [R]        in   optional: tokens t >= batch_size[r] are absent (ids -1,
+ *                              weights 0, their logits are not read)
+ *   score                      UEP_GATE_SOFTMAX or UEP_GATE_SIGMOID
+ *   scale                      finite, not 0
+ *   topk_ids   [R][T][K]  out
+ *   gate_w     [R][T][K]  out  fp32; sums and exponentials are fp32
+ *   err                   out  optional; UEP_ERR_LOGIT
+ * Returns UEP_EINVAL for null pointers, sizes < 1 (T may be 0), an unknown dtype or
+ * score, a bias with softmax, a bad scale; UEP_EGEOM for R > 64, E > 4096, K > 64,
+ * K > E or R*T*K >= 2^31.
+ * ------------------------------------------------------------------------- */
+enum { UEP_GATE_SOFTMAX = 0, UEP_GATE_SIGMOID = 1 };
+uep_status uep_gate(const void* logits, int32_t dtype, const float* bias,
+                    const int32_t* batch_size, int32_t R, int32_t T, int32_t E, int32_t K,
+                    int32_t score, int32_t renorm, float scale, int32_t* topk_ids,
+                    float* gate_w, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_gate_grad -- gradient of uep_gate's weights with respect to the logits (the
+ * selection is piecewise constant, the bias gets no gradient).  With g_k = scale * dw_k
+ * and u_k = gate_w_k / scale over the selected slots:
+ *   softmax, renorm   dl_k = u_k (g_k - sum_j u_j g_j)
+ *   softmax           dl_e = s_e (g_e - sum_j u_j g_j), g_e = 0 unless e is selected
+ *   sigmoid, renorm   dl_k = u_k (1 - s_k) (g_k - sum_j u_j g_j)
+ *   sigmoid           dl_k = u_k (1 - u_k) g_k
+ * and 0 for every other expert.  Slots with id -1 take no part; a token whose slots are
+ * all -1 gets zeros.
+ *
+ *   dgate_w    [R][T][K] fp32  in   gradient of the weights (uep_combine_grad's dgate_w)
+ *   logits     [R][T][E]       in   as given to uep_gate
+ *   topk_ids, gate_w           in   as written by uep_gate with the same score, renorm
+ *                                   and scale
+ *   dlogits    [R][T][E]       out  the logits' dtype; every element is written
+ *   err                        out  optional; UEP_ERR_ID_RANGE: an id outside [-1, E),
+ *                                   taken as -1
+ * Returns UEP_EINVAL / UEP_EGEOM like uep_gate.
+ * ------------------------------------------------------------------------- */
+uep_status uep_gate_grad(const float* dgate_w, const void* logits, int32_t dtype,
+                         const int32_t* topk_ids, const float* gate_w, int32_t R, int32_t T,
+                         int32_t E, int32_t K, int32_t score, int32_t renorm, float scale,
+                         void* dlogits, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_permute_grad -- gradient of uep_permute: every token sums the gradients of the
+ * dispatch rows that hold a copy of it,
+ *   dx[r][t] = bf16( sum_k dout[dest_row[r][t][k]] ), slots with row -1 skipped,
+ * k ascending from +0.0, additions rounded to nearest even in fp32, then nearest-even
+ * rounding to bf16.  [UEP] section "复用前向方案，完成权重恢复与梯度归约": backward reuses
+ * the forward plan, here its dest_row.
+ *
+ *   dout     [out_rows][H] bf16   in   gradient of the dispatch buffer, 16-byte aligned
+ *   dest_row [R][T][K]            in   as given to uep_permute
+ *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end) are written
+ *   dx       [R][T][H] bf16 bits  out  16-byte aligned; other ranks' rows are untouched
+ *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
+ * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
+ * ------------------------------------------------------------------------- */
+uep_status uep_permute_grad(const uint16_t* dout, int64_t out_rows, const int32_t* dest_row,
+                            int32_t R, int32_t T, int32_t K, int32_t H, int32_t r_begin,
+                            int32_t r_end, uint16_t* dx, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_combine_grad -- gradient of uep_combine with respect to the expert outputs and
+ * to the combine weights, one pass over both:
+ *   dout[dest_row[r][t][k]] = bf16( w[r][t][k] * dy[r][t] )     (one fp32 product)
+ *   dgate_w[r][t][k]        = sum_h dy[r][t][h] * out[dest_row[r][t][k]][h]
+ * the sum in fp32, in an order that depends on the geometry alone (the same call gives the
+ * same bits).  Slots with row -1 move nothing and get dgate_w 0.  Rows of dout that no
+ * slot names are left as they are.
+ *
+ *   dy       [R][T][H] bf16       in   gradient of the combined output, 16-byte aligned
+ *   out      [out_rows][H] bf16   in   uep_combine's dispatch buffer; may be NULL together
+ *                                      with dgate_w (then only dout is computed)
+ *   dest_row [R][T][K]            in   as given to uep_combine (no row named twice)
+ *   gate_w   [R][T][K] fp32       in
+ *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end)
+ *   dout     [out_rows][H] bf16   out  16-byte aligned; may be `out` itself (in place)
+ *   dgate_w  [R][T][K] fp32       out  slots of other ranks are untouched
+ *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
+ * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
+ * ------------------------------------------------------------------------- */
+uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, int64_t out_rows,
+                            const int32_t* dest_row, const float* gate_w, int32_t R, int32_t T,
+                            int32_t K, int32_t H, int32_t r_begin, int32_t r_end,
+                            uint16_t* dout, float* dgate_w, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * AdamW -- one optimizer step over many tensors in one launch.
+ * [UEP] section "共享冗余 slot 管理动态专家副本": redundant slots hold weights and gradients
+ * but no optimizer state; after the gradient reduction the mains alone are stepped.
+ * For every element, with t the step, lr = sched[0] * lr_scale, g = sched[1] * grad:
+ *   m = b1 m + (1 - b1) g;   v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
+ * in fp32 (every product and sum of m and v rounded on its own; the quotient within a few
+ * units in the last place).  An element whose g is not finite takes g = 0 and is flagged.
+ *
+ * States are fp32 or 8 bits.  8-bit states keep the upper bits of the fp32 number (its 8
+ * exponent bits and 3 mantissa bits: its level), as a distance from the largest level of
+ * each block of 256 elements: m in sign and 7 bits, v (never negative) in 8 bits.
+ *   code 0 = zero; v code c = level top_v - 255 + c, m code c = level top_m - 127 + c
+ *   tops[block] = top_m | top_v << 16; an m below the window becomes 0, a v above 0 never
+ *   falls below code 1, so no quotient grows by rounding
+ * Both are rounded stochastically (added to the lower 20 bits before they are cut), since
+ * a second moment that moves by 1 - b2 of itself a step would otherwise stay where it is
+ * for ever.  bf16 parameters are rounded the same way from the fp32 result.  The random
+ * bits are a function of (seed, t, the tensor's index, the element's index) alone:
+ *   key = mix(mix(t * 0x9E3779B9 + seed) ^ (index + 1));  for the elements 4i .. 4i+3
+ *   w0 = mix(i * 0x9E3779B9 ^ key), w1..w5 each the next xorshift (13, 17, 5) of the last
+ *   element 4i+j: parameter the lower (j even) or upper half of w[j / 2], m the lower and v
+ *   the upper half of w[2 + j];  all 32-bit;
+ *   mix(x): x ^= x >> 16; x *= 0x9E3779B9; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16
+ * with half a step = 2^15, added in units of 2^-16 of a step.
+ *
+ * uep_adamw_prepare (offline): copies a HOST table of tensors into the device buffer
+ *   `plan` of uep_adamw_plan_size() bytes (synchronous copy; outside the hot loop) and
+ *   writes the number of work tiles to *n_tiles (host).  The tensors stay where they are.
+ *   Every tensor of a plan has the same types: param_dtype and grad_dtype UEP_F32 or
+ *   UEP_BF16, state_bits 32 (m, v fp32) or 8 (m, v uint8, with tops); states start as
+ *   zeros.  `copy` is optional with fp32 parameters: the new value rounded to nearest bf16.
+ *   Pointers need the alignment of their own type only; tensors in which every group of four
+ *   elements is aligned (16 bytes of fp32, 8 of bf16, 4 of codes) are faster.
+ *   At most 65535 tensors of at most 2^33 elements.
+ * uep_adamw: one step.  n_tiles and the types as given to and by uep_adamw_prepare.
+ *   step   [1] int32  in   t >= 1, device memory
+ *   sched  [2] fp32   in   {learning rate, factor on every gradient}, device memory, so a
+ *                          captured graph can be replayed with new values
+ *   0 <= beta1, beta2 < 1, eps > 0 (double: 1 - beta is formed before it is rounded)
+ *   err               out  optional; UEP_ERR_GRAD, UEP_ERR_PLAN (then nothing else is written)
+ * uep_adamw_decode: the values that 8-bit states stand for (checkpoints), n elements from
+ *   the start of a tensor or of several whose starts are multiples of 256 apart;
+ *   m, v [n] of dtype UEP_F32 or UEP_BF16 (both hold them exactly)
+ * ------------------------------------------------------------------------- */
+typedef struct uep_adamw_tensor {
+  void* param;          /* [n] param_dtype, updated */
+  const void* grad;     /* [n] grad_dtype */
+  void* m;              /* [n] fp32 or uint8, updated */
+  void* v;              /* [n] fp32 or uint8, updated */
+  int32_t* tops;        /* [ceil(n / 256)], 8-bit states only (else NULL), updated */
+  uint16_t* copy;       /* [n] bf16 bits, written; optional, fp32 parameters only */
+  int64_t n;            /* elements, may be 0 */
+  float weight_decay;   /* wd */
+  float lr_scale;       /* this tensor's factor on the learning rate */
+} uep_adamw_tensor;
+size_t uep_adamw_plan_size(const uep_adamw_tensor* tensors_host, int32_t count);
+uep_status uep_adamw_prepare(const uep_adamw_tensor* tensors_host, int32_t count,
+                             int32_t param_dtype, int32_t grad_dtype, int32_t state_bits,
+                             void* plan, size_t plan_bytes, int64_t* n_tiles, void* stream);
+uep_status uep_adamw(const void* plan, int64_t n_tiles, int32_t param_dtype,
+                     int32_t grad_dtype, int32_t state_bits, const int32_t* step,
+                     const float* sched, double beta1, double beta2, double eps,
+                     uint32_t seed, int32_t* err, void* stream);
+uep_status uep_adamw_decode(const uint8_t* m_codes, const uint8_t* v_codes,
+                            const int32_t* tops, int64_t n, int32_t dtype, void* m, void* v,
+                            void* stream);
 
 #ifdef __cplusplus
 }

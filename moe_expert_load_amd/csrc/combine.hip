@@ -13,6 +13,9 @@
 // per lane (4 KiB per wave); the slices of 4 consecutive k are loaded together
 // (non-temporal: every dispatch row is read once; +3 % measured) before they are
 // accumulated in order.
+//
+// uep_permute_grad is the same gather without weights (every copy of a token hands its
+// gradient back): the kernel's unweighted form, dx[g] = bf16( sum_k dout[dest_row[g][k]] ).
 #include "common.h"
 
 namespace uep {
@@ -22,16 +25,7 @@ constexpr int kCbTokPerBlock = kCbThreads / kWave;
 constexpr int kCbVec = 4;     // 16-byte vectors per lane per slice (8 bf16 each)
 constexpr int kCbGroup = 4;   // rows loaded together
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// nearest-even fp32 -> bf16; a NaN becomes a quiet NaN with its sign
-__device__ __forceinline__ uint32_t f32_to_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7F800000u) == 0x7F800000u && (u & 0x007FFFFFu) != 0u) return ((u >> 16) | 0x40u) & 0xFFFFu;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-
+template <bool kWeighted>
 __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __restrict__ y_disp,
                                                              const int32_t* __restrict__ dest_row,
                                                              const float* __restrict__ gate_w,
@@ -46,7 +40,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
   const int64_t g = g0 + b * kCbTokPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (g >= g1) return;
   const int d_mine = checked_row(lane < K ? dest_row[g * K + lane] : -1, out_rows, err);
-  const int w_mine = lane < K ? __float_as_int(gate_w[g * K + lane]) : 0;
+  const int w_mine = kWeighted && lane < K ? __float_as_int(gate_w[g * K + lane]) : 0;
   for (int v0 = 0; v0 < nvec; v0 += kCbVec * kWave) {
     float acc[kCbVec * 8];
 #pragma unroll
@@ -74,8 +68,8 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
         for (int u = 0; u < kCbVec; ++u) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float p0 = w * bf16_lo(buf[q][u][c]);
-            const float p1 = w * bf16_hi(buf[q][u][c]);
+            const float p0 = kWeighted ? w * bf16_lo(buf[q][u][c]) : bf16_lo(buf[q][u][c]);
+            const float p1 = kWeighted ? w * bf16_hi(buf[q][u][c]) : bf16_hi(buf[q][u][c]);
             acc[u * 8 + 2 * c] = acc[u * 8 + 2 * c] + p0;
             acc[u * 8 + 2 * c + 1] = acc[u * 8 + 2 * c + 1] + p1;
           }
@@ -94,6 +88,29 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
   }
 }
 
+// The argument checks and the launch that both entry points share.
+static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_t* dest_row,
+                            const float* gate_w, bool weighted, int32_t R, int32_t T, int32_t K,
+                            int32_t H, int32_t r_begin, int32_t r_end, uint16_t* y, int32_t* err,
+                            void* stream) {
+  if (R <= 0 || T < 0 || K <= 0 || H <= 0 || out_rows < 0) return UEP_EINVAL;
+  if (r_begin < 0 || r_end > R || r_begin > r_end) return UEP_EINVAL;
+  if (K > 64 || H % 8 != 0 || H > (1 << 29) || (int64_t)R * T * K >= (1ll << 31))
+    return UEP_EGEOM;
+  const int64_t g0 = (int64_t)r_begin * T, g1 = (int64_t)r_end * T;
+  if (g1 == g0) return UEP_OK;
+  if (!rows || !dest_row || (weighted && !gate_w) || !y) return UEP_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(y)) % 16 != 0)
+    return UEP_EGEOM;
+  const int64_t blocks = (g1 - g0 + kCbTokPerBlock - 1) / kCbTokPerBlock;
+  auto kernel = weighted ? combine_kernel<true> : combine_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kCbThreads), 0, uep_stream(stream),
+                     reinterpret_cast<const u32x4*>(rows), dest_row, gate_w,
+                     reinterpret_cast<u32x4*>(y), out_rows, g0, g1, K, H / 8, err);
+  UEP_CHECK_LAUNCH();
+  return UEP_OK;
+}
+
 }  // namespace uep
 
 using namespace uep;
@@ -102,19 +119,14 @@ extern "C" uep_status uep_combine(const uint16_t* y_disp, int64_t out_rows,
                                   const int32_t* dest_row, const float* gate_w, int32_t R,
                                   int32_t T, int32_t K, int32_t H, int32_t r_begin, int32_t r_end,
                                   uint16_t* y, int32_t* err, void* stream) {
-  if (R <= 0 || T < 0 || K <= 0 || H <= 0 || out_rows < 0) return UEP_EINVAL;
-  if (r_begin < 0 || r_end > R || r_begin > r_end) return UEP_EINVAL;
-  if (K > 64 || H % 8 != 0 || H > (1 << 29) || (int64_t)R * T * K >= (1ll << 31))
-    return UEP_EGEOM;
-  const int64_t g0 = (int64_t)r_begin * T, g1 = (int64_t)r_end * T;
-  if (g1 == g0) return UEP_OK;
-  if (!y_disp || !dest_row || !gate_w || !y) return UEP_EINVAL;
-  if ((reinterpret_cast<uintptr_t>(y_disp) | reinterpret_cast<uintptr_t>(y)) % 16 != 0)
-    return UEP_EGEOM;
-  const int64_t blocks = (g1 - g0 + kCbTokPerBlock - 1) / kCbTokPerBlock;
-  hipLaunchKernelGGL(combine_kernel, dim3((unsigned)blocks), dim3(kCbThreads), 0,
-                     uep_stream(stream), reinterpret_cast<const u32x4*>(y_disp), dest_row, gate_w,
-                     reinterpret_cast<u32x4*>(y), out_rows, g0, g1, K, H / 8, err);
-  UEP_CHECK_LAUNCH();
-  return UEP_OK;
+  return cb_launch(y_disp, out_rows, dest_row, gate_w, true, R, T, K, H, r_begin, r_end, y, err,
+                   stream);
+}
+
+extern "C" uep_status uep_permute_grad(const uint16_t* dout, int64_t out_rows,
+                                       const int32_t* dest_row, int32_t R, int32_t T, int32_t K,
+                                       int32_t H, int32_t r_begin, int32_t r_end, uint16_t* dx,
+                                       int32_t* err, void* stream) {
+  return cb_launch(dout, out_rows, dest_row, nullptr, false, R, T, K, H, r_begin, r_end, dx, err,
+                   stream);
 }

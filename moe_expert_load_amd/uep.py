@@ -22,13 +22,20 @@ LIB_PATH = os.path.join(_HERE, "libuep.so")
 OK, EINVAL, EGEOM, EWORKSPACE, EHIP = 0, 1, 2, 3, 4
 ERR_ID_RANGE, ERR_DUP_ID, ERR_QUOTA_SUM, ERR_INST_DUP = 1, 2, 4, 8
 ERR_BAD_QUOTA, ERR_COVER, ERR_LP, ERR_ROW_RANGE = 16, 32, 64, 128
+ERR_LOGIT, ERR_GRAD, ERR_PLAN = 256, 512, 1024
 STAGE_WEIGHTS, STAGE_GRAD_REDUCE = 0, 1
+F32, BF16 = 0, 1
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
+ADAMW_BLOCK = 256       # elements of one tensor that share an entry of `tops` (8-bit states)
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
 _SZ = ctypes.c_size_t
+_U32 = ctypes.c_uint32
+_F = ctypes.c_float
+_D = ctypes.c_double
 
 # name -> (restype, argtypes); the exact list of symbols include/uep.h declares
 SIGNATURES = {
@@ -58,6 +65,14 @@ SIGNATURES = {
     "uep_lplb": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P]),
     "uep_lplb_plan_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "uep_lplb_plan": (_I, [_P, _I, _I, _I, _I, _P, _I, _P, _I, _I, _I] + [_P] * 12 + [_SZ, _P]),
+    "uep_gate": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
+    "uep_gate_grad": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "uep_permute_grad": (_I, [_P, _I64, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "uep_combine_grad": (_I, [_P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "uep_adamw_plan_size": (_SZ, [_P, _I]),
+    "uep_adamw_prepare": (_I, [_P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
+    "uep_adamw": (_I, [_P, _I64, _I, _I, _I, _P, _P, _D, _D, _D, _U32, _P, _P]),
+    "uep_adamw_decode": (_I, [_P, _P, _P, _I64, _I, _P, _P, _P]),
 }
 
 
@@ -314,6 +329,229 @@ def combine(out, dest_row, gate_w, y, r_begin=0, r_end=None, stream=None, err=No
     _check(LIB.uep_combine(_p(out), out.shape[0], _p(dest_row), _p(gate_w), R, T, K, H, r_begin,
                            r_end, _p(y), _p(err), _s(stream)), "uep_combine")
     return y
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _rows16(t: torch.Tensor, shape, name: str) -> None:
+    """A 16-bit tensor of exactly this shape (the row moves index it by the geometry)."""
+    if t.element_size() != 2 or tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name} must hold 16-bit elements of shape {list(shape)}, got "
+                        f"{t.dtype} {list(t.shape)}")
+
+
+def gate(logits, K, bias=None, batch_size=None, score=GATE_SOFTMAX, renorm=True, scale=1.0,
+         topk_ids=None, gate_w=None, err=None, stream=None):
+    """Router gate: logits [R][T][E] float32 or bfloat16 -> topk_ids [R][T][K] int32 (ties to
+    the lowest id, -1 where no expert is eligible) and gate_w [R][T][K] float32."""
+    if logits.dim() != 3:
+        raise TypeError("logits must be [R][T][E]")
+    R, T, E = logits.shape
+    dt = _dtype(logits, "logits")
+    _buf(bias, E, "bias", torch.float32)
+    _buf(batch_size, R, "batch_size")
+    _buf(err, 1, "err")
+    n = R * T * K
+    topk_ids = _new((R, T, K), logits) if topk_ids is None else _buf(topk_ids, n, "topk_ids")
+    gate_w = _new((R, T, K), logits, torch.float32) if gate_w is None \
+        else _buf(gate_w, n, "gate_w", torch.float32)
+    _check(LIB.uep_gate(_p(logits), dt, _p(bias), _p(batch_size), R, T, E, K, score,
+                        1 if renorm else 0, scale, _p(topk_ids), _p(gate_w), _p(err), _s(stream)),
+           "uep_gate")
+    return topk_ids, gate_w
+
+
+def gate_grad(dgate_w, logits, topk_ids, gate_w, score=GATE_SOFTMAX, renorm=True, scale=1.0,
+              dlogits=None, err=None, stream=None):
+    """Gradient of gate's weights: dgate_w [R][T][K] float32 -> dlogits [R][T][E] of the
+    logits' dtype, given what gate took and wrote."""
+    if logits.dim() != 3 or topk_ids.dim() != 3:
+        raise TypeError("logits must be [R][T][E] and topk_ids [R][T][K]")
+    R, T, E = logits.shape
+    dt = _dtype(logits, "logits")
+    _i32(topk_ids, "topk_ids")
+    if tuple(topk_ids.shape[:2]) != (R, T):
+        raise TypeError("logits and topk_ids must have the same [R][T]")
+    K = topk_ids.shape[2]
+    _buf(gate_w, R * T * K, "gate_w", torch.float32)
+    _buf(dgate_w, R * T * K, "dgate_w", torch.float32)
+    _buf(err, 1, "err")
+    dlogits = _new((R, T, E), logits, logits.dtype) if dlogits is None \
+        else _buf(dlogits, R * T * E, "dlogits", logits.dtype)
+    if dlogits.dtype != logits.dtype:
+        raise TypeError("dlogits must have the logits' dtype")
+    _check(LIB.uep_gate_grad(_p(dgate_w), _p(logits), dt, _p(topk_ids), _p(gate_w), R, T, E, K,
+                             score, 1 if renorm else 0, scale, _p(dlogits), _p(err), _s(stream)),
+           "uep_gate_grad")
+    return dlogits
+
+
+def permute_grad(dout, dest_row, dx, r_begin=0, r_end=None, stream=None, err=None):
+    """Gradient of permute: dout [P][H] bf16 -> dx [R][T][H] bf16, the sum over every token's
+    dispatch rows (rows of ranks in [r_begin, r_end) are written)."""
+    _i32(dest_row, "dest_row")
+    if dout.dim() != 2 or dest_row.dim() != 3:
+        raise TypeError("dout must be [P][H] and dest_row [R][T][K]")
+    R, T, K = dest_row.shape
+    P, H = dout.shape
+    r_end = R if r_end is None else r_end
+    _rows16(dout, (P, H), "dout")
+    _rows16(dx, (R, T, H), "dx")
+    _buf(err, 1, "err")
+    _check(LIB.uep_permute_grad(_p(dout), P, _p(dest_row), R, T, K, H, r_begin, r_end, _p(dx),
+                                _p(err), _s(stream)), "uep_permute_grad")
+    return dx
+
+
+def combine_grad(dy, out, dest_row, gate_w, dout, dgate_w=None, r_begin=0, r_end=None,
+                 stream=None, err=None):
+    """Gradients of combine: dy [R][T][H] bf16 -> dout [P][H] bf16 (the gradient of the expert
+    outputs; may be `out` itself) and dgate_w [R][T][K] float32.  With out None only dout is
+    computed."""
+    _i32(dest_row, "dest_row")
+    if dout.dim() != 2 or dest_row.dim() != 3:
+        raise TypeError("dout must be [P][H] and dest_row [R][T][K]")
+    R, T, K = dest_row.shape
+    P, H = dout.shape
+    r_end = R if r_end is None else r_end
+    _rows16(dy, (R, T, H), "dy")
+    _rows16(dout, (P, H), "dout")
+    if gate_w.dtype != torch.float32 or tuple(gate_w.shape) != (R, T, K):
+        raise TypeError("gate_w must be float32 [R][T][K]")
+    if out is None:
+        if dgate_w is not None:
+            raise TypeError("dgate_w needs the expert outputs `out`")
+    else:
+        _rows16(out, (P, H), "out")
+        dgate_w = _new((R, T, K), dy, torch.float32) if dgate_w is None else dgate_w
+        if dgate_w.dtype != torch.float32 or tuple(dgate_w.shape) != (R, T, K):
+            raise TypeError("dgate_w must be float32 [R][T][K]")
+    _buf(err, 1, "err")
+    _check(LIB.uep_combine_grad(_p(dy), _p(out), P, _p(dest_row), _p(gate_w), R, T, K, H, r_begin,
+                                r_end, _p(dout), _p(dgate_w), _p(err), _s(stream)),
+           "uep_combine_grad")
+    return dout, dgate_w
+
+
+class AdamWTensor(ctypes.Structure):
+    """struct uep_adamw_tensor of include/uep.h."""
+
+    _fields_ = [("param", _P), ("grad", _P), ("m", _P), ("v", _P), ("tops", _P), ("copy", _P),
+                ("n", _I64), ("weight_decay", _F), ("lr_scale", _F)]
+
+
+@dataclasses.dataclass(frozen=True)
+class AdamWPlan:
+    """A table of tensors from adamw_prepare: the device buffer, the sizes and types every
+    step passes back, and the tensors themselves, which the plan points into."""
+
+    buf: torch.Tensor
+    n_tiles: int
+    param_dtype: int
+    grad_dtype: int
+    state_bits: int
+    tensors: tuple
+
+
+def _per_tensor(x, n, name):
+    x = [float(x)] * n if isinstance(x, (int, float)) else [float(v) for v in x]
+    if len(x) != n:
+        raise TypeError(f"{name} must be one number or one for each of the {n} tensors")
+    return x
+
+
+def adamw_prepare(params, grads, m, v, copies=None, tops=None, weight_decay=0.0, lr_scale=1.0,
+                  device=None, stream=None) -> AdamWPlan:
+    """Offline: the plan of an AdamW step over lists of contiguous tensors.  params and grads
+    float32 or bfloat16 (one type each); m and v float32, or uint8 with `tops` (int32, one entry
+    per 256 elements) for 8-bit states; copies (bfloat16, optional) take the new values of
+    float32 params.  weight_decay and lr_scale: one number, or one per tensor."""
+    n = len(params)
+    lists = {"grads": grads, "m": m, "v": v, "copies": copies, "tops": tops}
+    for name, x in lists.items():
+        if x is not None and len(x) != n:
+            raise TypeError(f"{name} must have one tensor for each of the {n} params")
+    if m is None or v is None or grads is None:
+        raise TypeError("grads, m and v are needed")
+    bits = 8 if tops is not None else 32
+    state = torch.uint8 if bits == 8 else torch.float32
+    pd = _dtype(params[0], "params") if n else F32
+    gd = _dtype(grads[0], "grads") if n else F32
+    if copies is not None and pd != F32:
+        raise TypeError("copies go with float32 params")
+    wd, ls = _per_tensor(weight_decay, n, "weight_decay"), _per_tensor(lr_scale, n, "lr_scale")
+    table = (AdamWTensor * max(n, 1))()
+    written = []
+    for i in range(n):
+        k = params[i].numel()
+        want = [(params[i], params[0].dtype, k, "params"), (grads[i], grads[0].dtype, k, "grads"),
+                (m[i], state, k, "m"), (v[i], state, k, "v")]
+        if bits == 8:
+            want.append((tops[i], torch.int32, -(-k // ADAMW_BLOCK), "tops"))
+        if copies is not None:
+            want.append((copies[i], torch.bfloat16, k, "copies"))
+        for t, dt, size, name in want:
+            if t.dtype != dt or t.numel() != size or t.device != params[0].device:
+                raise TypeError(f"{name}[{i}] must be {dt} with {size} elements on "
+                                f"{params[0].device}, got {t.dtype}, {t.numel()}, {t.device}")
+        for t, dt, size, name in want:
+            _p(t)
+            if name != "grads" and size:
+                written.append((t.data_ptr(), t.data_ptr() + size * t.element_size(),
+                                f"{name}[{i}]"))
+        table[i] = AdamWTensor(params[i].data_ptr(), grads[i].data_ptr(), m[i].data_ptr(),
+                               v[i].data_ptr(), tops[i].data_ptr() if bits == 8 else None,
+                               copies[i].data_ptr() if copies is not None else None, k, wd[i],
+                               ls[i])
+    written.sort()
+    for a, b in zip(written, written[1:]):
+        if b[0] < a[1]:
+            raise TypeError(f"{a[2]} and {b[2]} overlap: one step would write them twice")
+    need = int(LIB.uep_adamw_plan_size(table, n))
+    dev = params[0].device if n else torch.device("cuda" if device is None else device)
+    buf = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    tiles = ctypes.c_int64(0)
+    _check(LIB.uep_adamw_prepare(table, n, pd, gd, bits, _p(buf), buf.numel(),
+                                 ctypes.byref(tiles), _s(stream)), "uep_adamw_prepare")
+    keep = tuple(tuple(x) for x in (params, grads, m, v, copies or (), tops or ()))
+    return AdamWPlan(buf, tiles.value, pd, gd, bits, keep)
+
+
+def adamw(plan, step, sched, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, err=None, stream=None):
+    """One AdamW step over the plan's tensors, in place.  step: int32 [1] on the device, the
+    number of this step (from 1); sched: float32 [2] on the device, the learning rate and a
+    factor on every gradient; seed: of the stochastic rounding (8-bit states, bf16 params)."""
+    if not isinstance(plan, AdamWPlan):
+        raise TypeError("plan must be the AdamWPlan that adamw_prepare returned")
+    _buf(step, 1, "step")
+    _buf(sched, 2, "sched", torch.float32)
+    _buf(err, 1, "err")
+    _check(LIB.uep_adamw(_p(plan.buf), plan.n_tiles, plan.param_dtype, plan.grad_dtype,
+                         plan.state_bits, _p(step), _p(sched), beta1, beta2, eps,
+                         seed & 0xFFFFFFFF, _p(err), _s(stream)), "uep_adamw")
+
+
+def adamw_decode(m_codes, v_codes, tops, m=None, v=None, dtype=torch.float32, stream=None):
+    """The values of 8-bit AdamW states: m_codes and v_codes uint8 [n] with their `tops` ->
+    m, v [n] (float32 or bfloat16, both exact)."""
+    n = m_codes.numel()
+    _buf(m_codes, n, "m_codes", torch.uint8)
+    _buf(v_codes, n, "v_codes", torch.uint8)
+    _buf(tops, -(-n // ADAMW_BLOCK), "tops")
+    m = _new(m_codes.shape, m_codes, dtype) if m is None else m
+    v = _new(m_codes.shape, m_codes, dtype) if v is None else v
+    dt = _dtype(m, "m")
+    _buf(m, n, "m", m.dtype)
+    _buf(v, n, "v", m.dtype)
+    _check(LIB.uep_adamw_decode(_p(m_codes), _p(v_codes), _p(tops), n, dt, _p(m), _p(v),
+                                _s(stream)), "uep_adamw_decode")
+    return m, v
 
 
 def device_copy(src, dst, stream=None):

@@ -23,6 +23,9 @@ the path itself fixes fp32).  Sources:
     - "从LP解决方案到Token调度" (from LP to token dispatch)               -> lplb
     - "背景知识与设计原则", "共享专家融合作为启用机制" (dispatch and combine) -> combine
 
+The training operators around the path (router gate, gradients of dispatch and combine,
+AdamW) are in gate, row_grad and adamw; the pages name these steps without writing them out.
+
 Parity status of each function (what pins it) is listed in the module headers.
 """
 
@@ -35,11 +38,14 @@ from .stage import stage_forward, grad_reduce
 from .philox import philox4x64_10, philox4x64_10_np
 from .waterfill import waterfill, extend_topk
 from .lplb import lplb_structure, lplb_lp, simplex, hamilton_quotas, lplb, lplb_sample
+from .gate import gate, gate_grad, gate_keys
+from .row_grad import permute_grad, combine_grad
+from . import adamw
 
 __all__ = [
     "load_matrix", "OracleInputError", "solve_quota", "reroute", "assign", "identity_quota",
     "permute", "permute_rows", "row_sources", "rows_of", "combine", "combine_f32", "combine_tokens", "f32_to_bf16_bits",
     "bf16_bits_to_f32", "stage_forward", "grad_reduce", "philox4x64_10", "philox4x64_10_np",
     "waterfill", "extend_topk", "lplb_structure", "lplb_lp", "simplex", "hamilton_quotas", "lplb",
-    "lplb_sample",
+    "lplb_sample", "gate", "gate_grad", "gate_keys", "permute_grad", "combine_grad", "adamw",
 ]

@@ -1,0 +1,241 @@
+"""GPU parity of uep_gate and uep_gate_grad against the oracle (64 bits).
+
+Ids have to be equal: softmax selects on the logits themselves, and the sigmoid cases are
+drawn so that no two selection scores of a token's best are nearer than fp32 can tell (checked
+on the oracle's scores).  Weights, in units eps = 2^-24 relative to the weight: one rounded
+difference inside the exponential (eps times the distance d to the largest logit), expf and
+sigmoid within 4 + 4 eps, a sum of E terms in any order (bounded by its longest chain,
+at most E / 16 + 8 additions, times the worst term's error again), a division and a product
+(4 eps).  Gradients: products and sums of at most K terms on top, relative to the sum of
+magnitudes; bf16 results add half a unit, 2^-8."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import oracle as O                                       # noqa: E402
+from moe_expert_load_amd import uep as U                 # noqa: E402
+from tests.gpu_helpers import DEV, to_dev, host, say, err_word  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24
+
+
+def draw_logits(seed, R, T, E, dtype, masked=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = 1.5 * torch.randn(R, T, E, generator=g)
+    if masked:
+        x[torch.rand(R, T, E, generator=g) < masked] = -float("inf")
+    return x.to(dtype)
+
+
+def weight_tol(x64, E):
+    finite = np.where(np.isfinite(x64), x64, 0.0)
+    d = finite.max(-1, keepdims=True) - finite.min(-1, keepdims=True)
+    return EPS * (2 * d + E / 16 + 40)
+
+
+def run_gate(x, K, bias=None, bs=None, score=0, renorm=True, scale=1.0):
+    err = err_word()
+    ids, w = U.gate(x.to(DEV), K, bias=None if bias is None else to_dev(bias, torch.float32),
+                    batch_size=None if bs is None else to_dev(bs), score=score, renorm=renorm,
+                    scale=scale, err=err)
+    return host(ids), host(w), int(host(err)[0])
+
+
+def check(seed, R, T, E, K, dtype, score, renorm, scale, masked=0.0, bs=None):
+    x = draw_logits(seed, R, T, E, dtype, masked)
+    x64 = x.double().numpy()
+    bias = (np.random.default_rng(seed).standard_normal(E) * 0.1).astype(np.float32) if score \
+        else None
+    ids_o, w_o = O.gate(x64, K, bias, bs, score, renorm, scale)
+    if score:            # rows in which fp32 may not tell two of the best apart are made equal
+        key = -np.sort(-O.gate_keys(x64, bias, score), -1)[..., :K + 1]
+        with np.errstate(invalid="ignore"):
+            gap = np.where(np.isfinite(key[..., 1:]), key[..., :-1] - key[..., 1:], 1.0)
+        near = gap.min(-1) < 8 * EPS if gap.shape[-1] else np.zeros((R, T), bool)
+        assert near.mean() < 0.05
+        far = np.argwhere(~near)[0]
+        x[torch.from_numpy(near)] = x[far[0], far[1]].clone()
+        x64 = x.double().numpy()
+        ids_o, w_o = O.gate(x64, K, bias, bs, score, renorm, scale)
+    ids, w, err = run_gate(x, K, bias, bs, score, renorm, scale)
+    assert err == 0
+    assert np.array_equal(ids, ids_o)
+    assert (np.abs(w - w_o) <= weight_tol(x64, E) * np.abs(w_o) + 1e-37).all()
+
+    # the gradient takes the library's own weights, as a program does
+    dw = np.random.default_rng(seed + 1).standard_normal((R, T, K)).astype(np.float32)
+    err = err_word()
+    d = U.gate_grad(to_dev(dw, torch.float32), x.to(DEV), to_dev(ids), to_dev(w, torch.float32),
+                    score=score, renorm=renorm, scale=scale, err=err)
+    assert int(host(err)[0]) == 0 and d.dtype == dtype
+    d_o = O.gate_grad(dw, x64, ids, w, score, renorm, scale)
+    on = ids >= 0
+    g = np.where(on, np.abs(dw * scale), 0.0)
+    s = O.gate_grad(np.zeros_like(dw), x64, ids, w, score, renorm, scale) * 0 + 1.0   # [R][T][E]
+    mag = s * (g.max(-1, keepdims=True) + (np.abs(w / scale) * g).sum(-1, keepdims=True))
+    if score == 0 and not renorm:      # the dense gradient scales with the expert's own score
+        fin = np.where(np.isfinite(x64), x64, -np.inf)
+        e = np.exp(fin - np.where(np.isfinite(fin.max(-1, keepdims=True)),
+                                  fin.max(-1, keepdims=True), 0))
+        mag = mag * e / np.maximum(e.sum(-1, keepdims=True), 1e-300)
+    bound = weight_tol(x64, E) * mag + EPS * (K + 8) * mag + 1e-37
+    if dtype == torch.bfloat16:
+        bound = bound * 1.01 + 2.0 ** -8 * np.abs(d_o)
+    assert (np.abs(host(d.float()) - d_o) <= bound).all()
+
+
+F, B = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("seed,R,T,E,K,dtype,score,renorm,scale,masked", [
+    (0, 4, 33, 128, 8, F, 0, True, 1.0, 0.0),       # Qwen-shaped router
+    (1, 2, 65, 256, 8, B, 1, True, 2.5, 0.0),       # DeepSeek-V3-shaped router
+    (2, 1, 1, 128, 8, F, 0, True, 1.0, 0.0),        # one token
+    (3, 1, 3, 1, 1, F, 0, False, 1.0, 0.0),         # one expert
+    (4, 3, 7, 61, 4, B, 0, False, 1.0, 0.3),        # odd expert count, masked experts
+    (5, 2, 19, 60, 4, F, 0, False, 0.5, 0.0),
+    (6, 2, 17, 8, 8, F, 1, False, -1.5, 0.2),       # K = E, negative scale, fewer than K left
+    (7, 1, 40, 200, 9, F, 1, True, 1.0, 0.1),       # K above eight
+    (8, 1, 13, 513, 10, B, 0, True, 1.0, 0.0),
+    (9, 2, 9, 1000, 16, F, 0, False, 1.0, 0.9),
+    (10, 1, 5, 4096, 64, F, 0, True, 1.0, 0.0),     # the largest sizes
+    (11, 1, 6, 3001, 33, B, 1, False, 1.0, 0.5),
+    (12, 5, 31, 96, 6, B, 0, True, 1.0, 0.95),      # rows with few experts left, some with none
+    (13, 7, 301, 130, 2, F, 0, True, 1.0, 0.0),
+    (14, 2, 77, 24, 3, F, 0, False, 1.0, 0.05),
+    (15, 1, 130, 320, 5, B, 0, False, 1.0, 0.0),
+])
+def test_gate_and_gradient(seed, R, T, E, K, dtype, score, renorm, scale, masked):
+    say("case: gate", seed, R, T, E, K, dtype, score, renorm, scale, masked)
+    check(seed, R, T, E, K, dtype, score, renorm, scale, masked)
+
+
+def test_absent_tokens():
+    say("case: gate batch sizes")
+    check(20, 3, 50, 64, 4, F, 0, True, 1.0, bs=np.array([50, 0, 17], np.int32))
+    check(21, 2, 9, 128, 8, B, 1, True, 1.0, bs=np.array([1, 8], np.int32))
+
+
+@pytest.mark.parametrize("K", [1, 4, 8, 12])
+def test_ties_go_to_the_lowest_id(K):
+    say("case: gate ties", K)
+    rng = np.random.default_rng(30 + K)
+    x = torch.from_numpy(rng.integers(-2, 3, (2, 100, 128)).astype(np.float32))
+    x[0, 0] = 0.0
+    x[0, 1] = torch.tensor([0.0, -0.0] * 64)
+    x[0, 2] = -1.5
+    ids, w, err = run_gate(x, K)
+    ids_o, _ = O.gate(x.double().numpy(), K)
+    assert np.array_equal(ids, ids_o) and err == 0
+    assert ids[0, 0].tolist() == list(range(K)) == ids[0, 1].tolist()
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+def test_special_logits(dtype):
+    """-infinity masks, NaN and +infinity mask and are flagged, the type's lowest value is an
+    ordinary logit (selected last), and so are values whose exponentials underflow."""
+    say("case: gate special logits", dtype)
+    inf, low = float("inf"), torch.finfo(dtype).min
+    E, K = 16, 4
+    x = torch.full((1, 8, E), -inf)
+    x[0, 1, 3], x[0, 1, 9] = low, 1.0                   # two left, one of them the lowest value
+    x[0, 2] = low                                        # all the lowest value: uniform
+    x[0, 3, :5] = torch.tensor([5.0, -200.0, -201.0, 4.0, -202.0])
+    x[0, 4] = torch.arange(E, dtype=torch.float32)
+    x = x.to(dtype)
+    for score in (0, 1):
+        for renorm in (True, False):
+            ids, w, err = run_gate(x, K, score=score, renorm=renorm)
+            ids_o, w_o = O.gate(x.double().numpy(), K, score=score, renorm=renorm)
+            assert err == 0
+            if score == 0:
+                assert np.array_equal(ids, ids_o)
+                assert (np.abs(w - w_o) <= 1e-6 * w_o + 1e-37).all()
+            assert (ids[0, 0] == -1).all() and (w[0, 0] == 0).all()
+            assert np.isfinite(w).all()
+            dw = torch.ones(1, 8, K, device=DEV)
+            d = host(U.gate_grad(dw, x.to(DEV), to_dev(ids), to_dev(w, torch.float32),
+                                 score=score, renorm=renorm).float())
+            assert np.isfinite(d).all() and (d[0, 0] == 0).all()
+            assert (d[0][~np.isfinite(x[0].float().numpy())] == 0).all()
+    y = x.clone()
+    y[0, 4, 15], y[0, 4, 14], y[0, 5, 2] = float("nan"), inf, inf
+    ids, w, err = run_gate(y, K)
+    assert err == U.ERR_LOGIT
+    assert ids[0, 4].tolist() == [13, 12, 11, 10] and (ids[0, 5] == -1).all()
+    assert np.isfinite(w).all()
+
+
+def test_bias_may_mask_experts():
+    say("case: gate bias masks")
+    x = torch.arange(12, dtype=torch.float32).view(1, 1, 12) / 4
+    bias = np.zeros(12, np.float32)
+    bias[[11, 10]] = -np.inf
+    ids, _, err = run_gate(x, 3, bias=bias, score=1)
+    assert ids[0, 0].tolist() == [9, 8, 7] and err == 0
+    bias[9] = np.nan
+    ids, _, err = run_gate(x, 3, bias=bias, score=1)
+    assert ids[0, 0].tolist() == [8, 7, 6] and err == U.ERR_LOGIT
+
+
+def test_gradient_skips_bad_ids_and_writes_every_element():
+    say("case: gate_grad ids out of range")
+    R, T, E, K = 1, 3, 40, 3
+    x = draw_logits(40, R, T, E, F)
+    ids, w, _ = run_gate(x, K)
+    bad = ids.copy()
+    bad[0, 1, 1], bad[0, 2, 0] = E, -7
+    for renorm, score in ((True, 0), (False, 0), (True, 1), (False, 1)):
+        err = err_word()
+        d = torch.full((R, T, E), float("nan"), device=DEV)
+        U.gate_grad(torch.ones(R, T, K, device=DEV), x.to(DEV), to_dev(bad),
+                    to_dev(w, torch.float32), score=score, renorm=renorm, dlogits=d, err=err)
+        assert int(host(err)[0]) == U.ERR_ID_RANGE
+        assert np.isfinite(host(d)).all()
+
+
+def test_unaligned_views_and_other_streams():
+    """A logits view that starts at an odd element, and calls on another stream."""
+    say("case: gate unaligned")
+    for dtype in (F, B):
+        flat = draw_logits(50, 1, 1, 1 + 6 * 128, dtype).view(-1).to(DEV)
+        x = flat[1:].view(1, 6, 128)
+        ids0, w0 = U.gate(x.clone(), 8)
+        ids1, w1 = U.gate(x, 8)
+        assert torch.equal(ids0, ids1) and torch.equal(w0, w1)
+        out = torch.zeros(1 + 6 * 128, dtype=dtype, device=DEV)
+        dw = torch.randn(1, 6, 8, device=DEV)
+        d0 = U.gate_grad(dw, x.clone(), ids0, w0, renorm=False)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        U.gate_grad(dw, x, ids0, w0, renorm=False, dlogits=out[1:], stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out[1:].view(1, 6, 128), d0) and float(out[0]) == 0
+
+
+def test_captured_graph_replays():
+    say("case: gate in a graph")
+    x = draw_logits(60, 2, 300, 128, F).to(DEV)
+    ids = torch.empty(2, 300, 8, dtype=torch.int32, device=DEV)
+    w = torch.empty(2, 300, 8, device=DEV)
+    dw = torch.randn(2, 300, 8, device=DEV)
+    dl = torch.empty_like(x)
+    U.gate(x, 8, topk_ids=ids, gate_w=w)
+    U.gate_grad(dw, x, ids, w, dlogits=dl)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        U.gate(x, 8, topk_ids=ids, gate_w=w)
+        U.gate_grad(dw, x, ids, w, dlogits=dl)
+    for seed in (61, 62, 63):
+        x.copy_(draw_logits(seed, 2, 300, 128, F).to(DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        i2, w2 = U.gate(x, 8)
+        assert torch.equal(ids, i2) and torch.equal(w, w2)
+        assert torch.equal(dl, U.gate_grad(dw, x, i2, w2))

@@ -1,0 +1,170 @@
+"""GPU parity of uep_permute_grad and uep_combine_grad against the oracle: dx and dout bit
+for bit; the weights' gradient against a 64-bit sum, to (H / 64 + 16) eps = 2^-24 of the
+sum of magnitudes (products of two bf16 are exact in fp32; a lane adds at most H / 64 + 7
+of them one after the other, and the lanes' sums and slices add a few more)."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import oracle as O                                       # noqa: E402
+from moe_expert_load_amd import uep as U                 # noqa: E402
+from tests.gpu_helpers import DEV, to_dev, host, say, err_word, random_routing  # noqa: E402
+from tests.test_gpu_combine import bits, oracle_dest_row  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24
+
+CASES = [
+    (0, 4, 512, 2, 8, 256, 0.0),          # tiny shape
+    (1, 3, 97, 3, 9, 8 * 300, 0.1),       # ragged slices
+    (2, 2, 40, 5, 10, 7168, 0.2),         # 14 KiB rows, empty slots
+    (3, 5, 33, 9, 15, 1032, 0.05),        # K = 9, odd row length
+    (4, 1, 64, 1, 1, 64, 0.3),            # one rank, one expert
+    (5, 1, 1, 8, 16, 4096, 0.0),          # one token
+    (6, 1, 3, 2, 4, 8, 0.0),              # the shortest rows
+    (7, 1, 7, 20, 24, 520, 0.1),          # many slots
+    (8, 2, 5, 4, 8, 16392, 0.3),          # rows longer than any slice
+    (9, 1, 2, 8, 8, 4096, 0.9),           # nearly everything empty
+]
+
+
+def make(seed, R, T, K, E, H, empty, extra=0):
+    rng = np.random.default_rng(seed)
+    ids = random_routing(rng, R, T, K, E, empty_frac=empty)
+    dr = oracle_dest_row(ids, E, 1, 2)
+    P = max(int((dr >= 0).sum()), 1) + extra
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    dy = torch.randn(R, T, H, generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.randn(P, H, generator=g, device=DEV).to(torch.bfloat16)
+    w = rng.random((R, T, K)).astype(np.float32) * 2 - 0.5
+    return dr, dy, out, w
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_permute_grad(case):
+    say("case: permute_grad", *case)
+    dr, dy, out, _ = make(*case)
+    dx = torch.full(dy.shape, 77, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+    U.permute_grad(out, to_dev(dr), dx)
+    assert np.array_equal(bits(dx), O.permute_grad(bits(out), dr))
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_combine_grad(case):
+    say("case: combine_grad", *case)
+    dr, dy, out, w = make(*case, extra=3)
+    P, H = out.shape
+    fill = torch.full((P, H), 77, dtype=torch.int16, device=DEV)
+    dout, dw = fill.clone().view(torch.bfloat16), torch.full(w.shape, 9.0, device=DEV)
+    err = err_word()
+    drow, wd = to_dev(dr), to_dev(w, torch.float32)
+    U.combine_grad(dy, out, drow, wd, dout, dw, err=err)
+    dout_o, dw_o, mag = O.combine_grad(bits(dy), bits(out), dr, w)
+    named = np.zeros(P, bool)
+    named[dr[dr >= 0]] = True
+    assert int(host(err)[0]) == 0
+    assert np.array_equal(bits(dout)[named], dout_o[named])
+    assert (bits(dout)[~named] == 77).all()                       # rows without a slot
+    assert (np.abs(host(dw) - dw_o) <= (H / 64 + 16) * EPS * mag).all()
+    assert (host(dw)[dr < 0] == 0).all()
+    # the same bits again, only dout without the weights' gradient, and in place
+    dw2, only, place = torch.empty_like(dw), fill.clone().view(torch.bfloat16), out.clone()
+    U.combine_grad(dy, out, drow, wd, dout, dw2)
+    assert torch.equal(dw, dw2)
+    U.combine_grad(dy, None, drow, wd, only)
+    assert np.array_equal(bits(only), bits(dout))
+    U.combine_grad(dy, place, drow, wd, place, dw2)
+    assert torch.equal(dw, dw2)
+    assert np.array_equal(bits(place)[named], dout_o[named])
+    assert np.array_equal(bits(place)[~named], bits(out)[~named])
+
+
+def test_rank_ranges_and_noops():
+    say("case: row gradients, rank ranges")
+    dr, dy, out, w = make(11, 4, 50, 4, 8, 512, 0.1)
+    drow, wd = to_dev(dr), to_dev(w, torch.float32)
+    fill = torch.full(dy.shape, 77, dtype=torch.int16, device=DEV)
+    dx = fill.clone().view(torch.bfloat16)
+    U.permute_grad(out, drow, dx, r_begin=1, r_end=3)
+    want = O.permute_grad(bits(out), dr)
+    assert np.array_equal(bits(dx)[1:3], want[1:3]) and (bits(dx)[[0, 3]] == 77).all()
+    dout = torch.full(out.shape, 77, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+    dw = torch.full(w.shape, 9.0, device=DEV)
+    U.combine_grad(dy, out, drow, wd, dout, dw, r_begin=2, r_end=3)
+    dout_o, dw_o, _ = O.combine_grad(bits(dy), bits(out), dr, w)
+    mine = dr[2][dr[2] >= 0]
+    assert np.array_equal(bits(dout)[mine], dout_o[mine])
+    rest = np.setdiff1d(np.arange(out.shape[0]), mine)
+    assert (bits(dout)[rest] == 77).all() and (host(dw)[[0, 1, 3]] == 9).all()
+    U.combine_grad(dy, out, drow, wd, dout, dw, r_begin=1, r_end=1)
+    assert (host(dw)[[0, 1, 3]] == 9).all()
+    none = to_dev(np.full(dr.shape, -1))
+    U.permute_grad(out, none, dx)
+    assert (bits(dx) == 0).all()
+    U.combine_grad(dy, out, none, wd, dout, dw)
+    assert (host(dw) == 0).all()
+
+
+def test_rows_outside_the_buffer_are_flagged():
+    say("case: row gradients, rows out of range")
+    dr, dy, out, w = make(12, 2, 30, 3, 6, 264, 0.0)
+    P = out.shape[0]
+    bad = dr.copy()
+    bad[0, 0, 0], bad[1, 5, 2], bad[1, 29, 1] = P, 2 ** 31 - 1, -9
+    ok = np.where((bad < -1) | (bad >= P), -1, bad)
+    e1, e2 = err_word(), err_word()
+    dx, dout = torch.empty_like(dy), torch.zeros_like(out)
+    U.permute_grad(out, to_dev(bad), dx, err=e1)
+    _, dw = U.combine_grad(dy, out, to_dev(bad), to_dev(w, torch.float32), dout, err=e2)
+    assert int(host(e1)[0]) == int(host(e2)[0]) == U.ERR_ROW_RANGE
+    assert np.array_equal(bits(dx), O.permute_grad(bits(out), ok))
+    dout_o, dw_o, mag = O.combine_grad(bits(dy), bits(out), ok, w)
+    assert np.array_equal(bits(dout), dout_o)
+    assert (np.abs(host(dw) - dw_o) <= (264 / 64 + 16) * EPS * mag).all()
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    say("case: row gradients, special values")
+    dr, dy, out, w = make(13, 1, 20, 2, 4, 64, 0.0)
+    dy[0, 3, 5], dy[0, 4, 0] = float("inf"), float("nan")
+    out[dr[0, 7, 1], 2] = float("nan")
+    dout = torch.empty_like(out)
+    _, dw = U.combine_grad(dy, out, to_dev(dr), to_dev(w, torch.float32), dout)
+    dout_o, _, _ = O.combine_grad(bits(dy), bits(out), dr, w)
+    a, b = host(dout.float()), O.bf16_bits_to_f32(dout_o)
+    assert np.array_equal(np.isnan(a), np.isnan(b))
+    assert np.array_equal(a[~np.isnan(a)], b[~np.isnan(b)])
+    hot = np.zeros((20, 2), bool)
+    hot[3], hot[4], hot[7, 1] = True, True, True
+    assert np.array_equal(~np.isfinite(host(dw)[0]), hot)
+
+
+def test_gradients_match_torchs_autograd():
+    """The whole chain x -> permute -> scale -> combine against torch in float64: the
+    library's dx and dgate_w are those of the same function, to the bf16 steps between (three
+    roundings of 2^-8 each, relative to sums of magnitudes)."""
+    say("case: row gradients against autograd")
+    dr, dy, _, w = make(14, 2, 60, 4, 8, 128, 0.1)
+    R, T, K = dr.shape
+    P = int((dr >= 0).sum())
+    x = torch.randn(R, T, 128, device=DEV).to(torch.bfloat16)
+    drow, wd = to_dev(dr), to_dev(w, torch.float32)
+    disp = torch.zeros(P, 128, dtype=torch.bfloat16, device=DEV)
+    U.permute(x, drow, disp)
+    dout = torch.empty_like(disp)
+    _, dw = U.combine_grad(dy, disp, drow, wd, dout)
+    dx = torch.empty_like(x)
+    U.permute_grad(dout, drow, dx)
+    xa = x.double().cpu().requires_grad_()
+    wa = torch.from_numpy(w).double().requires_grad_()
+    on = torch.from_numpy((dr >= 0).astype(np.float64))
+    y = ((wa * on).sum(-1, keepdim=True)) * xa              # every copy of a token is the token
+    (y * dy.double().cpu()).sum().backward()
+    mag = ((wa.abs() * on).sum(-1, keepdim=True) * dy.double().cpu().abs()).detach().numpy()
+    assert (np.abs(host(dx.double()) - xa.grad.numpy()) <= 3 * 2.0 ** -8 * mag + 1e-30).all()
+    m2 = (xa.detach().abs() * dy.double().cpu().abs()).sum(-1, keepdim=True).numpy()
+    assert (np.abs(host(dw) - wa.grad.numpy()) <= 18 * EPS * m2).all()
