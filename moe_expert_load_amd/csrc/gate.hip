@@ -1,9 +1,7 @@
 // Router gate and its gradient (uep.h: uep_gate, uep_gate_grad).
 //
-// Selection runs on 64-bit keys that order by (score, lowest id): an fp32 score widened
-// to double is exact and leaves 29 zero mantissa bits, which take the expert id, inverted
-// for positive scores (adding low bits to a positive double raises it, to a negative one
-// lowers it).  Keys are distinct, so one maximum names both the winner and its id.
+// The selection compares distinct keys that order by (rank, lowest id), so that one maximum
+// names both the winner and its id.
 #include "common.h"
 
 namespace uep {
@@ -11,6 +9,9 @@ namespace uep {
 constexpr int kGtThreads = 256;
 constexpr int kGtTokPerBlock = kGtThreads / kWave;
 constexpr int kGtMaxE = 4096;
+// Up to this many tokens a call is bound by its latency and takes 16 lanes per token (the
+// shortest chain); above, by its instructions and takes as few lanes as hold the experts.
+constexpr int64_t kGtFew = 4096;
 
 template <typename T>
 __device__ __forceinline__ float gt_load(const T* p, int64_t i);
@@ -32,25 +33,259 @@ __device__ __forceinline__ bool gt_bad(float x) {
 
 __device__ __forceinline__ float gt_sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-constexpr double kGtNone = -__builtin_inf();
-
-__device__ __forceinline__ double gt_key(float f, int e) {
-  const uint64_t u = (uint64_t)__double_as_longlong((double)(f + 0.0f));   // -0 counts as +0
-  return __longlong_as_double((long long)(u | ((int64_t)u < 0 ? (uint64_t)e
-                                                              : (uint64_t)(kGtMaxE - 1 - e))));
-}
-__device__ __forceinline__ int gt_key_id(double k) {
-  const uint64_t u = (uint64_t)__double_as_longlong(k);
-  const int low = (int)(u & (kGtMaxE - 1));
-  return (int64_t)u < 0 ? low : kGtMaxE - 1 - low;
+// The sigmoid as the selection uses it: exp2 and a refined reciprocal instead of the exact
+// division (5 instead of about 20 instructions for each of the E experts); within 4 units
+// of 2^-24 of the true value, like the exact one after its own roundings.  The exponent is
+// capped so that the refinement sees no infinity: scores below 2^-126 tie.
+__device__ __forceinline__ float gt_rank_sigmoid(float x) {
+  const float d = 1.0f + __builtin_amdgcn_exp2f(fminf(-1.44269504f * x, 126.0f));
+  const float r = __builtin_amdgcn_rcpf(d);
+  return fmaf(r, fmaf(-d, r, 1.0f), r);
 }
 
+// What one expert is ranked by: its logit or its score with the bias; eligible if finite.
+__device__ __forceinline__ float gt_rank(float x, int score, const float* bias, int e) {
+  return score ? gt_rank_sigmoid(x) + (bias ? bias[e] : 0.0f) : x;
+}
+
+// The fp32 bits in unsigned order (-0 as +0); 0 for an expert that is not eligible, which
+// no finite value maps to.
+__device__ __forceinline__ uint32_t gt_order(float f, bool able) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return able ? o : 0u;
+}
+__device__ __forceinline__ float gt_unorder(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+
+// Keys order by (rank, lowest id).  Key64: the 32 ordered bits and the inverted id as the
+// mantissa of a double in [1, 2), so that one v_max_f64 / v_min_f64 compares both (64-bit
+// integers have no such instruction: a compare and two selects).  Key32: bf16 logits
+// leave the lower half of the word for the id.
+struct Key64 {
+  typedef double type;
+  static __device__ __forceinline__ double make(uint32_t o, int inv_id) {
+    return __hiloint2double((int)__builtin_amdgcn_alignbit(0x3FFu, o, 12),
+                            (int)(o << 20 | (uint32_t)inv_id));
+  }
+  static __device__ __forceinline__ double hi(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
+  static __device__ __forceinline__ double lo(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t order(double k) {
+    return (uint32_t)__double2hiint(k) << 12 | (uint32_t)__double2loint(k) >> 20;
+  }
+  static __device__ __forceinline__ int inv_id(double k) { return __double2loint(k) & 0xFFFFF; }
+  template <int kDpp>
+  static __device__ __forceinline__ double moved(double k) {
+    return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(k), kDpp, 0xF, 0xF, true),
+                            __builtin_amdgcn_mov_dpp(__double2loint(k), kDpp, 0xF, 0xF, true));
+  }
+};
+struct Key32 {
+  typedef uint32_t type;
+  static __device__ __forceinline__ uint32_t make(uint32_t o, int inv_id) {
+    return (o & 0xFFFF0000u) | (uint32_t)inv_id;
+  }
+  static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min(a, b); }
+  // the cut lower half: zeros of a positive value, ones of a negative one
+  static __device__ __forceinline__ uint32_t order(uint32_t k) {
+    return k & 0x80000000u ? k & 0xFFFF0000u : (k & 0xFFFF0000u ? k | 0xFFFFu : 0u);
+  }
+  static __device__ __forceinline__ int inv_id(uint32_t k) { return (int)(k & 0xFFFFu); }
+  template <int kDpp>
+  static __device__ __forceinline__ uint32_t moved(uint32_t k) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)k, kDpp, 0xF, 0xF, true);
+  }
+};
+constexpr int kGtInv = 0xFFFF;                      // inverted id = kGtInv - id
+
+// ---------------------------------------------------------------------------------------
+// Few slots and experts: kL lanes per token, up to 32 experts per lane, a running list of
+// the kN >= K best.  Sorting networks on registers: every kN experts are sorted (Batcher's
+// odd-even mergesort), merged into the list (the larger of list[i] and sorted[kN - 1 - i]
+// are the kN best and bitonic; a bitonic merge sorts them), and the kL lanes' lists are
+// merged the same way with DPP moves.
+constexpr int kGtPer = 32;
+
+template <typename KY, int kN>
+__device__ __forceinline__ void gt_order_pair(typename KY::type (&a)[kN], int i, int j) {
+  const typename KY::type x = KY::hi(a[i], a[j]), y = KY::lo(a[i], a[j]);
+  a[i] = x;
+  a[j] = y;
+}
+template <typename KY, int kN>
+__device__ __forceinline__ void gt_sort(typename KY::type (&a)[kN]) {
+#pragma unroll
+  for (int p = 1; p < kN; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < kN; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < kN && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+            gt_order_pair<KY>(a, i + j, i + j + k);
+}
+template <typename KY, int kN>
+__device__ __forceinline__ void gt_merge(typename KY::type (&a)[kN], const typename KY::type (&b)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) a[i] = KY::hi(a[i], b[kN - 1 - i]);
+#pragma unroll
+  for (int s = kN / 2; s >= 1; s /= 2)
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (!(i & s)) gt_order_pair<KY>(a, i, i + s);
+}
+template <typename KY, int kDpp, int kN>
+__device__ __forceinline__ void gt_merge_lanes(typename KY::type (&a)[kN]) {
+  typename KY::type b[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) b[i] = KY::template moved<kDpp>(a[i]);
+  gt_merge<KY>(a, b);
+}
+
+// sum over the kL lanes of a token
+template <int kL>
+__device__ __forceinline__ float gt_lanes_sum(float v) {
+  auto add = [](float a, int b) { return a + __int_as_float(b); };
+  v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));   // xor 1
+  v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));   // xor 2
+  if (kL >= 8) v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));
+  if (kL >= 16) v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));
+  return v;
+}
+
+template <typename T, typename KY, int kL, int kN>
+__global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
+    const T* __restrict__ logits, const float* __restrict__ bias,
+    const int32_t* __restrict__ batch_size, int64_t n_tok, int tok_per_rank, int E, int K,
+    int score, int renorm, float scale, int vec, int32_t* __restrict__ topk_ids,
+    float* __restrict__ gate_w, int32_t* err) {
+  typedef typename KY::type key_t;
+  constexpr int kCe = 16 / sizeof(T);                 // experts of one 16-byte load
+  const int lane = threadIdx.x % kL;
+  const int64_t g = (int64_t)blockIdx.x * (kGtThreads / kL) + threadIdx.x / kL;
+  bool live = g < n_tok;
+  if (live && batch_size) live = (int)(g % tok_per_rank) < batch_size[g / tok_per_rank];
+  const T* row = logits + (live ? g : 0) * (int64_t)E;
+  float x[kGtPer];
+#pragma unroll
+  for (int c = 0; c < kGtPer / kCe; ++c) {
+    const int e0 = (c * kL + lane) * kCe;
+    if (c * kL * kCe >= E) {                          // uniform: no lane has such experts
+#pragma unroll
+      for (int j = 0; j < kCe; ++j) x[c * kCe + j] = -__builtin_inff();
+    } else if (vec) {                                 // rows of whole 16-byte vectors
+      const bool in = live && e0 < E;
+      const u32x4 w = in ? *reinterpret_cast<const u32x4*>(row + e0)
+                         : sizeof(T) == 4 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
+                                          : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+#pragma unroll
+      for (int j = 0; j < kCe; ++j)
+        x[c * kCe + j] = sizeof(T) == 4 ? __uint_as_float(w[j & 3])
+                         : j & 1        ? bf16_hi(w[j / 2 & 3]) : bf16_lo(w[j / 2 & 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kCe; ++j)
+        x[c * kCe + j] = live && e0 + j < E ? gt_load(row, e0 + j) : -__builtin_inff();
+    }
+  }
+  key_t best[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) best[i] = KY::make(0u, 0);
+  bool odd = false;                                   // something that is not finite
+#pragma unroll
+  for (int q = 0; q < kGtPer / kN; ++q) {
+    if (q * kN / kCe * kCe * kL >= E) break;          // uniform
+    key_t a[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int n = q * kN + i, e = (n / kCe * kL + lane) * kCe + n % kCe;
+      float f = x[n];
+      bool able = gt_finite(f);
+      if (score) {
+        f = gt_rank(f, score, bias, min(e, E - 1));
+        able &= gt_finite(f);
+      }
+      odd |= !able;
+      a[i] = KY::make(gt_order(f, able), kGtInv - e);
+    }
+    gt_sort<KY>(a);
+    if (q == 0) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) best[i] = a[i];
+    } else {
+      gt_merge<KY>(best, a);
+    }
+  }
+  if (ballot(odd)) {                                  // find out whether it was a mask
+    bool bad = false;
+#pragma unroll
+    for (int n = 0; n < kGtPer; ++n) {
+      const int e = (n / kCe * kL + lane) * kCe + n % kCe;
+      bad |= gt_bad(x[n]);
+      if (score && e < E && gt_finite(x[n])) bad |= gt_bad(gt_rank(x[n], score, bias, e));
+    }
+    if (ballot(bad) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_LOGIT);
+  }
+  gt_merge_lanes<KY, 0xB1>(best);                     // xor 1
+  gt_merge_lanes<KY, 0x4E>(best);                     // xor 2
+  if (kL >= 8) gt_merge_lanes<KY, 0x141>(best);       // the other half of 8 (row_half_mirror)
+  if (kL >= 16) gt_merge_lanes<KY, 0x140>(best);      // the other half of 16 (row_mirror)
+
+  constexpr int kSlots = kN > kL ? kN / kL : 1;       // a lane's slots, consecutive
+  const uint32_t top_o = KY::order(best[0]);
+  const float top = top_o ? gt_unorder(top_o) : 0.0f; // softmax: the largest logit
+  int id[kSlots];
+  float s[kSlots], mine = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    key_t k = best[i];
+#pragma unroll
+    for (int l = 1; l < kL && l * kSlots + i < kN; ++l)
+      if (lane == l) k = best[l * kSlots + i];
+    const uint32_t o = KY::order(k);
+    const bool on = o != 0u && lane * kSlots + i < K;
+    id[i] = on ? kGtInv - KY::inv_id(k) : -1;
+    s[i] = 0.0f;
+    if (on) s[i] = score ? gt_sigmoid(gt_load(row, id[i])) : expf(gt_unorder(o) - top);
+    mine += s[i];
+  }
+  float total = 1.0f;
+  if (renorm) {
+    total = gt_lanes_sum<kL>(mine);
+  } else if (!score) {
+    float z = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kGtPer; ++n)
+      z += gt_finite(x[n]) ? __builtin_amdgcn_exp2f(1.44269504f * (x[n] - top)) : 0.0f;
+    total = gt_lanes_sum<kL>(z);
+  }
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int k = lane * kSlots + i;
+    if (g < n_tok && k < K) {
+      topk_ids[g * K + k] = id[i];
+      gate_w[g * K + k] = s[i] > 0.0f ? scale * (s[i] / total) : 0.0f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Any size: one wave per token, kVpt experts per lane (expert j * 64 + lane); K rounds of a
+// wave maximum over the keys left.
 __device__ __forceinline__ double gt_wave_max(double v) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const double w = __shfl_xor(v, o, kWave);
-    v = w > v ? w : v;
-  }
+  for (int o = 32; o > 0; o >>= 1) v = Key64::hi(v, __shfl_xor(v, o, kWave));
   return v;
 }
 __device__ __forceinline__ float gt_wave_sum(float v) {
@@ -59,8 +294,6 @@ __device__ __forceinline__ float gt_wave_sum(float v) {
   return v;
 }
 
-// One wave per token, kVpt experts per lane (expert j * 64 + lane); K rounds of a wave
-// maximum over the keys left.
 template <typename T, int kVpt>
 __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
@@ -77,6 +310,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     }
     return;
   }
+  const double none = Key64::make(0u, 0);
   double key[kVpt];
   float val[kVpt];
   bool bad = false;
@@ -84,14 +318,14 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
   for (int j = 0; j < kVpt; ++j) {
     const int e = j * kWave + lane;
     const float x = e < E ? gt_load(logits, g * E + e) : -__builtin_inff();
-    bad |= gt_bad(x);
     val[j] = x;
-    key[j] = kGtNone;
-    if (gt_finite(x)) {
-      const float f = score ? gt_sigmoid(x) + (bias ? bias[e] : 0.0f) : x;
+    bad |= gt_bad(x);
+    float f = x;
+    if (score && gt_finite(x)) {
+      f = gt_rank(x, score, bias, e);
       bad |= gt_bad(f);
-      if (gt_finite(f)) key[j] = gt_key(f, e);
     }
+    key[j] = gt_finite(f) ? Key64::make(gt_order(f, true), kGtInv - e) : none;
   }
   if (ballot(bad) && lane == 0) set_err(err, UEP_ERR_LOGIT);
   int id_mine = -1;
@@ -99,17 +333,17 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
   for (int k = 0; k < K; ++k) {
     double m = key[0];
 #pragma unroll
-    for (int j = 1; j < kVpt; ++j) m = key[j] > m ? key[j] : m;
+    for (int j = 1; j < kVpt; ++j) m = Key64::hi(m, key[j]);
     m = gt_wave_max(m);
-    if (m == kGtNone) break;
+    if (m == none) break;
 #pragma unroll
-    for (int j = 0; j < kVpt; ++j) key[j] = key[j] == m ? kGtNone : key[j];
-    if (k == 0) top = (float)m;   // softmax: the largest logit, up to the id bits (a shift)
-    if (lane == k) id_mine = gt_key_id(m);
+    for (int j = 0; j < kVpt; ++j) key[j] = key[j] == m ? none : key[j];
+    if (k == 0) top = gt_unorder(Key64::order(m));    // softmax: the largest logit
+    if (lane == k) id_mine = kGtInv - Key64::inv_id(m);
   }
   const bool on = id_mine >= 0;
   const float l = on ? gt_load(logits, g * E + id_mine) : 0.0f;
-  float s = on ? (score ? gt_sigmoid(l) : expf(l - top)) : 0.0f;
+  const float s = on ? (score ? gt_sigmoid(l) : expf(l - top)) : 0.0f;
   float total = 1.0f;
   if (renorm) {
     total = gt_wave_sum(s);
@@ -188,6 +422,73 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
   }
 }
 
+struct GtCall {
+  const void* logits;
+  const float* bias;
+  const int32_t* batch_size;
+  int64_t n_tok;
+  int T, E, K, score, renorm;
+  float scale;
+  int32_t* topk_ids;
+  float* gate_w;
+  int32_t* err;
+  hipStream_t stream;
+};
+
+// workgroups for n_tok tokens, `per` each; a launch holds below 2^32 threads
+static bool gt_blocks(int64_t n_tok, int per, unsigned* blocks) {
+  const int64_t n = (n_tok + per - 1) / per;
+  *blocks = (unsigned)n;
+  return n < (1ll << 32) / kGtThreads;
+}
+
+template <typename T, typename KY, int kL, int kN>
+static uep_status gt_sorted(const GtCall& c) {
+  unsigned blocks;
+  if (!gt_blocks(c.n_tok, kGtThreads / kL, &blocks)) return UEP_EGEOM;
+  const int vec = (reinterpret_cast<uintptr_t>(c.logits) | (uintptr_t)c.E * sizeof(T)) % 16 == 0;
+  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kL, kN>), dim3(blocks), dim3(kGtThreads), 0,
+                     c.stream, static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok, c.T,
+                     c.E, c.K, c.score, c.renorm, c.scale, vec, c.topk_ids, c.gate_w, c.err);
+  UEP_CHECK_LAUNCH();
+  return UEP_OK;
+}
+
+template <typename T, int kVpt>
+static uep_status gt_general(const GtCall& c) {
+  unsigned blocks;
+  if (!gt_blocks(c.n_tok, kGtTokPerBlock, &blocks)) return UEP_EGEOM;
+  hipLaunchKernelGGL((gate_kernel<T, kVpt>), dim3(blocks), dim3(kGtThreads), 0, c.stream,
+                     static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok, c.T, c.E, c.K,
+                     c.score, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
+  UEP_CHECK_LAUNCH();
+  return UEP_OK;
+}
+
+template <typename T, typename KY, int kL>
+static uep_status gt_by_slots(const GtCall& c) {
+  return c.K <= 4 ? gt_sorted<T, KY, kL, 4>(c)
+         : c.K <= 8 ? gt_sorted<T, KY, kL, 8>(c) : gt_sorted<T, KY, kL, 16>(c);
+}
+
+template <typename T, typename KY>
+static uep_status gt_by_experts(const GtCall& c) {
+  if (c.E <= 4 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, 4>(c);
+  if (c.E <= 8 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, 8>(c);
+  return gt_by_slots<T, KY, 16>(c);
+}
+
+template <typename T>
+static uep_status gt_launch(const GtCall& c) {
+  if (c.K <= 16 && c.E <= 16 * kGtPer) {
+    if (sizeof(T) == 2 && c.score == UEP_GATE_SOFTMAX) return gt_by_experts<T, Key32>(c);
+    return gt_by_experts<T, Key64>(c);
+  }
+  if (c.E <= 256) return gt_general<T, 4>(c);
+  if (c.E <= 1024) return gt_general<T, 16>(c);
+  return gt_general<T, 64>(c);
+}
+
 static uep_status gt_check(const void* logits, int32_t dtype, int32_t R, int32_t T, int32_t E,
                            int32_t K, int32_t score, float scale) {
   if (R <= 0 || T < 0 || E <= 0 || K <= 0) return UEP_EINVAL;
@@ -214,27 +515,9 @@ extern "C" uep_status uep_gate(const void* logits, int32_t dtype, const float* b
   if (T == 0) return UEP_OK;
   if (!topk_ids || !gate_w) return UEP_EINVAL;
   const int64_t n_tok = (int64_t)R * T;
-  const unsigned blocks = (unsigned)((n_tok + kGtTokPerBlock - 1) / kGtTokPerBlock);
-  hipStream_t s = uep_stream(stream);
-#define UEP_GATE(VPT)                                                                         \
-  do {                                                                                        \
-    if (dtype == UEP_F32)                                                                     \
-      hipLaunchKernelGGL((gate_kernel<float, VPT>), dim3(blocks), dim3(kGtThreads), 0, s,      \
-                         static_cast<const float*>(logits), bias, batch_size, n_tok, T, E, K,  \
-                         score, renorm, scale, topk_ids, gate_w, err);                         \
-    else                                                                                      \
-      hipLaunchKernelGGL((gate_kernel<uint16_t, VPT>), dim3(blocks), dim3(kGtThreads), 0, s,   \
-                         static_cast<const uint16_t*>(logits), bias, batch_size, n_tok, T, E,  \
-                         K, score, renorm, scale, topk_ids, gate_w, err);                      \
-  } while (0)
-  if (E <= 128) UEP_GATE(2);
-  else if (E <= 256) UEP_GATE(4);
-  else if (E <= 512) UEP_GATE(8);
-  else if (E <= 1024) UEP_GATE(16);
-  else UEP_GATE(64);
-#undef UEP_GATE
-  UEP_CHECK_LAUNCH();
-  return UEP_OK;
+  const GtCall c{logits, bias, batch_size, n_tok, T, E, K, score, renorm, scale, topk_ids, gate_w,
+                 err, uep_stream(stream)};
+  return dtype == UEP_F32 ? gt_launch<float>(c) : gt_launch<uint16_t>(c);
 }
 
 extern "C" uep_status uep_gate_grad(const float* dgate_w, const void* logits, int32_t dtype,
@@ -247,7 +530,8 @@ extern "C" uep_status uep_gate_grad(const float* dgate_w, const void* logits, in
   if (T == 0) return UEP_OK;
   if (!dgate_w || !topk_ids || !gate_w || !dlogits) return UEP_EINVAL;
   const int64_t n_tok = (int64_t)R * T;
-  const unsigned blocks = (unsigned)((n_tok + kGtTokPerBlock - 1) / kGtTokPerBlock);
+  unsigned blocks;
+  if (!gt_blocks(n_tok, kGtTokPerBlock, &blocks)) return UEP_EGEOM;
   hipStream_t s = uep_stream(stream);
   if (dtype == UEP_F32)
     hipLaunchKernelGGL(gate_grad_kernel<float>, dim3(blocks), dim3(kGtThreads), 0, s, dgate_w,
