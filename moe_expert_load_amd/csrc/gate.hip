@@ -43,11 +43,6 @@ __device__ __forceinline__ float gt_rank_sigmoid(float x) {
   return fmaf(r, fmaf(-d, r, 1.0f), r);
 }
 
-// What one expert is ranked by: its logit or its score with the bias; eligible if finite.
-__device__ __forceinline__ float gt_rank(float x, int score, const float* bias, int e) {
-  return score ? gt_rank_sigmoid(x) + (bias ? bias[e] : 0.0f) : x;
-}
-
 // The fp32 bits in unsigned order (-0 as +0); 0 for an expert that is not eligible, which
 // no finite value maps to.
 __device__ __forceinline__ uint32_t gt_order(float f, bool able) {
@@ -164,56 +159,75 @@ __device__ __forceinline__ float gt_lanes_sum(float v) {
   return v;
 }
 
-template <typename T, typename KY, int kL, int kN>
+// kCe consecutive values from p[e0], `fill` from p[E] on; vec: all or none are there, aligned.
+template <int kCe, typename T>
+__device__ __forceinline__ void gt_chunk(const T* p, int e0, int E, bool vec, float fill,
+                                         float (&v)[kCe]) {
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < kCe; ++j) v[j] = fill;
+    if (e0 < E) {
+      constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+      for (int h = 0; h < kCe / kPer; ++h) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p + e0 + h * kPer);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          v[h * kPer + j] = sizeof(T) == 4 ? __uint_as_float(w[j & 3])
+                            : j & 1        ? bf16_hi(w[j / 2 & 3]) : bf16_lo(w[j / 2 & 3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kCe; ++j) v[j] = e0 + j < E ? gt_load(p, e0 + j) : fill;
+  }
+}
+
+template <typename T, typename KY, bool kSigmoid, int kL, int kN>
 __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
     const int32_t* __restrict__ batch_size, int64_t n_tok, int tok_per_rank, int E, int K,
-    int score, int renorm, float scale, int vec, int32_t* __restrict__ topk_ids,
+    int renorm, float scale, int vec, int vec_bias, int32_t* __restrict__ topk_ids,
     float* __restrict__ gate_w, int32_t* err) {
   typedef typename KY::type key_t;
   constexpr int kCe = 16 / sizeof(T);                 // experts of one 16-byte load
+  constexpr int kChunks = kGtPer / kCe;
   const int lane = threadIdx.x % kL;
   const int64_t g = (int64_t)blockIdx.x * (kGtThreads / kL) + threadIdx.x / kL;
   bool live = g < n_tok;
   if (live && batch_size) live = (int)(g % tok_per_rank) < batch_size[g / tok_per_rank];
   const T* row = logits + (live ? g : 0) * (int64_t)E;
-  float x[kGtPer];
+  const int e_end = live ? E : 0;
+  float x[kChunks][kCe];
 #pragma unroll
-  for (int c = 0; c < kGtPer / kCe; ++c) {
-    const int e0 = (c * kL + lane) * kCe;
-    if (c * kL * kCe >= E) {                          // uniform: no lane has such experts
+  for (int c = 0; c < kChunks; ++c) {
 #pragma unroll
-      for (int j = 0; j < kCe; ++j) x[c * kCe + j] = -__builtin_inff();
-    } else if (vec) {                                 // rows of whole 16-byte vectors
-      const bool in = live && e0 < E;
-      const u32x4 w = in ? *reinterpret_cast<const u32x4*>(row + e0)
-                         : sizeof(T) == 4 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
-                                          : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+    for (int j = 0; j < kCe; ++j) x[c][j] = -__builtin_inff();
+    if (c * kL * kCe < E)                             // uniform: some lane has such experts
+      gt_chunk<kCe>(row, (c * kL + lane) * kCe, e_end, vec, -__builtin_inff(), x[c]);
+  }
+  float y[kChunks][kCe];                              // what the selection ranks by
 #pragma unroll
-      for (int j = 0; j < kCe; ++j)
-        x[c * kCe + j] = sizeof(T) == 4 ? __uint_as_float(w[j & 3])
-                         : j & 1        ? bf16_hi(w[j / 2 & 3]) : bf16_lo(w[j / 2 & 3]);
-    } else {
+  for (int c = 0; c < kChunks; ++c) {
+    if (kSigmoid && bias && c * kL * kCe < E)
+      gt_chunk<kCe>(bias, (c * kL + lane) * kCe, E, vec_bias, 0.0f, y[c]);
+    else
 #pragma unroll
-      for (int j = 0; j < kCe; ++j)
-        x[c * kCe + j] = live && e0 + j < E ? gt_load(row, e0 + j) : -__builtin_inff();
-    }
+      for (int j = 0; j < kCe; ++j) y[c][j] = 0.0f;
   }
   key_t best[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) best[i] = KY::make(0u, 0);
   bool odd = false;                                   // something that is not finite
 #pragma unroll
   for (int q = 0; q < kGtPer / kN; ++q) {
-    if (q * kN / kCe * kCe * kL >= E) break;          // uniform
+    if (q > 0 && q * kN / kCe * kCe * kL >= E) break; // uniform
     key_t a[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int n = q * kN + i, e = (n / kCe * kL + lane) * kCe + n % kCe;
-      float f = x[n];
+      float f = x[n / kCe][n % kCe];
       bool able = gt_finite(f);
-      if (score) {
-        f = gt_rank(f, score, bias, min(e, E - 1));
+      if (kSigmoid) {
+        f = gt_rank_sigmoid(f) + y[n / kCe][n % kCe];
         able &= gt_finite(f);
       }
       odd |= !able;
@@ -230,11 +244,9 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
   if (ballot(odd)) {                                  // find out whether it was a mask
     bool bad = false;
 #pragma unroll
-    for (int n = 0; n < kGtPer; ++n) {
-      const int e = (n / kCe * kL + lane) * kCe + n % kCe;
-      bad |= gt_bad(x[n]);
-      if (score && e < E && gt_finite(x[n])) bad |= gt_bad(gt_rank(x[n], score, bias, e));
-    }
+    for (int n = 0; n < kGtPer; ++n) bad |= gt_bad(x[n / kCe][n % kCe]);
+    if (kSigmoid && bias)                             // a score plus a finite bias is finite
+      for (int e = threadIdx.x % kWave; e < E; e += kWave) bad |= gt_bad(bias[e]);
     if (ballot(bad) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_LOGIT);
   }
   gt_merge_lanes<KY, 0xB1>(best);                     // xor 1
@@ -257,17 +269,19 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const bool on = o != 0u && lane * kSlots + i < K;
     id[i] = on ? kGtInv - KY::inv_id(k) : -1;
     s[i] = 0.0f;
-    if (on) s[i] = score ? gt_sigmoid(gt_load(row, id[i])) : expf(gt_unorder(o) - top);
+    if (on) s[i] = kSigmoid ? gt_sigmoid(gt_load(row, id[i])) : expf(gt_unorder(o) - top);
     mine += s[i];
   }
   float total = 1.0f;
   if (renorm) {
     total = gt_lanes_sum<kL>(mine);
-  } else if (!score) {
+  } else if (!kSigmoid) {
     float z = 0.0f;
 #pragma unroll
-    for (int n = 0; n < kGtPer; ++n)
-      z += gt_finite(x[n]) ? __builtin_amdgcn_exp2f(1.44269504f * (x[n] - top)) : 0.0f;
+    for (int n = 0; n < kGtPer; ++n) {
+      const float f = x[n / kCe][n % kCe];
+      z += gt_finite(f) ? __builtin_amdgcn_exp2f(1.44269504f * (f - top)) : 0.0f;
+    }
     total = gt_lanes_sum<kL>(z);
   }
 #pragma unroll
@@ -322,7 +336,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     bad |= gt_bad(x);
     float f = x;
     if (score && gt_finite(x)) {
-      f = gt_rank(x, score, bias, e);
+      f = gt_rank_sigmoid(x) + (bias ? bias[e] : 0.0f);
       bad |= gt_bad(f);
     }
     key[j] = gt_finite(f) ? Key64::make(gt_order(f, true), kGtInv - e) : none;
@@ -442,14 +456,16 @@ static bool gt_blocks(int64_t n_tok, int per, unsigned* blocks) {
   return n < (1ll << 32) / kGtThreads;
 }
 
-template <typename T, typename KY, int kL, int kN>
+template <typename T, typename KY, bool kSigmoid, int kL, int kN>
 static uep_status gt_sorted(const GtCall& c) {
   unsigned blocks;
   if (!gt_blocks(c.n_tok, kGtThreads / kL, &blocks)) return UEP_EGEOM;
   const int vec = (reinterpret_cast<uintptr_t>(c.logits) | (uintptr_t)c.E * sizeof(T)) % 16 == 0;
-  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kL, kN>), dim3(blocks), dim3(kGtThreads), 0,
-                     c.stream, static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok, c.T,
-                     c.E, c.K, c.score, c.renorm, c.scale, vec, c.topk_ids, c.gate_w, c.err);
+  const int vec_bias = (reinterpret_cast<uintptr_t>(c.bias) | (uintptr_t)c.E * 4) % 16 == 0 &&
+                       c.E % (16 / (int)sizeof(T)) == 0;
+  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kSigmoid, kL, kN>), dim3(blocks), dim3(kGtThreads),
+                     0, c.stream, static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok,
+                     c.T, c.E, c.K, c.renorm, c.scale, vec, vec_bias, c.topk_ids, c.gate_w, c.err);
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }
@@ -465,24 +481,26 @@ static uep_status gt_general(const GtCall& c) {
   return UEP_OK;
 }
 
-template <typename T, typename KY, int kL>
+template <typename T, typename KY, bool kSigmoid, int kL>
 static uep_status gt_by_slots(const GtCall& c) {
-  return c.K <= 4 ? gt_sorted<T, KY, kL, 4>(c)
-         : c.K <= 8 ? gt_sorted<T, KY, kL, 8>(c) : gt_sorted<T, KY, kL, 16>(c);
+  return c.K <= 4   ? gt_sorted<T, KY, kSigmoid, kL, 4>(c)
+         : c.K <= 8 ? gt_sorted<T, KY, kSigmoid, kL, 8>(c)
+                    : gt_sorted<T, KY, kSigmoid, kL, 16>(c);
 }
 
-template <typename T, typename KY>
+template <typename T, typename KY, bool kSigmoid>
 static uep_status gt_by_experts(const GtCall& c) {
-  if (c.E <= 4 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, 4>(c);
-  if (c.E <= 8 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, 8>(c);
-  return gt_by_slots<T, KY, 16>(c);
+  if (c.E <= 4 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, kSigmoid, 4>(c);
+  if (c.E <= 8 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, kSigmoid, 8>(c);
+  return gt_by_slots<T, KY, kSigmoid, 16>(c);
 }
 
 template <typename T>
 static uep_status gt_launch(const GtCall& c) {
   if (c.K <= 16 && c.E <= 16 * kGtPer) {
-    if (sizeof(T) == 2 && c.score == UEP_GATE_SOFTMAX) return gt_by_experts<T, Key32>(c);
-    return gt_by_experts<T, Key64>(c);
+    if (c.score == UEP_GATE_SIGMOID) return gt_by_experts<T, Key64, true>(c);
+    if (sizeof(T) == 2) return gt_by_experts<T, Key32, false>(c);
+    return gt_by_experts<T, Key64, false>(c);
   }
   if (c.E <= 256) return gt_general<T, 4>(c);
   if (c.E <= 1024) return gt_general<T, 16>(c);
