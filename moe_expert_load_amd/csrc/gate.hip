@@ -2,6 +2,8 @@
 //
 // The selection compares distinct keys that order by (rank, lowest id), so that one maximum
 // names both the winner and its id.
+#include <algorithm>
+
 #include "common.h"
 
 namespace uep {
@@ -374,65 +376,150 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
 }
 
 template <typename T>
-__device__ __forceinline__ void gt_store(T* p, int64_t i, float v);
-template <>
-__device__ __forceinline__ void gt_store<float>(float* p, int64_t i, float v) { p[i] = v; }
-template <>
-__device__ __forceinline__ void gt_store<uint16_t>(uint16_t* p, int64_t i, float v) {
-  p[i] = (uint16_t)f32_to_bf16(v);
+__device__ __forceinline__ void gt_store(T* p, int64_t i, float v) {
+  if constexpr (sizeof(T) == 4) p[i] = v;
+  else p[i] = (T)f32_to_bf16(v);
 }
 
-// One wave per token: lane k holds slot k, then the wave writes the row.
-template <typename T>
+// ---------------------------------------------------------------------------------------
+// Gradient.  A wave takes 64 / kp tokens, kp the power of two from K up: a lane per slot for
+// the coefficients, then the tokens' rows, which are one contiguous stretch of dlogits, in
+// windows of kGtWin elements.  The slots' values are scattered into a window in LDS that is
+// zero otherwise, the window goes out in 16-byte stores that need no row to be aligned, and
+// the slots put their zeros back.  Bound by those stores.
+//
+// Weights that are not renormalised make the softmax's gradient dense.  Its scores need no
+// pass over the row: s_e = u_r exp(l_e - l_r) for any selected slot r, and the slot of the
+// largest weight is taken.  (A row whose largest weight is tiny, possible only where a
+// caller has dropped slots, sums its exponentials.)
+constexpr int kGtWin = 1024;
+constexpr float kGtTiny = 1e-20f;
+constexpr int kGtGradBlocks = 256 * 8;    // every CU's fill of them; they step through the tokens
+
+template <typename T, bool kDense>
 __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
     const float* __restrict__ dgate_w, const T* __restrict__ logits,
     const int32_t* __restrict__ topk_ids, const float* __restrict__ gate_w, int64_t n_tok, int E,
-    int K, int score, int renorm, float scale, T* __restrict__ dlogits, int32_t* err) {
-  const int lane = threadIdx.x % kWave;
-  const int64_t g = (int64_t)blockIdx.x * kGtTokPerBlock + threadIdx.x / kWave;
-  if (g >= n_tok) return;
-  int id = lane < K ? topk_ids[g * K + lane] : -1;
-  const bool bad = id < -1 || id >= E;
-  if (ballot(bad) && lane == 0) set_err(err, UEP_ERR_ID_RANGE);
-  if (bad) id = -1;
-  const float gk = id >= 0 ? scale * dgate_w[g * K + lane] : 0.0f;
-  const float u = id >= 0 ? gate_w[g * K + lane] / scale : 0.0f;
-  const float dot = gt_wave_sum(u * gk);
-  float d;
-  if (score)
-    d = renorm ? (id >= 0 ? u * (1.0f - gt_sigmoid(gt_load(logits, g * E + id))) * (gk - dot) : 0.0f)
-               : u * (1.0f - u) * gk;
-  else
-    d = renorm ? u * (gk - dot) : gk;
-  const bool dense = !score && !renorm;
-  float m = -__builtin_inff(), z = 0.0f;
-  if (dense && ballot(id >= 0)) {
-    for (int e = lane; e < E; e += kWave) {
-      const float x = gt_load(logits, g * E + e);
-      if (gt_finite(x)) m = fmaxf(m, x);
-    }
+    uint32_t e_magic, int K, int lg_kp, int score, int renorm, float scale, int vec,
+    T* __restrict__ dlogits, int32_t* err) {
+  constexpr int kCe = 16 / sizeof(T);
+  __shared__ __attribute__((aligned(16))) float win_all[kGtThreads / kWave][kGtWin];
+  __shared__ __attribute__((aligned(16))) f32x4 par_all[kDense ? kGtThreads / kWave : 1][kWave];
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  float* win = win_all[wave];
+  f32x4* par = par_all[kDense ? wave : 0];
+  for (int i = lane * 4; i < kGtWin; i += kWave * 4)
+    *reinterpret_cast<f32x4*>(win + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int kp = 1 << lg_kp, tpw = kWave >> lg_kp;
+  const int tok = lane >> lg_kp, k = lane & (kp - 1);
+  const int64_t n_grp = (n_tok + tpw - 1) / tpw;
+  for (int64_t grp = (int64_t)blockIdx.x * kGtTokPerBlock + wave; grp < n_grp;
+       grp += (int64_t)gridDim.x * kGtTokPerBlock) {
+    const int64_t g0 = grp * tpw, g = g0 + tok;
+    const bool there = k < K && g < n_tok;
+    int id = there ? topk_ids[g * K + k] : -1;
+    const bool bad = id < -1 || id >= E;
+    if (ballot(bad) && lane == 0) set_err(err, UEP_ERR_ID_RANGE);
+    if (bad) id = -1;
+    const bool on = id >= 0;
+    const float gk = on ? scale * dgate_w[g * K + k] : 0.0f;
+    const float u = on ? gate_w[g * K + k] / scale : 0.0f;
+    const float l = on && (kDense || (score && renorm)) ? gt_load(logits, g * E + id) : 0.0f;
+    float dot = u * gk;
+    for (int o = kp / 2; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
+    float d;
+    if (kDense) {
+      d = gk;
+      float ur = on ? u : -1.0f, lr = on ? l : __builtin_inff();   // no slot: every score 0
+      for (int o = kp / 2; o > 0; o >>= 1) {
+        const float u2 = __shfl_xor(ur, o, kWave), l2 = __shfl_xor(lr, o, kWave);
+        if (u2 > ur || (u2 == ur && l2 > lr)) { ur = u2; lr = l2; }
+      }
+      uint64_t tiny = ballot(k == 0 && ur >= 0.0f && ur < kGtTiny);
+      while (tiny) {
+        const int at = __ffsll((unsigned long long)tiny) - 1;
+        tiny &= tiny - 1;
+        const int64_t gr = g0 + (at >> lg_kp);
+        float m = -__builtin_inff(), z = 0.0f;
+        for (int e = lane; e < E; e += kWave) {
+          const float x = gt_load(logits, gr * E + e);
+          if (gt_finite(x)) m = fmaxf(m, x);
+        }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
-    for (int e = lane; e < E; e += kWave) {
-      const float x = gt_load(logits, g * E + e);
-      if (gt_finite(x)) z += expf(x - m);
+        for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+        for (int e = lane; e < E; e += kWave) {
+          const float x = gt_load(logits, gr * E + e);
+          if (gt_finite(x)) z += expf(x - m);
+        }
+        z = gt_wave_sum(z);
+        if (tok == at >> lg_kp) {
+          ur = 1.0f / z;
+          lr = m;
+        }
+      }
+      if (k == 0) par[tok] = f32x4{lr, fmaxf(ur, 0.0f), dot, 0.0f};
+    } else if (score) {
+      d = renorm ? u * (1.0f - gt_sigmoid(l)) * (gk - dot) : u * (1.0f - u) * gk;
+    } else {
+      d = u * (gk - dot);
     }
-    z = gt_wave_sum(z);
-  }
-  for (int e0 = 0; e0 < E; e0 += kWave) {
-    const int e = e0 + lane;
-    float v = 0.0f;
-    for (int k = 0; k < K; ++k) {
-      const int idk = readlane(id, k);
-      const float dk = __int_as_float(readlane(__float_as_int(d), k));
-      v = idk == e ? dk : v;
+    const int total = (int)min((int64_t)tpw, n_tok - g0) * E;
+    const int unit = vec ? kCe : 1;
+    // the window starts `lead` elements before the stretch, on a 16-byte boundary of dlogits
+    const int lead = vec ? (int)((g0 * E) % kCe) : 0;
+    const int pos = tok * E + id + lead;
+    T* dst = dlogits + g0 * E - lead;
+    const T* src = logits + g0 * E - lead;            // not read at `lead` elements
+    for (int o = 0; o < total + lead; o += kGtWin) {
+      const bool mine = on && pos >= o && pos < o + kGtWin;
+      if (mine) win[pos - o] = d;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int end = min(kGtWin, total + lead - o);
+      for (int i = lane * unit; i < end; i += kWave * unit) {
+        const int at = o + i;                         // element of the stretch, plus lead
+        float v[kCe];
+        if (vec) {
+#pragma unroll
+          for (int j = 0; j < kCe; j += 4)
+            *reinterpret_cast<f32x4*>(v + j) = *reinterpret_cast<const f32x4*>(win + i + j);
+        } else {
+          v[0] = win[i];
+        }
+        if constexpr (kDense) {                       // vec: rows of whole units, lead 0
+          const int row = E == 1 ? at : (int)__umulhi((uint32_t)at, e_magic);
+          const f32x4 q = par[row];
+          float x[kCe];
+          if (vec) {
+            gt_chunk<kCe>(src, at, INT32_MAX, true, 0.0f, x);
+          } else {
+            x[0] = gt_load(src, at);
+          }
+#pragma unroll
+          for (int j = 0; j < kCe; ++j) {
+            if (!vec && j > 0) break;
+            const float s = q[1] * __builtin_amdgcn_exp2f(1.44269504f * (x[j] - q[0]));
+            v[j] = gt_finite(x[j]) ? s * (v[j] - q[2]) : 0.0f;
+          }
+        }
+        if (vec && at >= lead && at + kCe <= total + lead) {
+          u32x4 w;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = sizeof(T) == 4 ? __float_as_uint(v[j])
+                                  : f32_to_bf16(v[2 * j & (kCe - 1)]) |
+                                        (f32_to_bf16(v[(2 * j + 1) & (kCe - 1)]) << 16);
+          *reinterpret_cast<u32x4*>(dst + at) = w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCe; ++j)               // single elements, and a stretch's ends
+            if (j < unit && at + j >= lead && at + j < total + lead) gt_store(dst, at + j, v[j]);
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (mine) win[pos - o] = 0.0f;
     }
-    if (e >= E) continue;
-    if (dense && z > 0.0f) {
-      const float x = gt_load(logits, g * E + e);
-      v = gt_finite(x) ? expf(x - m) / z * (v - dot) : 0.0f;
-    }
-    gt_store(dlogits, g * E + e, v);
   }
 }
 
@@ -548,17 +635,30 @@ extern "C" uep_status uep_gate_grad(const float* dgate_w, const void* logits, in
   if (T == 0) return UEP_OK;
   if (!dgate_w || !topk_ids || !gate_w || !dlogits) return UEP_EINVAL;
   const int64_t n_tok = (int64_t)R * T;
-  unsigned blocks;
-  if (!gt_blocks(n_tok, kGtTokPerBlock, &blocks)) return UEP_EGEOM;
+  int lg_kp = 0;
+  while ((1 << lg_kp) < K) ++lg_kp;
+  const int64_t n_grp = (n_tok + (kWave >> lg_kp) - 1) / (kWave >> lg_kp);
+  const unsigned blocks = (unsigned)std::min<int64_t>(
+      (n_grp + kGtTokPerBlock - 1) / kGtTokPerBlock, kGtGradBlocks);
+  const uint32_t e_magic = (uint32_t)(((1ull << 32) + E - 1) / E);
+  const bool dense = score == UEP_GATE_SOFTMAX && !renorm;
+  const uintptr_t size = dtype == UEP_F32 ? 4 : 2;
+  // dense rows are read in the units that are written, so they hold whole ones
+  const int vec = reinterpret_cast<uintptr_t>(dlogits) % 16 == 0 &&
+                  (!dense || (reinterpret_cast<uintptr_t>(logits) % 16 == 0 && E * size % 16 == 0));
   hipStream_t s = uep_stream(stream);
-  if (dtype == UEP_F32)
-    hipLaunchKernelGGL(gate_grad_kernel<float>, dim3(blocks), dim3(kGtThreads), 0, s, dgate_w,
-                       static_cast<const float*>(logits), topk_ids, gate_w, n_tok, E, K, score,
-                       renorm, scale, static_cast<float*>(dlogits), err);
-  else
-    hipLaunchKernelGGL(gate_grad_kernel<uint16_t>, dim3(blocks), dim3(kGtThreads), 0, s, dgate_w,
-                       static_cast<const uint16_t*>(logits), topk_ids, gate_w, n_tok, E, K, score,
-                       renorm, scale, static_cast<uint16_t*>(dlogits), err);
+#define UEP_GATE_GRAD(T, DENSE)                                                                  \
+  hipLaunchKernelGGL((gate_grad_kernel<T, DENSE>), dim3(blocks), dim3(kGtThreads), 0, s, dgate_w, \
+                     static_cast<const T*>(logits), topk_ids, gate_w, n_tok, E, e_magic, K, lg_kp, \
+                     score, renorm, scale, vec, static_cast<T*>(dlogits), err)
+  if (dtype == UEP_F32) {
+    if (dense) UEP_GATE_GRAD(float, true);
+    else UEP_GATE_GRAD(float, false);
+  } else {
+    if (dense) UEP_GATE_GRAD(uint16_t, true);
+    else UEP_GATE_GRAD(uint16_t, false);
+  }
+#undef UEP_GATE_GRAD
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }
