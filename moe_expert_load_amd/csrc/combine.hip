@@ -16,6 +16,8 @@
 //
 // uep_permute_grad is the same gather without weights (every copy of a token hands its
 // gradient back): the kernel's unweighted form, dx[g] = bf16( sum_k dout[dest_row[g][k]] ).
+#include <algorithm>
+
 #include "common.h"
 
 namespace uep {
@@ -24,6 +26,9 @@ constexpr int kCbThreads = 256;
 constexpr int kCbTokPerBlock = kCbThreads / kWave;
 constexpr int kCbVec = 4;     // 16-byte vectors per lane per slice (8 bf16 each)
 constexpr int kCbGroup = 4;   // rows loaded together
+// Up to this many tokens, which leave SIMDs without a wave, a token's slices go to up to 16
+// waves instead of one after the other to one.
+constexpr int64_t kCbFew = 512;
 
 template <bool kWeighted>
 __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __restrict__ y_disp,
@@ -32,16 +37,18 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
                                                              u32x4* __restrict__ y,
                                                              int64_t out_rows, int64_t g0,
                                                              int64_t g1, int K, int nvec,
-                                                             int32_t* err) {
+                                                             int parts, int32_t* err) {
 #pragma clang fp contract(off)
   const int lane = threadIdx.x % kWave;
   const int64_t b = xcd_block(blockIdx.x, gridDim.x);
   // the wave's token, uniform (readfirstlane), so the row spans below live in SGPRs
-  const int64_t g = g0 + b * kCbTokPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t wv = b * kCbTokPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t g = g0 + (parts == 1 ? wv : (int)wv / parts);
+  const int part = parts == 1 ? 0 : (int)wv % parts;
   if (g >= g1) return;
   const int d_mine = checked_row(lane < K ? dest_row[g * K + lane] : -1, out_rows, err);
   const int w_mine = kWeighted && lane < K ? __float_as_int(gate_w[g * K + lane]) : 0;
-  for (int v0 = 0; v0 < nvec; v0 += kCbVec * kWave) {
+  for (int v0 = part * kCbVec * kWave; v0 < nvec; v0 += parts * kCbVec * kWave) {
     float acc[kCbVec * 8];
 #pragma unroll
     for (int i = 0; i < kCbVec * 8; ++i) acc[i] = 0.0f;
@@ -82,7 +89,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
       u32x4 o;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        o[c] = f32_to_bf16(acc[u * 8 + 2 * c]) | (f32_to_bf16(acc[u * 8 + 2 * c + 1]) << 16);
+        o[c] = pack_bf16(acc[u * 8 + 2 * c], acc[u * 8 + 2 * c + 1]);
       stream_store(o, dst, (v0 + u * kWave + lane) * 16);
     }
   }
@@ -102,11 +109,14 @@ static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_
   if (!rows || !dest_row || (weighted && !gate_w) || !y) return UEP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(y)) % 16 != 0)
     return UEP_EGEOM;
-  const int64_t blocks = (g1 - g0 + kCbTokPerBlock - 1) / kCbTokPerBlock;
+  const int slices = (H / 8 + kCbVec * kWave - 1) / (kCbVec * kWave);
+  const int parts = g1 - g0 <= kCbFew ? std::min(slices, 16) : 1;
+  const int64_t blocks = ((g1 - g0) * parts + kCbTokPerBlock - 1) / kCbTokPerBlock;
   auto kernel = weighted ? combine_kernel<true> : combine_kernel<false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kCbThreads), 0, uep_stream(stream),
                      reinterpret_cast<const u32x4*>(rows), dest_row, gate_w,
-                     reinterpret_cast<u32x4*>(y), out_rows, g0, g1, K, H / 8, err);
+                     reinterpret_cast<u32x4*>(y), out_rows, g0, g1, K, H / 8, parts,
+                     err);
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }

@@ -162,6 +162,27 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// Two of them in one word, by the instruction that does the same to every input (compared
+// over all 2^32).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// Wave-wide sum in a fixed order, uniform result: DPP butterflies inside each row of 16
+// lanes (xor 1, xor 2, then the mirrored halves and rows, whose lanes are all alike by
+// then), the four rows by readlane.  Every lane of the wave must be active.
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));
+  v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));
+  const int b = __float_as_int(v);
+  return (__int_as_float(readlane(b, 0)) + __int_as_float(readlane(b, 16))) +
+         (__int_as_float(readlane(b, 32)) + __int_as_float(readlane(b, 48)));
+}
+
 __device__ __forceinline__ void set_err(int32_t* err, int bits) {
   if (err) atomicOr(err, bits);
 }
