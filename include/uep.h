@@ -593,7 +593,8 @@ uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, int64_t out
  *   step   [1] int32  in   t >= 1, device memory
  *   sched  [2] fp32   in   {learning rate, factor on every gradient}, device memory, so a
  *                          captured graph can be replayed with new values
- *   0 <= beta1, beta2 < 1, eps > 0 (double: 1 - beta is formed before it is rounded)
+ *   0 <= beta1, beta2 < 1, 2^-126 <= eps <= 2^126 (double: 1 - beta is formed before it is
+ *   rounded)
  *   err               out  optional; UEP_ERR_GRAD, UEP_ERR_PLAN (then nothing else is written)
  * uep_adamw_decode: the values that 8-bit states stand for (checkpoints), n elements from
  *   the start of a tensor or of several whose starts are multiples of 256 apart;

@@ -15,6 +15,7 @@ constexpr int kAwThreads = 256;
 constexpr int kAwWaves = kAwThreads / kWave;
 constexpr int kAwChunk = 4 * kWave;               // elements of a wave's chunk = state block
 constexpr int kAwUnroll = 4;                      // chunks per wave
+constexpr int kAwAhead = 2;                       // chunks whose loads are in flight together
 constexpr int kAwTile = kAwChunk * kAwWaves * kAwUnroll;
 constexpr int32_t kAwMagic = 0x41645757;
 constexpr int kAwMaxLevel = 0x7F7;                // largest finite: exponent 254, mantissa 7
@@ -50,7 +51,7 @@ __device__ __forceinline__ uint32_t aw_next(uint32_t x) {   // xorshift32 (Marsa
   return x ^ (x << 5);
 }
 
-// Four consecutive elements; kFull: all there and the pointer aligned for one access.
+// Four consecutive elements of an array, as loaded; kFull: all there and aligned for one access.
 template <bool kFull, typename T>
 __device__ __forceinline__ void aw_load(const T* p, int left, T (&v)[4]) {
   if constexpr (kFull) {
@@ -77,124 +78,239 @@ __device__ __forceinline__ void aw_store(T* p, int left, const T (&v)[4]) {
       if (j < left) p[j] = v[j];
   }
 }
+// bf16 and codes travel as words: two or four elements of one register.
+template <bool kFull>
+__device__ __forceinline__ void aw_load(const uint16_t* p, int left, uint32_t (&w)[2]) {
+  if constexpr (kFull) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    w[0] = x.x;
+    w[1] = x.y;
+  } else {
+    uint16_t v[4];
+    aw_load<false>(p, left, v);
+    w[0] = v[0] | (uint32_t)v[1] << 16;
+    w[1] = v[2] | (uint32_t)v[3] << 16;
+  }
+}
+template <bool kFull>
+__device__ __forceinline__ void aw_store(uint16_t* p, int left, const uint32_t (&w)[2]) {
+  if constexpr (kFull) {
+    *reinterpret_cast<uint2*>(p) = uint2{w[0], w[1]};
+  } else {
+    const uint16_t v[4] = {(uint16_t)w[0], (uint16_t)(w[0] >> 16), (uint16_t)w[1],
+                           (uint16_t)(w[1] >> 16)};
+    aw_store<false>(p, left, v);
+  }
+}
+template <bool kFull>
+__device__ __forceinline__ uint32_t aw_load_codes(const uint8_t* p, int left) {
+  if constexpr (kFull) return *reinterpret_cast<const uint32_t*>(p);
+  uint8_t v[4];
+  aw_load<false>(p, left, v);
+  return v[0] | (uint32_t)v[1] << 8 | (uint32_t)v[2] << 16 | (uint32_t)v[3] << 24;
+}
+template <bool kFull>
+__device__ __forceinline__ void aw_store_codes(uint8_t* p, int left, uint32_t w) {
+  if constexpr (kFull) {
+    *reinterpret_cast<uint32_t*>(p) = w;
+  } else {
+    const uint8_t v[4] = {(uint8_t)w, (uint8_t)(w >> 8), (uint8_t)(w >> 16), (uint8_t)(w >> 24)};
+    aw_store<false>(p, left, v);
+  }
+}
 
-__device__ __forceinline__ float aw_f32(float x) { return x; }
-__device__ __forceinline__ float aw_f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+// What a lane holds of one chunk, as loaded: fp32 as it is, bf16 in words.
+template <typename T>
+struct AwFour {
+  float x[4];
+  template <bool kFull>
+  __device__ __forceinline__ void load(const void* p, int64_t i, int left) {
+    aw_load<kFull>(static_cast<const float*>(p) + i, left, x);
+  }
+  __device__ __forceinline__ float at(int j) const { return x[j]; }
+};
+template <>
+struct AwFour<uint16_t> {
+  uint32_t w[2];
+  template <bool kFull>
+  __device__ __forceinline__ void load(const void* p, int64_t i, int left) {
+    aw_load<kFull>(static_cast<const uint16_t*>(p) + i, left, w);
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+  }
+};
+template <typename P, typename G, bool k8>
+struct AwChunk {
+  AwFour<P> p;
+  AwFour<G> g;
+  AwFour<float> m, v;                             // fp32 states
+  uint32_t mc, vc;                                // 8-bit states
+  int tops;
+  template <bool kFull>
+  __device__ __forceinline__ void load(const AwTensor& t, int64_t chunk, int64_t i, int left) {
+    p.template load<kFull>(t.t.param, i, left);
+    g.template load<kFull>(t.t.grad, i, left);
+    if constexpr (k8) {
+      mc = aw_load_codes<kFull>(static_cast<const uint8_t*>(t.t.m) + i, left);
+      vc = aw_load_codes<kFull>(static_cast<const uint8_t*>(t.t.v) + i, left);
+      tops = t.t.tops[chunk / kAwChunk];
+    } else {
+      m.template load<kFull>(t.t.m, i, left);
+      v.template load<kFull>(t.t.v, i, left);
+    }
+  }
+};
 
-// Level of |x| after adding `dither` / 2^16 of a step; 0 for x = 0.
-__device__ __forceinline__ int aw_level(float x, uint32_t dither) {
-  const uint32_t bits = __float_as_uint(x) & 0x7FFFFFFFu;
-  const int level = (int)((bits + (dither << 4)) >> 20);
-  return bits ? min(level, kAwMaxLevel) : 0;
+// Value of code j of a word: its level (size - span + top), cut at 0; code 0 is zero.
+__device__ __forceinline__ float aw_decode_m(uint32_t codes, int j, int top) {
+  const int size = (codes >> (8 * j)) & 127;
+  const uint32_t x = (uint32_t)max((size << 20) + ((top - 127) << 20), 0);
+  return __uint_as_float((size ? x : 0u) | ((codes << (24 - 8 * j)) & 0x80000000u));
 }
-__device__ __forceinline__ float aw_value(int level) {
-  return __uint_as_float((uint32_t)max(level, 0) << 20);
-}
-__device__ __forceinline__ float aw_decode_m(uint32_t code, int top) {
-  const int size = code & 127;
-  const float x = size ? aw_value(size - 127 + top) : 0.0f;
-  return code & 128 ? -x : x;
-}
-__device__ __forceinline__ float aw_decode_v(uint32_t code, int top) {
-  return code ? aw_value((int)code - 255 + top) : 0.0f;
+__device__ __forceinline__ float aw_decode_v(uint32_t codes, int j, int top) {
+  const int size = (codes >> (8 * j)) & 255;
+  const uint32_t x = (uint32_t)max((size << 20) + ((top - 255) << 20), 0);
+  return __uint_as_float(size ? x : 0u);
 }
 
 struct AwScalars {
-  float decay, rate, root2, scale;                // 1 - lr wd, lr / bc1, sqrt(bc2), sched[1]
+  float decay, rate, root2, scale;                // 1 - lr wd, lr / bc1, 1 / sqrt(bc2), sched[1]
 };
 
+// 1 - beta^t from t log beta <= 0 in double (in fp32, 1 - 0.999^1 would be good to 5 digits):
+// with y = k ln 2 + r, 1 - e^y = (1 - 2^k) - 2^k (e^r - 1), e^r - 1 by its series, whose first
+// term left out is r^11 / 11! < 4e-13.
+__device__ __forceinline__ float aw_correction(double y) {
+  if (y < -700.0) return 1.0f;                    // also beta = 0
+  const double k = __builtin_rint(y * 1.4426950408889634);
+  const double r = fma(k, -0.6931471805599453, y);
+  double s = 1.0 / 3628800.0;
+  s = fma(s, r, 1.0 / 362880.0);
+  s = fma(s, r, 1.0 / 40320.0);
+  s = fma(s, r, 1.0 / 5040.0);
+  s = fma(s, r, 1.0 / 720.0);
+  s = fma(s, r, 1.0 / 120.0);
+  s = fma(s, r, 1.0 / 24.0);
+  s = fma(s, r, 1.0 / 6.0);
+  s = fma(s, r, 0.5);
+  s = fma(s * r, r, r);
+  const double p = __builtin_amdgcn_ldexp(1.0, (int)k);
+  return (float)((1.0 - p) - p * s);
+}
+
+// One chunk: step, round, store.
+template <typename P, typename G, bool k8, bool kFull>
+__device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, k8>& in,
+                                         int64_t chunk, int64_t i, int left, const AwScalars& c,
+                                         const AwArgs& a, uint32_t key) {
+#pragma clang fp contract(off)
+  float m[4], v[4], w[4], root[4];
+  bool bad = false, tiny = false;
+  const int tops = k8 ? __builtin_amdgcn_readfirstlane(in.tops) : 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float g = in.g.at(j) * c.scale;
+    const bool off = (__float_as_uint(g) & 0x7F800000u) == 0x7F800000u;
+    bad |= off;
+    g = off ? 0.0f : g;
+    m[j] = k8 ? aw_decode_m(in.mc, j, tops & 0xFFFF) : in.m.at(j);
+    v[j] = k8 ? aw_decode_v(in.vc, j, tops >> 16) : in.v.at(j);
+    m[j] = m[j] * a.b1 + g * a.ob1;
+    v[j] = v[j] * a.b2 + g * g * a.ob2;
+    // root and reciprocal by the hardware's approximations, each within a unit in the last
+    // place; the root takes a subnormal number for 0, so those go the long way
+    root[j] = __builtin_amdgcn_sqrtf(v[j]);
+    tiny |= __builtin_amdgcn_classf(v[j], 1 << 7);
+  }
+  if (ballot(tiny))
+#pragma unroll
+    for (int j = 0; j < 4; ++j) root[j] = sqrtf(v[j]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float q = m[j] * __builtin_amdgcn_rcpf(fmaf(root[j], c.root2, a.eps));
+    w[j] = fmaf(-c.rate, q, in.p.at(j) * c.decay);
+  }
+  uint32_t r[6] = {0};
+  if constexpr (k8 || sizeof(P) == 2) {
+    r[0] = aw_mix((uint32_t)(i >> 2) * 0x9E3779B9u ^ key);
+#pragma unroll
+    for (int j = 1; j < (k8 ? 6 : 2); ++j) r[j] = aw_next(r[j - 1]);
+  }
+  if constexpr (sizeof(P) == 2) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t bits = __float_as_uint(w[j]);
+      const uint32_t d = j & 1 ? r[j / 2] >> 16 : r[j / 2] & 0xFFFFu;
+      // an infinity or NaN is cut as it is (a NaN's upper bits are set)
+      o[j] = (bits & 0x7F800000u) == 0x7F800000u ? bits : bits + d;
+    }
+    const uint32_t word[2] = {o[0] >> 16 | (o[1] & 0xFFFF0000u), o[2] >> 16 | (o[3] & 0xFFFF0000u)};
+    aw_store<kFull>(static_cast<uint16_t*>(t.t.param) + i, left, word);
+  } else {
+    aw_store<kFull>(static_cast<float*>(t.t.param) + i, left, w);
+    if (t.t.copy) {
+      const uint32_t word[2] = {pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
+      aw_store<kFull>(t.t.copy + i, left, word);
+    }
+  }
+  if constexpr (k8) {
+    uint32_t bm[4], bv[4];
+    int lm[4], lv[4], top_m = 0, top_v = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool on = kFull || j < left;
+      bm[j] = on ? __float_as_uint(m[j]) & 0x7FFFFFFFu : 0u;
+      bv[j] = on ? __float_as_uint(v[j]) : 0u;    // v >= +0
+      lm[j] = min((int)((bm[j] + ((r[2 + j] & 0xFFFFu) << 4)) >> 20), kAwMaxLevel);
+      lv[j] = min((int)((bv[j] + ((r[2 + j] >> 16) << 4)) >> 20), kAwMaxLevel);
+      top_m = max(top_m, lm[j]);
+      top_v = max(top_v, lv[j]);
+    }
+    top_m = wave_max(top_m);
+    top_v = wave_max(top_v);
+    uint32_t mc = 0, vc = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int cm = bm[j] ? max(lm[j] - top_m + 127, 0) : 0;
+      const uint32_t sign = __float_as_uint(m[j]) >> 24 & 128u;
+      mc |= (cm ? (uint32_t)cm | sign : 0u) << (8 * j);
+      vc |= (bv[j] ? (uint32_t)max(lv[j] - top_v + 255, 1) : 0u) << (8 * j);
+    }
+    aw_store_codes<kFull>(static_cast<uint8_t*>(t.t.m) + i, left, mc);
+    aw_store_codes<kFull>(static_cast<uint8_t*>(t.t.v) + i, left, vc);
+    if (threadIdx.x % kWave == 0) t.t.tops[chunk / kAwChunk] = top_m | top_v << 16;
+  } else {
+    aw_store<kFull>(static_cast<float*>(t.t.m) + i, left, m);
+    aw_store<kFull>(static_cast<float*>(t.t.v) + i, left, v);
+  }
+  return bad;
+}
+
+// A tile: kAwAhead chunks are loaded together, then stepped one by one.
 template <typename P, typename G, bool k8, bool kFull>
 __device__ __forceinline__ bool aw_tile(const AwTensor& t, int64_t base, const AwScalars& c,
                                         const AwArgs& a, uint32_t key) {
-#pragma clang fp contract(off)
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const P* p_in = static_cast<const P*>(t.t.param);
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   bool bad = false;
-  for (int u = 0; u < kAwUnroll; ++u) {
-    const int64_t chunk = base + (int64_t)(u * kAwWaves + wave) * kAwChunk;
-    if (chunk >= t.t.n) break;
-    const int64_t i = chunk + lane * 4;
-    const int left = (int)min((int64_t)4, t.t.n - i);     // <= 0: past the end
-    P p[4];
-    G g[4];
-    aw_load<kFull>(p_in + i, left, p);
-    aw_load<kFull>(static_cast<const G*>(t.t.grad) + i, left, g);
-    float m[4], v[4];
-    if constexpr (k8) {
-      uint8_t mc[4], vc[4];
-      aw_load<kFull>(static_cast<const uint8_t*>(t.t.m) + i, left, mc);
-      aw_load<kFull>(static_cast<const uint8_t*>(t.t.v) + i, left, vc);
-      const int tops = t.t.tops[chunk / kAwChunk];
+  constexpr int kAhead = kFull ? kAwAhead : 1;
+  for (int u = 0; u < kAwUnroll; u += kAhead) {
+    AwChunk<P, G, k8> in[kAhead];
+    if (!kFull && base + (int64_t)(u * kAwWaves + wave) * kAwChunk >= t.t.n) break;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        m[j] = aw_decode_m(mc[j], tops & 0xFFFF);
-        v[j] = aw_decode_v(vc[j], tops >> 16);
-      }
-    } else {
-      aw_load<kFull>(static_cast<const float*>(t.t.m) + i, left, m);
-      aw_load<kFull>(static_cast<const float*>(t.t.v) + i, left, v);
+    for (int h = 0; h < kAhead; ++h) {
+      const int64_t chunk = base + (int64_t)((u + h) * kAwWaves + wave) * kAwChunk;
+      const int64_t i = chunk + lane * 4;
+      in[h].template load<kFull>(t, chunk, i, (int)min((int64_t)4, t.t.n - i));
     }
-    float w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float gj = aw_f32(g[j]) * c.scale;
-      const bool off = (__float_as_uint(gj) & 0x7F800000u) == 0x7F800000u;
-      bad |= off;
-      gj = off ? 0.0f : gj;
-      m[j] = m[j] * a.b1 + gj * a.ob1;
-      v[j] = v[j] * a.b2 + gj * gj * a.ob2;
-      w[j] = aw_f32(p[j]) * c.decay - c.rate * (m[j] / (sqrtf(v[j]) / c.root2 + a.eps));
-    }
-    uint32_t r[6] = {0};
-    if constexpr (k8 || sizeof(P) == 2) {
-      r[0] = aw_mix((uint32_t)(i >> 2) * 0x9E3779B9u ^ key);
-#pragma unroll
-      for (int j = 1; j < 6; ++j) r[j] = aw_next(r[j - 1]);
-    }
-    if constexpr (sizeof(P) == 2) {
-      uint16_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t bits = __float_as_uint(w[j]);
-        const uint32_t d = j & 1 ? r[j / 2] >> 16 : r[j / 2] & 0xFFFFu;
-        // an infinity or NaN is cut as it is (a NaN's upper bits are set)
-        o[j] = (uint16_t)(((bits & 0x7F800000u) == 0x7F800000u ? bits : bits + d) >> 16);
-      }
-      aw_store<kFull>(static_cast<uint16_t*>(t.t.param) + i, left, o);
-    } else {
-      aw_store<kFull>(static_cast<float*>(t.t.param) + i, left, w);
-      if (t.t.copy) {
-        uint16_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = (uint16_t)f32_to_bf16(w[j]);
-        aw_store<kFull>(t.t.copy + i, left, o);
-      }
-    }
-    if constexpr (k8) {
-      int lm[4], lv[4], top_m = 0, top_v = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool on = kFull || j < left;
-        lm[j] = on ? aw_level(m[j], r[2 + j] & 0xFFFFu) : 0;
-        lv[j] = on ? aw_level(v[j], r[2 + j] >> 16) : 0;
-        top_m = max(top_m, lm[j]);
-        top_v = max(top_v, lv[j]);
-      }
-      top_m = wave_max(top_m);
-      top_v = wave_max(top_v);
-      uint8_t mc[4], vc[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int cm = max(lm[j] - top_m + 127, 0);
-        mc[j] = (uint8_t)(m[j] != 0.0f && cm ? cm | (m[j] < 0.0f ? 128 : 0) : 0);
-        vc[j] = (uint8_t)(v[j] > 0.0f ? max(lv[j] - top_v + 255, 1) : 0);
-      }
-      aw_store<kFull>(static_cast<uint8_t*>(t.t.m) + i, left, mc);
-      aw_store<kFull>(static_cast<uint8_t*>(t.t.v) + i, left, vc);
-      if (lane == 0) t.t.tops[chunk / kAwChunk] = top_m | top_v << 16;
-    } else {
-      aw_store<kFull>(static_cast<float*>(t.t.m) + i, left, m);
-      aw_store<kFull>(static_cast<float*>(t.t.v) + i, left, v);
+    for (int h = 0; h < kAhead; ++h) {
+      const int64_t chunk = base + (int64_t)((u + h) * kAwWaves + wave) * kAwChunk;
+      const int64_t i = chunk + lane * 4;
+      bad |= aw_chunk<P, G, k8, kFull>(t, in[h], chunk, i, (int)min((int64_t)4, t.t.n - i), c, a,
+                                       key);
     }
   }
   return bad;
@@ -219,11 +335,14 @@ __global__ __launch_bounds__(kAwThreads) void adamw_kernel(const char* __restric
   const AwTensor& x = tensors[q];
   const int64_t base = ((int64_t)blockIdx.x - x.first_tile) * kAwTile;
   const float lr = sched[0] * x.t.lr_scale;
-  // 1 - beta^t = -expm1(t log beta), in double: 1 - 0.999^1 in fp32 is good to 5 digits only
+  // both corrections at once: even lanes the first, odd lanes the second
+  const float bc = aw_correction(t * (threadIdx.x & 1 ? a.log_b2 : a.log_b1));
+  const float bc1 = __int_as_float(readlane(__float_as_int(bc), 0));
+  const float bc2 = __int_as_float(readlane(__float_as_int(bc), 1));
   AwScalars c;
   c.decay = 1.0f - lr * x.t.weight_decay;
-  c.rate = lr / (float)-expm1(t * a.log_b1);
-  c.root2 = sqrtf((float)-expm1(t * a.log_b2));
+  c.rate = lr / bc1;
+  c.root2 = 1.0f / sqrtf(bc2);
   c.scale = sched[1];
   const uint32_t key = aw_mix(aw_mix((uint32_t)t * 0x9E3779B9u + a.seed) ^ (uint32_t)(q + 1));
   const bool full = x.vec && base + kAwTile <= x.t.n;
@@ -232,20 +351,41 @@ __global__ __launch_bounds__(kAwThreads) void adamw_kernel(const char* __restric
   if (ballot(bad) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_GRAD);
 }
 
+// Four elements per thread; kVec: every pointer is aligned for them.
 template <typename T>
 __global__ __launch_bounds__(kAwThreads) void adamw_decode_kernel(
     const uint8_t* __restrict__ mc, const uint8_t* __restrict__ vc,
-    const int32_t* __restrict__ tops, int64_t n, T* __restrict__ m, T* __restrict__ v) {
-  const int64_t i = (int64_t)blockIdx.x * kAwThreads + threadIdx.x;
+    const int32_t* __restrict__ tops, int64_t n, int vec, T* __restrict__ m, T* __restrict__ v) {
+  const int64_t i = ((int64_t)blockIdx.x * kAwThreads + threadIdx.x) * 4;
   if (i >= n) return;
-  const int top = tops[i / kAwChunk];
-  const float a = aw_decode_m(mc[i], top & 0xFFFF), b = aw_decode_v(vc[i], top >> 16);
+  const int top = tops[i / kAwChunk], left = (int)min((int64_t)4, n - i);
+  const bool full = vec && left == 4;
+  const uint32_t cm = full ? aw_load_codes<true>(mc + i, 4) : aw_load_codes<false>(mc + i, left);
+  const uint32_t cv = full ? aw_load_codes<true>(vc + i, 4) : aw_load_codes<false>(vc + i, left);
+  float a[4], b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    a[j] = aw_decode_m(cm, j, top & 0xFFFF);
+    b[j] = aw_decode_v(cv, j, top >> 16);
+  }
   if constexpr (sizeof(T) == 4) {
-    m[i] = a;
-    v[i] = b;
+    if (full) {
+      aw_store<true>(m + i, 4, a);
+      aw_store<true>(v + i, 4, b);
+    } else {
+      aw_store<false>(m + i, left, a);
+      aw_store<false>(v + i, left, b);
+    }
   } else {
-    m[i] = (T)(__float_as_uint(a) >> 16);
-    v[i] = (T)(__float_as_uint(b) >> 16);
+    const uint32_t wa[2] = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
+    const uint32_t wb[2] = {pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
+    if (full) {
+      aw_store<true>(m + i, 4, wa);
+      aw_store<true>(v + i, 4, wb);
+    } else {
+      aw_store<false>(m + i, left, wa);
+      aw_store<false>(v + i, left, wb);
+    }
   }
 }
 
@@ -343,7 +483,7 @@ extern "C" uep_status uep_adamw(const void* plan, int64_t n_tiles, int32_t param
       (grad_dtype != UEP_F32 && grad_dtype != UEP_BF16) || (state_bits != 8 && state_bits != 32))
     return UEP_EINVAL;
   if (!(beta1 >= 0.0 && beta1 < 1.0 && beta2 >= 0.0 && beta2 < 1.0) ||
-      !(eps > 0.0 && eps < __builtin_inf()))
+      !(eps >= 0x1p-126 && eps <= 0x1p126))    // a normal fp32 number
     return UEP_EINVAL;
   if (n_tiles >= (1 << 24)) return UEP_EGEOM;
   if (n_tiles == 0) return UEP_OK;
@@ -380,15 +520,19 @@ extern "C" uep_status uep_adamw_decode(const uint8_t* m_codes, const uint8_t* v_
   if (n < 0 || (dtype != UEP_F32 && dtype != UEP_BF16)) return UEP_EINVAL;
   if (n == 0) return UEP_OK;
   if (!m_codes || !v_codes || !tops || !m || !v) return UEP_EINVAL;
-  const int64_t blocks = (n + kAwThreads - 1) / kAwThreads;
+  const int64_t blocks = (n + 4 * kAwThreads - 1) / (4 * kAwThreads);
   if (blocks >= (1 << 24)) return UEP_EGEOM;
+  const uintptr_t align = dtype == UEP_F32 ? 16 : 8;
+  const int vec = ((uintptr_t)m_codes | (uintptr_t)v_codes) % 4 == 0 &&
+                  ((uintptr_t)m | (uintptr_t)v) % align == 0;
   hipStream_t s = uep_stream(stream);
   if (dtype == UEP_F32)
     hipLaunchKernelGGL(adamw_decode_kernel<float>, dim3((unsigned)blocks), dim3(kAwThreads), 0, s,
-                       m_codes, v_codes, tops, n, static_cast<float*>(m), static_cast<float*>(v));
+                       m_codes, v_codes, tops, n, vec, static_cast<float*>(m),
+                       static_cast<float*>(v));
   else
     hipLaunchKernelGGL(adamw_decode_kernel<uint16_t>, dim3((unsigned)blocks), dim3(kAwThreads), 0,
-                       s, m_codes, v_codes, tops, n, static_cast<uint16_t*>(m),
+                       s, m_codes, v_codes, tops, n, vec, static_cast<uint16_t*>(m),
                        static_cast<uint16_t*>(v));
   UEP_CHECK_LAUNCH();
   return UEP_OK;

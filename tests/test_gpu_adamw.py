@@ -162,6 +162,17 @@ def test_huge_and_tiny_gradients_in_8_bits():
     assert torch.isfinite(p).all()
 
 
+def test_second_moments_below_the_normal_range():
+    """Squares around 2^-126 with an eps of 1e-30: the root of a subnormal number counts."""
+    say("case: adamw, subnormal second moments")
+    rng = np.random.default_rng(105)
+    n = 5000
+    g = (10.0 ** rng.uniform(-22, -18, n) * rng.choice([-1, 1], n)).astype(np.float32)
+    z = torch.zeros(n, device=DEV)
+    check_step([torch.ones(n, device=DEV)], [place(g, F, 0)], [z], [z.clone()], None, None, 1,
+               1e-3, 1.0, [0.0], [1.0], (0.9, 0.999), 1e-30, 0)
+
+
 def test_plan_errors_leave_everything_alone():
     say("case: adamw plan errors")
     p, g, m, v = (torch.ones(500, device=DEV) for _ in range(4))
