@@ -588,7 +588,7 @@ uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, int64_t out
  *   zeros.  `copy` is optional with fp32 parameters: the new value rounded to nearest bf16.
  *   Pointers need the alignment of their own type only; tensors in which every group of four
  *   elements is aligned (16 bytes of fp32, 8 of bf16, 4 of codes) are faster.
- *   At most 65535 tensors of at most 2^33 elements.
+ *   At most 65535 tensors of at most 2^33 elements, 1.7e10 together.
  * uep_adamw: one step.  n_tiles and the types as given to and by uep_adamw_prepare.
  *   step   [1] int32  in   t >= 1, device memory
  *   sched  [2] fp32   in   {learning rate, factor on every gradient}, device memory, so a
@@ -598,7 +598,7 @@ uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, int64_t out
  *   err               out  optional; UEP_ERR_GRAD, UEP_ERR_PLAN (then nothing else is written)
  * uep_adamw_decode: the values that 8-bit states stand for (checkpoints), n elements from
  *   the start of a tensor or of several whose starts are multiples of 256 apart;
- *   m, v [n] of dtype UEP_F32 or UEP_BF16 (both hold them exactly)
+ *   m, v [n] of dtype UEP_F32 or UEP_BF16 (both hold them exactly); n < 1.7e10
  * ------------------------------------------------------------------------- */
 typedef struct uep_adamw_tensor {
   void* param;          /* [n] param_dtype, updated */

@@ -1,8 +1,8 @@
 // AdamW over many tensors in one launch, states in fp32 or 8 bits (uep.h: AdamW).
 //
 // HBM-bound: every element's parameter, gradient and states are read once and written
-// once.  The plan lists the work as tiles of 4096 elements of one tensor each; a
-// 256-thread workgroup takes one tile, each wave four chunks of 256 consecutive elements
+// once.  The plan lists the work as tiles of 1024 or 4096 elements of one tensor each; a
+// 256-thread workgroup takes one tile, each wave one or four chunks of 256 consecutive elements
 // (four per lane: 16-byte accesses for fp32, 8 for bf16, 4 for the codes).  A chunk is a
 // block of the 8-bit states, so a block's largest level is one reduction over a wave.
 #include <stdlib.h>
@@ -14,16 +14,15 @@ namespace uep {
 constexpr int kAwThreads = 256;
 constexpr int kAwWaves = kAwThreads / kWave;
 constexpr int kAwChunk = 4 * kWave;               // elements of a wave's chunk = state block
-constexpr int kAwUnroll = 4;                      // chunks per wave
-constexpr int kAwAhead = 2;                       // chunks whose loads are in flight together
-constexpr int kAwTile = kAwChunk * kAwWaves * kAwUnroll;
+constexpr int kAwLong = 4;                        // chunks per wave of a long tile
+constexpr int64_t kAwLongFrom = 4ll << 20;
 constexpr int32_t kAwMagic = 0x41645757;
 constexpr int kAwMaxLevel = 0x7F7;                // largest finite: exponent 254, mantissa 7
 constexpr int64_t kAwMaxElems = 1ll << 33;
 constexpr int kAwMaxTensors = 65535;
 
 struct AwHeader {
-  int32_t magic, count, param_dtype, grad_dtype, state_bits, n_tiles, pad[2];
+  int32_t magic, count, param_dtype, grad_dtype, state_bits, n_tiles, unroll, pad;
 };
 struct AwTensor {
   uep_adamw_tensor t;
@@ -51,12 +50,15 @@ __device__ __forceinline__ uint32_t aw_next(uint32_t x) {   // xorshift32 (Marsa
   return x ^ (x << 5);
 }
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 // Four consecutive elements of an array, as loaded; kFull: all there and aligned for one access.
+// Accesses are non-temporal: every byte is used once a step.
 template <bool kFull, typename T>
 __device__ __forceinline__ void aw_load(const T* p, int left, T (&v)[4]) {
   if constexpr (kFull) {
     typedef T vec __attribute__((ext_vector_type(4)));
-    const vec x = *reinterpret_cast<const vec*>(p);
+    const vec x = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = x[j];
   } else {
@@ -71,7 +73,7 @@ __device__ __forceinline__ void aw_store(T* p, int left, const T (&v)[4]) {
     vec x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = v[j];
-    *reinterpret_cast<vec*>(p) = x;
+    __builtin_nontemporal_store(x, reinterpret_cast<vec*>(p));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -82,7 +84,7 @@ __device__ __forceinline__ void aw_store(T* p, int left, const T (&v)[4]) {
 template <bool kFull>
 __device__ __forceinline__ void aw_load(const uint16_t* p, int left, uint32_t (&w)[2]) {
   if constexpr (kFull) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     w[0] = x.x;
     w[1] = x.y;
   } else {
@@ -95,7 +97,7 @@ __device__ __forceinline__ void aw_load(const uint16_t* p, int left, uint32_t (&
 template <bool kFull>
 __device__ __forceinline__ void aw_store(uint16_t* p, int left, const uint32_t (&w)[2]) {
   if constexpr (kFull) {
-    *reinterpret_cast<uint2*>(p) = uint2{w[0], w[1]};
+    __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
   } else {
     const uint16_t v[4] = {(uint16_t)w[0], (uint16_t)(w[0] >> 16), (uint16_t)w[1],
                            (uint16_t)(w[1] >> 16)};
@@ -104,7 +106,7 @@ __device__ __forceinline__ void aw_store(uint16_t* p, int left, const uint32_t (
 }
 template <bool kFull>
 __device__ __forceinline__ uint32_t aw_load_codes(const uint8_t* p, int left) {
-  if constexpr (kFull) return *reinterpret_cast<const uint32_t*>(p);
+  if constexpr (kFull) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
   uint8_t v[4];
   aw_load<false>(p, left, v);
   return v[0] | (uint32_t)v[1] << 8 | (uint32_t)v[2] << 16 | (uint32_t)v[3] << 24;
@@ -112,7 +114,7 @@ __device__ __forceinline__ uint32_t aw_load_codes(const uint8_t* p, int left) {
 template <bool kFull>
 __device__ __forceinline__ void aw_store_codes(uint8_t* p, int left, uint32_t w) {
   if constexpr (kFull) {
-    *reinterpret_cast<uint32_t*>(p) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(p));
   } else {
     const uint8_t v[4] = {(uint8_t)w, (uint8_t)(w >> 8), (uint8_t)(w >> 16), (uint8_t)(w >> 24)};
     aw_store<false>(p, left, v);
@@ -162,16 +164,84 @@ struct AwChunk {
   }
 };
 
-// Value of code j of a word: its level (size - span + top), cut at 0; code 0 is zero.
+// Value of code j of a word: its level (size - span + top), cut at 0; code 0 is zero.  kPlain:
+// the block's window lies above level 0 (top >= span), so that nothing is cut.
+template <bool kPlain>
 __device__ __forceinline__ float aw_decode_m(uint32_t codes, int j, int top) {
   const int size = (codes >> (8 * j)) & 127;
-  const uint32_t x = (uint32_t)max((size << 20) + ((top - 127) << 20), 0);
-  return __uint_as_float((size ? x : 0u) | ((codes << (24 - 8 * j)) & 0x80000000u));
+  int x = (size << 20) + ((top - 127) << 20);
+  if (!kPlain) x = max(x, 0);
+  return __uint_as_float((size ? (uint32_t)x : 0u) | ((codes << (24 - 8 * j)) & 0x80000000u));
 }
+template <bool kPlain>
 __device__ __forceinline__ float aw_decode_v(uint32_t codes, int j, int top) {
   const int size = (codes >> (8 * j)) & 255;
-  const uint32_t x = (uint32_t)max((size << 20) + ((top - 255) << 20), 0);
-  return __uint_as_float(size ? x : 0u);
+  int x = (size << 20) + ((top - 255) << 20);
+  if (!kPlain) x = max(x, 0);
+  return __uint_as_float(size ? (uint32_t)x : 0u);
+}
+__device__ __forceinline__ void aw_decode(uint32_t mc, uint32_t vc, int tops, float (&m)[4],
+                                          float (&v)[4]) {
+  const int top_m = tops & 0xFFFF, top_v = tops >> 16;
+  if (top_m >= 127 && top_v >= 255) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m[j] = aw_decode_m<true>(mc, j, top_m);
+      v[j] = aw_decode_v<true>(vc, j, top_v);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m[j] = aw_decode_m<false>(mc, j, top_m);
+      v[j] = aw_decode_v<false>(vc, j, top_v);
+    }
+  }
+}
+
+// Codes of four new m and v and their block's tops; the whole wave calls it with its chunk.
+// Levels come from the random words r; the common case, in which both windows lie above
+// level 0 and below infinity, needs no check of zeros (their code comes out below 0) and no
+// clamp.
+__device__ __forceinline__ int aw_encode(const float (&m)[4], const float (&v)[4],
+                                         const uint32_t* r, int left, uint32_t* mc, uint32_t* vc) {
+  uint32_t bm[4], bv[4];
+  int lm[4], lv[4], top_m = 0, top_v = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool on = j < left;
+    bm[j] = on ? __float_as_uint(m[j]) & 0x7FFFFFFFu : 0u;
+    bv[j] = on ? __float_as_uint(v[j]) : 0u;      // v >= +0
+    lm[j] = (int)((bm[j] + ((r[j] & 0xFFFFu) << 4)) >> 20);
+    lv[j] = (int)((bv[j] + ((r[j] >> 16) << 4)) >> 20);
+    top_m = max(top_m, lm[j]);
+    top_v = max(top_v, lv[j]);
+  }
+  top_m = wave_max(top_m);
+  top_v = wave_max(top_v);
+  uint32_t cm[4], cv[4];
+  if (top_m > 127 && top_v > 255 && max(top_m, top_v) <= kAwMaxLevel) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cm[j] = (uint32_t)max(lm[j] - top_m + 127, 0);
+      cv[j] = (uint32_t)max(lv[j] - top_v + 255, (int)min(bv[j], 1u));
+    }
+  } else {
+    top_m = min(top_m, kAwMaxLevel);
+    top_v = min(top_v, kAwMaxLevel);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cm[j] = bm[j] ? (uint32_t)max(min(lm[j], kAwMaxLevel) - top_m + 127, 0) : 0u;
+      cv[j] = bv[j] ? (uint32_t)max(min(lv[j], kAwMaxLevel) - top_v + 255, 1) : 0u;
+    }
+  }
+  *mc = *vc = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t sign = __float_as_uint(m[j]) >> 24 & 128u;
+    *mc |= (cm[j] ? cm[j] | sign : 0u) << (8 * j);
+    *vc |= cv[j] << (8 * j);
+  }
+  return top_m | top_v << 16;
 }
 
 struct AwScalars {
@@ -205,19 +275,30 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
                                          int64_t chunk, int64_t i, int left, const AwScalars& c,
                                          const AwArgs& a, uint32_t key) {
 #pragma clang fp contract(off)
-  float m[4], v[4], w[4], root[4];
+  float g[4], m[4], v[4], w[4], root[4];
   bool bad = false, tiny = false;
-  const int tops = k8 ? __builtin_amdgcn_readfirstlane(in.tops) : 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float g = in.g.at(j) * c.scale;
-    const bool off = (__float_as_uint(g) & 0x7F800000u) == 0x7F800000u;
-    bad |= off;
-    g = off ? 0.0f : g;
-    m[j] = k8 ? aw_decode_m(in.mc, j, tops & 0xFFFF) : in.m.at(j);
-    v[j] = k8 ? aw_decode_v(in.vc, j, tops >> 16) : in.v.at(j);
-    m[j] = m[j] * a.b1 + g * a.ob1;
-    v[j] = v[j] * a.b2 + g * g * a.ob2;
+    g[j] = in.g.at(j) * c.scale;
+    bad |= (__float_as_uint(g[j]) & 0x7F800000u) == 0x7F800000u;
+  }
+  if (ballot(bad))
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if ((__float_as_uint(g[j]) & 0x7F800000u) == 0x7F800000u) g[j] = 0.0f;
+  if constexpr (k8) {
+    aw_decode(in.mc, in.vc, __builtin_amdgcn_readfirstlane(in.tops), m, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      m[j] = in.m.at(j);
+      v[j] = in.v.at(j);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    m[j] = m[j] * a.b1 + g[j] * a.ob1;
+    v[j] = v[j] * a.b2 + g[j] * g[j] * a.ob2;
     // root and reciprocal by the hardware's approximations, each within a unit in the last
     // place; the root takes a subnormal number for 0, so those go the long way
     root[j] = __builtin_amdgcn_sqrtf(v[j]);
@@ -243,8 +324,9 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
     for (int j = 0; j < 4; ++j) {
       const uint32_t bits = __float_as_uint(w[j]);
       const uint32_t d = j & 1 ? r[j / 2] >> 16 : r[j / 2] & 0xFFFFu;
-      // an infinity or NaN is cut as it is (a NaN's upper bits are set)
-      o[j] = (bits & 0x7F800000u) == 0x7F800000u ? bits : bits + d;
+      // a NaN is cut as it is.  With 8-bit states it needs no check: it was made here or came
+      // from a bf16 parameter, so its lower half is zero and nothing carries
+      o[j] = !k8 && (bits & 0x7FFFFFFFu) > 0x7F800000u ? bits : bits + d;
     }
     const uint32_t word[2] = {o[0] >> 16 | (o[1] & 0xFFFF0000u), o[2] >> 16 | (o[3] & 0xFFFF0000u)};
     aw_store<kFull>(static_cast<uint16_t*>(t.t.param) + i, left, word);
@@ -256,31 +338,11 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
     }
   }
   if constexpr (k8) {
-    uint32_t bm[4], bv[4];
-    int lm[4], lv[4], top_m = 0, top_v = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool on = kFull || j < left;
-      bm[j] = on ? __float_as_uint(m[j]) & 0x7FFFFFFFu : 0u;
-      bv[j] = on ? __float_as_uint(v[j]) : 0u;    // v >= +0
-      lm[j] = min((int)((bm[j] + ((r[2 + j] & 0xFFFFu) << 4)) >> 20), kAwMaxLevel);
-      lv[j] = min((int)((bv[j] + ((r[2 + j] >> 16) << 4)) >> 20), kAwMaxLevel);
-      top_m = max(top_m, lm[j]);
-      top_v = max(top_v, lv[j]);
-    }
-    top_m = wave_max(top_m);
-    top_v = wave_max(top_v);
-    uint32_t mc = 0, vc = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int cm = bm[j] ? max(lm[j] - top_m + 127, 0) : 0;
-      const uint32_t sign = __float_as_uint(m[j]) >> 24 & 128u;
-      mc |= (cm ? (uint32_t)cm | sign : 0u) << (8 * j);
-      vc |= (bv[j] ? (uint32_t)max(lv[j] - top_v + 255, 1) : 0u) << (8 * j);
-    }
+    uint32_t mc, vc;
+    const int tops = aw_encode(m, v, r + 2, kFull ? 4 : left, &mc, &vc);
     aw_store_codes<kFull>(static_cast<uint8_t*>(t.t.m) + i, left, mc);
     aw_store_codes<kFull>(static_cast<uint8_t*>(t.t.v) + i, left, vc);
-    if (threadIdx.x % kWave == 0) t.t.tops[chunk / kAwChunk] = top_m | top_v << 16;
+    if (threadIdx.x % kWave == 0) t.t.tops[chunk / kAwChunk] = tops;
   } else {
     aw_store<kFull>(static_cast<float*>(t.t.m) + i, left, m);
     aw_store<kFull>(static_cast<float*>(t.t.v) + i, left, v);
@@ -288,15 +350,16 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
   return bad;
 }
 
-// A tile: kAwAhead chunks are loaded together, then stepped one by one.
-template <typename P, typename G, bool k8, bool kFull>
+// A tile of kU chunks for each wave, the loads of a full one all issued before the first is
+// stepped.
+template <typename P, typename G, bool k8, int kU, bool kFull>
 __device__ __forceinline__ bool aw_tile(const AwTensor& t, int64_t base, const AwScalars& c,
                                         const AwArgs& a, uint32_t key) {
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   bool bad = false;
-  constexpr int kAhead = kFull ? kAwAhead : 1;
-  for (int u = 0; u < kAwUnroll; u += kAhead) {
+  constexpr int kAhead = kFull ? kU : 1;
+  for (int u = 0; u < kU; u += kAhead) {
     AwChunk<P, G, k8> in[kAhead];
     if (!kFull && base + (int64_t)(u * kAwWaves + wave) * kAwChunk >= t.t.n) break;
 #pragma unroll
@@ -316,6 +379,15 @@ __device__ __forceinline__ bool aw_tile(const AwTensor& t, int64_t base, const A
   return bad;
 }
 
+template <typename P, typename G, bool k8, int kU>
+__device__ __forceinline__ bool aw_step(const AwTensor& t, int64_t tile, const AwScalars& c,
+                                        const AwArgs& a, uint32_t key) {
+  constexpr int kTile = kU * kAwWaves * kAwChunk;
+  const int64_t base = (tile - t.first_tile) * kTile;
+  return t.vec && base + kTile <= t.t.n ? aw_tile<P, G, k8, kU, true>(t, base, c, a, key)
+                                        : aw_tile<P, G, k8, kU, false>(t, base, c, a, key);
+}
+
 template <typename P, typename G, bool k8>
 __global__ __launch_bounds__(kAwThreads) void adamw_kernel(const char* __restrict__ plan,
                                                            int32_t n_tiles, int32_t types,
@@ -333,7 +405,6 @@ __global__ __launch_bounds__(kAwThreads) void adamw_kernel(const char* __restric
   const int32_t* tiles = reinterpret_cast<const int32_t*>(tensors + h.count);
   const int q = tiles[blockIdx.x];
   const AwTensor& x = tensors[q];
-  const int64_t base = ((int64_t)blockIdx.x - x.first_tile) * kAwTile;
   const float lr = sched[0] * x.t.lr_scale;
   // both corrections at once: even lanes the first, odd lanes the second
   const float bc = aw_correction(t * (threadIdx.x & 1 ? a.log_b2 : a.log_b1));
@@ -345,9 +416,9 @@ __global__ __launch_bounds__(kAwThreads) void adamw_kernel(const char* __restric
   c.root2 = 1.0f / sqrtf(bc2);
   c.scale = sched[1];
   const uint32_t key = aw_mix(aw_mix((uint32_t)t * 0x9E3779B9u + a.seed) ^ (uint32_t)(q + 1));
-  const bool full = x.vec && base + kAwTile <= x.t.n;
-  const bool bad = full ? aw_tile<P, G, k8, true>(x, base, c, a, key)
-                        : aw_tile<P, G, k8, false>(x, base, c, a, key);
+  bool bad;
+  if (k8 && h.unroll == kAwLong) bad = aw_step<P, G, k8, kAwLong>(x, blockIdx.x, c, a, key);
+  else bad = aw_step<P, G, k8, 1>(x, blockIdx.x, c, a, key);
   if (ballot(bad) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_GRAD);
 }
 
@@ -363,11 +434,7 @@ __global__ __launch_bounds__(kAwThreads) void adamw_decode_kernel(
   const uint32_t cm = full ? aw_load_codes<true>(mc + i, 4) : aw_load_codes<false>(mc + i, left);
   const uint32_t cv = full ? aw_load_codes<true>(vc + i, 4) : aw_load_codes<false>(vc + i, left);
   float a[4], b[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    a[j] = aw_decode_m(cm, j, top & 0xFFFF);
-    b[j] = aw_decode_v(cv, j, top >> 16);
-  }
+  aw_decode(cm, cv, __builtin_amdgcn_readfirstlane(top), a, b);   // a wave is one block
   if constexpr (sizeof(T) == 4) {
     if (full) {
       aw_store<true>(m + i, 4, a);
@@ -389,19 +456,27 @@ __global__ __launch_bounds__(kAwThreads) void adamw_decode_kernel(
   }
 }
 
-static int64_t aw_tiles(int64_t n) { return (n + kAwTile - 1) / kAwTile; }
+// Elements of a tile: one chunk per wave; four with 8-bit states from 4 M elements on, where the
+// step is bound by its instructions and a tile's own (its tensor, the corrections) count.
+static int64_t aw_tile_elems(int32_t state_bits, int64_t elems) {
+  return (int64_t)kAwChunk * kAwWaves * (state_bits == 8 && elems >= kAwLongFrom ? kAwLong : 1);
+}
 
-// Host table check: UEP_OK and the number of tiles, or why not.
-static uep_status aw_count(const uep_adamw_tensor* t, int32_t count, int64_t* tiles) {
+// Host table check: UEP_OK with all elements and the tiles they make, or why not.
+static uep_status aw_count(const uep_adamw_tensor* t, int32_t count, int32_t state_bits,
+                           int64_t* tile, int64_t* tiles) {
   if (count < 0 || (count > 0 && !t)) return UEP_EINVAL;
   if (count > kAwMaxTensors) return UEP_EGEOM;
-  *tiles = 0;
+  int64_t elems = 0;
   for (int32_t q = 0; q < count; ++q) {
     if (t[q].n < 0) return UEP_EINVAL;
     if (t[q].n > kAwMaxElems) return UEP_EGEOM;
-    *tiles += aw_tiles(t[q].n);
+    elems += t[q].n;
   }
-  return *tiles < (1 << 24) ? UEP_OK : UEP_EGEOM;   // a launch holds below 2^32 threads
+  *tile = aw_tile_elems(state_bits, elems);
+  *tiles = 0;
+  for (int32_t q = 0; q < count; ++q) *tiles += (t[q].n + *tile - 1) / *tile;
+  return UEP_OK;
 }
 
 static size_t aw_bytes(int32_t count, int64_t tiles) {
@@ -413,17 +488,18 @@ static size_t aw_bytes(int32_t count, int64_t tiles) {
 using namespace uep;
 
 extern "C" size_t uep_adamw_plan_size(const uep_adamw_tensor* tensors_host, int32_t count) {
-  int64_t tiles = 0;
-  return aw_count(tensors_host, count, &tiles) == UEP_OK ? aw_bytes(count, tiles) : 0;
+  int64_t tile, tiles;                            // one chunk per wave: the most tiles
+  return aw_count(tensors_host, count, 32, &tile, &tiles) == UEP_OK ? aw_bytes(count, tiles) : 0;
 }
 
 extern "C" uep_status uep_adamw_prepare(const uep_adamw_tensor* tensors_host, int32_t count,
                                         int32_t param_dtype, int32_t grad_dtype,
                                         int32_t state_bits, void* plan, size_t plan_bytes,
                                         int64_t* n_tiles, void* stream) {
-  int64_t tiles = 0;
-  const uep_status st = aw_count(tensors_host, count, &tiles);
+  int64_t tile = 0, tiles = 0;
+  const uep_status st = aw_count(tensors_host, count, state_bits, &tile, &tiles);
   if (st != UEP_OK) return st;
+  if (tiles >= (1 << 24)) return UEP_EGEOM;         // a launch holds below 2^32 threads
   if ((param_dtype != UEP_F32 && param_dtype != UEP_BF16) ||
       (grad_dtype != UEP_F32 && grad_dtype != UEP_BF16) || (state_bits != 8 && state_bits != 32) ||
       !plan || !n_tiles)
@@ -454,8 +530,9 @@ extern "C" uep_status uep_adamw_prepare(const uep_adamw_tensor* tensors_host, in
   h->grad_dtype = grad_dtype;
   h->state_bits = state_bits;
   h->n_tiles = (int32_t)tiles;
+  h->unroll = (int32_t)(tile / (kAwChunk * kAwWaves));
   AwTensor* d = reinterpret_cast<AwTensor*>(w + sizeof(AwHeader));
-  int32_t* tile = reinterpret_cast<int32_t*>(d + count);
+  int32_t* tensor_of = reinterpret_cast<int32_t*>(d + count);
   int64_t at = 0;
   for (int32_t q = 0; q < count; ++q) {
     const uep_adamw_tensor& t = tensors_host[q];
@@ -464,7 +541,7 @@ extern "C" uep_status uep_adamw_prepare(const uep_adamw_tensor* tensors_host, in
     d[q].vec = (uintptr_t)t.param % (4 * p_size) == 0 && (uintptr_t)t.grad % (4 * g_size) == 0 &&
                (uintptr_t)t.m % (4 * s_size) == 0 && (uintptr_t)t.v % (4 * s_size) == 0 &&
                (uintptr_t)t.copy % 8 == 0;
-    for (int64_t k = aw_tiles(t.n); k > 0; --k) tile[at++] = q;
+    for (int64_t k = (t.n + tile - 1) / tile; k > 0; --k) tensor_of[at++] = q;
   }
   hipStream_t s = uep_stream(stream);
   hipError_t e = hipMemcpyAsync(plan, w, bytes, hipMemcpyHostToDevice, s);
