@@ -11,6 +11,7 @@ namespace uep {
 constexpr int kGtThreads = 256;
 constexpr int kGtTokPerBlock = kGtThreads / kWave;
 constexpr int kGtMaxE = 4096;
+constexpr int kGtSortE = 512;         // most experts of the kernel that sorts in registers
 // Up to this many tokens a call is bound by its latency and takes 16 lanes per token (the
 // shortest chain); above, by its instructions and takes as few lanes as hold the experts.
 constexpr int64_t kGtFew = 4096;
@@ -36,35 +37,29 @@ __device__ __forceinline__ bool gt_bad(float x) {
 __device__ __forceinline__ float gt_sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // The sigmoid as the selection uses it: exp2 and a refined reciprocal instead of the exact
-// division (5 instead of about 20 instructions for each of the E experts); within 4 units
-// of 2^-24 of the true value, like the exact one after its own roundings.  The exponent is
-// capped so that the refinement sees no infinity: scores below 2^-126 tie.
+// division (6 instead of about 20 instructions for each of the E experts); within 4 units
+// of 2^-24 of the true value, like the exact one after its own roundings.  Where exp2
+// overflows the refinement makes a NaN, which the median takes to 0.
 __device__ __forceinline__ float gt_rank_sigmoid(float x) {
-  const float d = 1.0f + __builtin_amdgcn_exp2f(fminf(-1.44269504f * x, 126.0f));
+  const float d = 1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x);
   const float r = __builtin_amdgcn_rcpf(d);
-  return fmaf(r, fmaf(-d, r, 1.0f), r);
+  return __builtin_amdgcn_fmed3f(fmaf(r, fmaf(-d, r, 1.0f), r), 0.0f, 1.0f);
 }
 
-// The fp32 bits in unsigned order (-0 as +0); 0 for an expert that is not eligible, which
-// no finite value maps to.
-__device__ __forceinline__ uint32_t gt_order(float f, bool able) {
-  const uint32_t u = __float_as_uint(f + 0.0f);
-  const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  return able ? o : 0u;
-}
-__device__ __forceinline__ float gt_unorder(uint32_t o) {
-  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
-}
+// Keys order by (rank, lowest id), rank an fp32 number that is finite, or -infinity for an
+// expert that is not eligible.  Key64: a double with the rank's bits above and the inverted id
+// below (its complement under a negative rank, where larger magnitudes are smaller), so that
+// one v_max_f64 / v_min_f64 compares both; 64-bit integers have no such instruction, a
+// compare and two selects.  The rank's exponent is never all of the double's, so no key is a
+// NaN.  Key32: bf16 logits leave the lower half of the word for the id; unsigned order.
+constexpr int kGtInv = 0xFFFF;                      // inverted id = kGtInv - id
+constexpr float kGtMasked = -__builtin_inff();
 
-// Keys order by (rank, lowest id).  Key64: the 32 ordered bits and the inverted id as the
-// mantissa of a double in [1, 2), so that one v_max_f64 / v_min_f64 compares both (64-bit
-// integers have no such instruction: a compare and two selects).  Key32: bf16 logits
-// leave the lower half of the word for the id.
 struct Key64 {
   typedef double type;
-  static __device__ __forceinline__ double make(uint32_t o, int inv_id) {
-    return __hiloint2double((int)__builtin_amdgcn_alignbit(0x3FFu, o, 12),
-                            (int)(o << 20 | (uint32_t)inv_id));
+  static __device__ __forceinline__ double make(float f, int inv_id) {
+    const int u = __float_as_int(f);
+    return __hiloint2double(u, inv_id ^ (u >> 31));
   }
   static __device__ __forceinline__ double hi(double a, double b) {
     double r;
@@ -76,10 +71,12 @@ struct Key64 {
     asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
     return r;
   }
-  static __device__ __forceinline__ uint32_t order(double k) {
-    return (uint32_t)__double2hiint(k) << 12 | (uint32_t)__double2loint(k) >> 20;
+  static __device__ __forceinline__ float rank(double k) {
+    return __int_as_float(__double2hiint(k));
   }
-  static __device__ __forceinline__ int inv_id(double k) { return __double2loint(k) & 0xFFFFF; }
+  static __device__ __forceinline__ int id(double k) {
+    return kGtInv - ((__double2loint(k) ^ (__double2hiint(k) >> 31)) & 0xFFFF);
+  }
   template <int kDpp>
   static __device__ __forceinline__ double moved(double k) {
     return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(k), kDpp, 0xF, 0xF, true),
@@ -88,31 +85,29 @@ struct Key64 {
 };
 struct Key32 {
   typedef uint32_t type;
-  static __device__ __forceinline__ uint32_t make(uint32_t o, int inv_id) {
+  static __device__ __forceinline__ uint32_t make(float f, int inv_id) {
+    const uint32_t u = __float_as_uint(f);
+    const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
     return (o & 0xFFFF0000u) | (uint32_t)inv_id;
   }
   static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max(a, b); }
   static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min(a, b); }
-  // the cut lower half: zeros of a positive value, ones of a negative one
-  static __device__ __forceinline__ uint32_t order(uint32_t k) {
-    return k & 0x80000000u ? k & 0xFFFF0000u : (k & 0xFFFF0000u ? k | 0xFFFFu : 0u);
+  static __device__ __forceinline__ float rank(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u ? k ^ 0x80000000u : ~k) & 0xFFFF0000u);
   }
-  static __device__ __forceinline__ int inv_id(uint32_t k) { return (int)(k & 0xFFFFu); }
+  static __device__ __forceinline__ int id(uint32_t k) { return kGtInv - (int)(k & 0xFFFFu); }
   template <int kDpp>
   static __device__ __forceinline__ uint32_t moved(uint32_t k) {
     return (uint32_t)__builtin_amdgcn_mov_dpp((int)k, kDpp, 0xF, 0xF, true);
   }
 };
-constexpr int kGtInv = 0xFFFF;                      // inverted id = kGtInv - id
 
 // ---------------------------------------------------------------------------------------
-// Few slots and experts: kL lanes per token, up to 32 experts per lane, a running list of
-// the kN >= K best.  Sorting networks on registers: every kN experts are sorted (Batcher's
+// Few slots and experts: kL lanes per token, kPer experts per lane, a running list of the
+// kN >= K best.  Sorting networks on registers: every kN experts are sorted (Batcher's
 // odd-even mergesort), merged into the list (the larger of list[i] and sorted[kN - 1 - i]
 // are the kN best and bitonic; a bitonic merge sorts them), and the kL lanes' lists are
 // merged the same way with DPP moves.
-constexpr int kGtPer = 32;
-
 template <typename KY, int kN>
 __device__ __forceinline__ void gt_order_pair(typename KY::type (&a)[kN], int i, int j) {
   const typename KY::type x = KY::hi(a[i], a[j]), y = KY::lo(a[i], a[j]);
@@ -161,31 +156,32 @@ __device__ __forceinline__ float gt_lanes_sum(float v) {
   return v;
 }
 
-// kCe consecutive values from p[e0], `fill` from p[E] on; vec: all or none are there, aligned.
-template <int kCe, typename T>
-__device__ __forceinline__ void gt_chunk(const T* p, int e0, int E, bool vec, float fill,
-                                         float (&v)[kCe]) {
+// 16 bytes of a row of E elements from element e0 on, -infinity past its end; vec: all or none
+// are there, and aligned.
+template <typename T>
+__device__ __forceinline__ u32x4 gt_load16(const T* p, int e0, int E, bool vec) {
+  constexpr uint32_t kFill = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+  u32x4 w = {kFill, kFill, kFill, kFill};
   if (vec) {
-#pragma unroll
-    for (int j = 0; j < kCe; ++j) v[j] = fill;
-    if (e0 < E) {
-      constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-      for (int h = 0; h < kCe / kPer; ++h) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(p + e0 + h * kPer);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          v[h * kPer + j] = sizeof(T) == 4 ? __uint_as_float(w[j & 3])
-                            : j & 1        ? bf16_hi(w[j / 2 & 3]) : bf16_lo(w[j / 2 & 3]);
-      }
-    }
+    if (e0 < E) w = *reinterpret_cast<const u32x4*>(p + e0);
   } else {
 #pragma unroll
-    for (int j = 0; j < kCe; ++j) v[j] = e0 + j < E ? gt_load(p, e0 + j) : fill;
+    for (int j = 0; j < 16 / (int)sizeof(T); ++j)
+      if (e0 + j < E) {
+        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(p[e0 + j]);
+        else w[j / 2] = j & 1 ? (w[j / 2] & 0xFFFFu) | (uint32_t)p[e0 + j] << 16
+                              : (w[j / 2] & 0xFFFF0000u) | p[e0 + j];
+      }
   }
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ float gt_element(u32x4 w, int j) {
+  if (sizeof(T) == 4) return __uint_as_float(w[j & 3]);
+  return j & 1 ? bf16_hi(w[j / 2 & 3]) : bf16_lo(w[j / 2 & 3]);
 }
 
-template <typename T, typename KY, bool kSigmoid, int kL, int kN>
+template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
 __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
     const int32_t* __restrict__ batch_size, int64_t n_tok, int tok_per_rank, int E, int K,
@@ -193,47 +189,72 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     float* __restrict__ gate_w, int32_t* err) {
   typedef typename KY::type key_t;
   constexpr int kCe = 16 / sizeof(T);                 // experts of one 16-byte load
-  constexpr int kChunks = kGtPer / kCe;
+  constexpr int kChunks = kPer / kCe;
   const int lane = threadIdx.x % kL;
   const int64_t g = (int64_t)blockIdx.x * (kGtThreads / kL) + threadIdx.x / kL;
   bool live = g < n_tok;
   if (live && batch_size) live = (int)(g % tok_per_rank) < batch_size[g / tok_per_rank];
   const T* row = logits + (live ? g : 0) * (int64_t)E;
-  const int e_end = live ? E : 0;
-  float x[kChunks][kCe];
+  u32x4 raw[kChunks];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-#pragma unroll
-    for (int j = 0; j < kCe; ++j) x[c][j] = -__builtin_inff();
-    if (c * kL * kCe < E)                             // uniform: some lane has such experts
-      gt_chunk<kCe>(row, (c * kL + lane) * kCe, e_end, vec, -__builtin_inff(), x[c]);
-  }
-  float y[kChunks][kCe];                              // what the selection ranks by
-#pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    if (kSigmoid && bias && c * kL * kCe < E)
-      gt_chunk<kCe>(bias, (c * kL + lane) * kCe, E, vec_bias, 0.0f, y[c]);
-    else
-#pragma unroll
-      for (int j = 0; j < kCe; ++j) y[c][j] = 0.0f;
+  for (int c = 0; c < kChunks; ++c)                   // the first is never skipped
+    raw[c] = gt_load16(row, (c * kL + lane) * kCe, live ? E : 0, vec);
+  bool bad = false, odd_bias = false;
+  if (kSigmoid && bias) {                             // each lane of the wave a few of them
+    for (int e = threadIdx.x % kWave; e < E; e += kWave) bad |= gt_bad(bias[e]);
+    odd_bias = ballot(bad) != 0;
   }
   key_t best[kN];
-  bool odd = false;                                   // something that is not finite
 #pragma unroll
-  for (int q = 0; q < kGtPer / kN; ++q) {
-    if (q > 0 && q * kN / kCe * kCe * kL >= E) break; // uniform
+  for (int q = 0; q < kPer / kN; ++q) {
+    if (q > 0 && q * kN / kCe * kCe * kL >= E) break; // uniform: no lane has such experts
+    float f[kN];
+    bool odd = odd_bias;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int n = q * kN + i;
+      f[i] = gt_element<T>(raw[n / kCe], n % kCe);
+      // softmax: NaN and +infinity (bits 0, 1, 9); -infinity is ranked as it is
+      odd |= kSigmoid ? !gt_finite(f[i]) : __builtin_amdgcn_classf(f[i], 0x203);
+    }
+    if (kSigmoid) {
+      float y[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) y[i] = 0.0f;
+      if (bias) {
+#pragma unroll
+        for (int h = 0; h < kN; h += 4) {
+          const int n = q * kN + h, e = (n / kCe * kL + lane) * kCe + n % kCe;
+          const u32x4 w = gt_load16(bias, e, E, vec_bias);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[h + j] = __uint_as_float(w[j]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) y[i] += gt_rank_sigmoid(f[i]);
+      if (ballot(odd))
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          bad |= gt_bad(f[i]);
+          if (!gt_finite(f[i]) || !gt_finite(y[i])) y[i] = kGtMasked;
+        }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) f[i] = y[i];
+    } else {
+      if (ballot(odd))
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          bad |= gt_bad(f[i]);
+          if (!gt_finite(f[i])) f[i] = kGtMasked;
+        }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) f[i] += 0.0f;      // -0 ties with +0
+    }
     key_t a[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int n = q * kN + i, e = (n / kCe * kL + lane) * kCe + n % kCe;
-      float f = x[n / kCe][n % kCe];
-      bool able = gt_finite(f);
-      if (kSigmoid) {
-        f = gt_rank_sigmoid(f) + y[n / kCe][n % kCe];
-        able &= gt_finite(f);
-      }
-      odd |= !able;
-      a[i] = KY::make(gt_order(f, able), kGtInv - e);
+      const int n = q * kN + i;
+      a[i] = KY::make(f[i], kGtInv - ((n / kCe * kL + lane) * kCe + n % kCe));
     }
     gt_sort<KY>(a);
     if (q == 0) {
@@ -243,22 +264,14 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
       gt_merge<KY>(best, a);
     }
   }
-  if (ballot(odd)) {                                  // find out whether it was a mask
-    bool bad = false;
-#pragma unroll
-    for (int n = 0; n < kGtPer; ++n) bad |= gt_bad(x[n / kCe][n % kCe]);
-    if (kSigmoid && bias)                             // a score plus a finite bias is finite
-      for (int e = threadIdx.x % kWave; e < E; e += kWave) bad |= gt_bad(bias[e]);
-    if (ballot(bad) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_LOGIT);
-  }
+  if (ballot(bad) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_LOGIT);
   gt_merge_lanes<KY, 0xB1>(best);                     // xor 1
   gt_merge_lanes<KY, 0x4E>(best);                     // xor 2
   if (kL >= 8) gt_merge_lanes<KY, 0x141>(best);       // the other half of 8 (row_half_mirror)
   if (kL >= 16) gt_merge_lanes<KY, 0x140>(best);      // the other half of 16 (row_mirror)
 
   constexpr int kSlots = kN > kL ? kN / kL : 1;       // a lane's slots, consecutive
-  const uint32_t top_o = KY::order(best[0]);
-  const float top = top_o ? gt_unorder(top_o) : 0.0f; // softmax: the largest logit
+  const float top = KY::rank(best[0]);                // softmax: the largest logit
   int id[kSlots];
   float s[kSlots], mine = 0.0f;
 #pragma unroll
@@ -267,11 +280,11 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
 #pragma unroll
     for (int l = 1; l < kL && l * kSlots + i < kN; ++l)
       if (lane == l) k = best[l * kSlots + i];
-    const uint32_t o = KY::order(k);
-    const bool on = o != 0u && lane * kSlots + i < K;
-    id[i] = on ? kGtInv - KY::inv_id(k) : -1;
+    const float f = KY::rank(k);
+    const bool on = f > kGtMasked && lane * kSlots + i < K;
+    id[i] = on ? KY::id(k) : -1;
     s[i] = 0.0f;
-    if (on) s[i] = kSigmoid ? gt_sigmoid(gt_load(row, id[i])) : expf(gt_unorder(o) - top);
+    if (on) s[i] = kSigmoid ? gt_sigmoid(gt_load(row, id[i])) : expf(f - top);
     mine += s[i];
   }
   float total = 1.0f;
@@ -280,8 +293,8 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
   } else if (!kSigmoid) {
     float z = 0.0f;
 #pragma unroll
-    for (int n = 0; n < kGtPer; ++n) {
-      const float f = x[n / kCe][n % kCe];
+    for (int n = 0; n < kPer; ++n) {
+      const float f = gt_element<T>(raw[n / kCe], n % kCe);
       z += gt_finite(f) ? __builtin_amdgcn_exp2f(1.44269504f * (f - top)) : 0.0f;
     }
     total = gt_lanes_sum<kL>(z);
@@ -326,7 +339,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     }
     return;
   }
-  const double none = Key64::make(0u, 0);
+  const double none = Key64::make(kGtMasked, 0);
   double key[kVpt];
   float val[kVpt];
   bool bad = false;
@@ -336,12 +349,12 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     const float x = e < E ? gt_load(logits, g * E + e) : -__builtin_inff();
     val[j] = x;
     bad |= gt_bad(x);
-    float f = x;
+    float f = x + 0.0f;
     if (score && gt_finite(x)) {
       f = gt_rank_sigmoid(x) + (bias ? bias[e] : 0.0f);
       bad |= gt_bad(f);
     }
-    key[j] = gt_finite(f) ? Key64::make(gt_order(f, true), kGtInv - e) : none;
+    key[j] = gt_finite(f) ? Key64::make(f, kGtInv - e) : none;
   }
   if (ballot(bad) && lane == 0) set_err(err, UEP_ERR_LOGIT);
   int id_mine = -1;
@@ -354,8 +367,8 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     if (m == none) break;
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) key[j] = key[j] == m ? none : key[j];
-    if (k == 0) top = gt_unorder(Key64::order(m));    // softmax: the largest logit
-    if (lane == k) id_mine = kGtInv - Key64::inv_id(m);
+    if (k == 0) top = Key64::rank(m);                 // softmax: the largest logit
+    if (lane == k) id_mine = Key64::id(m);
   }
   const bool on = id_mine >= 0;
   const float l = on ? gt_load(logits, g * E + id_mine) : 0.0f;
@@ -491,7 +504,9 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
           const f32x4 q = par[row];
           float x[kCe];
           if (vec) {
-            gt_chunk<kCe>(src, at, INT32_MAX, true, 0.0f, x);
+            const u32x4 w = *reinterpret_cast<const u32x4*>(src + at);
+#pragma unroll
+            for (int j = 0; j < kCe; ++j) x[j] = gt_element<T>(w, j);
           } else {
             x[0] = gt_load(src, at);
           }
@@ -543,14 +558,13 @@ static bool gt_blocks(int64_t n_tok, int per, unsigned* blocks) {
   return n < (1ll << 32) / kGtThreads;
 }
 
-template <typename T, typename KY, bool kSigmoid, int kL, int kN>
+template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
 static uep_status gt_sorted(const GtCall& c) {
   unsigned blocks;
   if (!gt_blocks(c.n_tok, kGtThreads / kL, &blocks)) return UEP_EGEOM;
   const int vec = (reinterpret_cast<uintptr_t>(c.logits) | (uintptr_t)c.E * sizeof(T)) % 16 == 0;
-  const int vec_bias = (reinterpret_cast<uintptr_t>(c.bias) | (uintptr_t)c.E * 4) % 16 == 0 &&
-                       c.E % (16 / (int)sizeof(T)) == 0;
-  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kSigmoid, kL, kN>), dim3(blocks), dim3(kGtThreads),
+  const int vec_bias = (reinterpret_cast<uintptr_t>(c.bias) | (uintptr_t)c.E * 4) % 16 == 0;
+  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kSigmoid, kL, kN, kPer>), dim3(blocks), dim3(kGtThreads),
                      0, c.stream, static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok,
                      c.T, c.E, c.K, c.renorm, c.scale, vec, vec_bias, c.topk_ids, c.gate_w, c.err);
   UEP_CHECK_LAUNCH();
@@ -568,23 +582,24 @@ static uep_status gt_general(const GtCall& c) {
   return UEP_OK;
 }
 
-template <typename T, typename KY, bool kSigmoid, int kL>
+template <typename T, typename KY, bool kSigmoid, int kL, int kPer>
 static uep_status gt_by_slots(const GtCall& c) {
-  return c.K <= 4   ? gt_sorted<T, KY, kSigmoid, kL, 4>(c)
-         : c.K <= 8 ? gt_sorted<T, KY, kSigmoid, kL, 8>(c)
-                    : gt_sorted<T, KY, kSigmoid, kL, 16>(c);
+  return c.K <= 4   ? gt_sorted<T, KY, kSigmoid, kL, 4, kPer>(c)
+         : c.K <= 8 ? gt_sorted<T, KY, kSigmoid, kL, 8, kPer>(c)
+                    : gt_sorted<T, KY, kSigmoid, kL, 16, kPer>(c);
 }
 
 template <typename T, typename KY, bool kSigmoid>
 static uep_status gt_by_experts(const GtCall& c) {
-  if (c.E <= 4 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, kSigmoid, 4>(c);
-  if (c.E <= 8 * kGtPer && c.n_tok > kGtFew) return gt_by_slots<T, KY, kSigmoid, 8>(c);
-  return gt_by_slots<T, KY, kSigmoid, 16>(c);
+  if (c.n_tok <= kGtFew) return gt_by_slots<T, KY, kSigmoid, 16, 32>(c);
+  if (c.E <= 4 * 32) return gt_by_slots<T, KY, kSigmoid, 4, 32>(c);
+  if (c.E <= 4 * 64) return gt_by_slots<T, KY, kSigmoid, 4, 64>(c);
+  return gt_by_slots<T, KY, kSigmoid, 8, 64>(c);
 }
 
 template <typename T>
 static uep_status gt_launch(const GtCall& c) {
-  if (c.K <= 16 && c.E <= 16 * kGtPer) {
+  if (c.K <= 16 && c.E <= kGtSortE) {
     if (c.score == UEP_GATE_SIGMOID) return gt_by_experts<T, Key64, true>(c);
     if (sizeof(T) == 2) return gt_by_experts<T, Key32, false>(c);
     return gt_by_experts<T, Key64, false>(c);

@@ -116,8 +116,15 @@ def _p(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without a Stream object around it, which costs 3 us a call: a
+# third of what a small call takes.
+_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _RAW_STREAM is not None:
+            return ctypes.c_void_p(_RAW_STREAM(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
