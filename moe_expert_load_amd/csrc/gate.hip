@@ -34,16 +34,18 @@ __device__ __forceinline__ bool gt_bad(float x) {
   return !gt_finite(x) && __float_as_uint(x) != 0xFF800000u;
 }
 
-__device__ __forceinline__ float gt_sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// exp(x) for x <= 0 in units of 2^-24: the argument, rounded twice, is 2 |x| off, exp2 two more.
+__device__ __forceinline__ float gt_exp(float x) {
+  return __builtin_amdgcn_exp2f(1.44269504f * x);
+}
 
-// The sigmoid as the selection uses it: exp2 and a refined reciprocal instead of the exact
-// division (6 instead of about 20 instructions for each of the E experts); within 4 units
-// of 2^-24 of the true value, like the exact one after its own roundings.  Where exp2
-// overflows the refinement makes a NaN, which the median takes to 0.
-__device__ __forceinline__ float gt_rank_sigmoid(float x) {
-  const float d = 1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x);
-  const float r = __builtin_amdgcn_rcpf(d);
-  return __builtin_amdgcn_fmed3f(fmaf(r, fmaf(-d, r, 1.0f), r), 0.0f, 1.0f);
+// Sigmoid by exp2 and the hardware's reciprocal instead of an exact division (4 instead of about
+// 20 instructions for each of the E experts).  In units of 2^-24: the exponential's
+// argument, rounded once, is |x| off and exp2 two more, together at most
+// s (1 - s)(|x| + 2) < 0.8 of the score; 1 + e is rounded once and the reciprocal within 1.6:
+// under 4 in all.
+__device__ __forceinline__ float gt_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }
 
 // Keys order by (rank, lowest id), rank an fp32 number that is finite, or -infinity for an
@@ -57,9 +59,13 @@ constexpr float kGtMasked = -__builtin_inff();
 
 struct Key64 {
   typedef double type;
-  static __device__ __forceinline__ double make(float f, int inv_id) {
-    const int u = __float_as_int(f);
-    return __hiloint2double(u, inv_id ^ (u >> 31));
+  // of expert e ^ f; inv = kGtInv ^ f is a constant, kept in a scalar register so that one
+  // three-way xor makes the lower word
+  static __device__ __forceinline__ double make(float rank, int inv, int e) {
+    const int u = __float_as_int(rank);
+    int low;
+    asm("v_bitop3_b32 %0, %1, %2, %3 bitop3:0x96" : "=v"(low) : "v"(u >> 31), "s"(inv), "v"(e));
+    return __hiloint2double(u, low);
   }
   static __device__ __forceinline__ double hi(double a, double b) {
     double r;
@@ -85,10 +91,10 @@ struct Key64 {
 };
 struct Key32 {
   typedef uint32_t type;
-  static __device__ __forceinline__ uint32_t make(float f, int inv_id) {
-    const uint32_t u = __float_as_uint(f);
+  static __device__ __forceinline__ uint32_t make(float rank, int inv, int e) {
+    const uint32_t u = __float_as_uint(rank);
     const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-    return (o & 0xFFFF0000u) | (uint32_t)inv_id;
+    return (o & 0xFFFF0000u) | (uint32_t)(inv ^ e);
   }
   static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return max(a, b); }
   static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return min(a, b); }
@@ -200,9 +206,9 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
   for (int c = 0; c < kChunks; ++c)                   // the first is never skipped
     raw[c] = gt_load16(row, (c * kL + lane) * kCe, live ? E : 0, vec);
   bool bad = false, odd_bias = false;
-  if (kSigmoid && bias) {                             // each lane of the wave a few of them
-    for (int e = threadIdx.x % kWave; e < E; e += kWave) bad |= gt_bad(bias[e]);
-    odd_bias = ballot(bad) != 0;
+  if (kSigmoid && bias) {                             // each thread a few of them
+    for (int e = threadIdx.x; e < E; e += kGtThreads) bad |= gt_bad(bias[e]);
+    odd_bias = __syncthreads_or(bad);
   }
   key_t best[kN];
 #pragma unroll
@@ -231,7 +237,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
         }
       }
 #pragma unroll
-      for (int i = 0; i < kN; ++i) y[i] += gt_rank_sigmoid(f[i]);
+      for (int i = 0; i < kN; ++i) y[i] += gt_sigmoid(f[i]);
       if (ballot(odd))
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
@@ -253,8 +259,9 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     key_t a[kN];
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
+      // the expert is n / kCe * kL * kCe + lane * kCe + n % kCe, three separate bit fields
       const int n = q * kN + i;
-      a[i] = KY::make(f[i], kGtInv - ((n / kCe * kL + lane) * kCe + n % kCe));
+      a[i] = KY::make(f[i], kGtInv ^ (n / kCe * kL * kCe + n % kCe), lane * kCe);
     }
     gt_sort<KY>(a);
     if (q == 0) {
@@ -284,7 +291,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const bool on = f > kGtMasked && lane * kSlots + i < K;
     id[i] = on ? KY::id(k) : -1;
     s[i] = 0.0f;
-    if (on) s[i] = kSigmoid ? gt_sigmoid(gt_load(row, id[i])) : expf(f - top);
+    if (on) s[i] = kSigmoid ? gt_sigmoid(gt_load(row, id[i])) : gt_exp(f - top);
     mine += s[i];
   }
   float total = 1.0f;
@@ -295,16 +302,17 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
 #pragma unroll
     for (int n = 0; n < kPer; ++n) {
       const float f = gt_element<T>(raw[n / kCe], n % kCe);
-      z += gt_finite(f) ? __builtin_amdgcn_exp2f(1.44269504f * (f - top)) : 0.0f;
+      z += gt_finite(f) ? gt_exp(f - top) : 0.0f;
     }
     total = gt_lanes_sum<kL>(z);
   }
+  const float norm = total > 0.0f ? scale / total : 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int k = lane * kSlots + i;
     if (g < n_tok && k < K) {
       topk_ids[g * K + k] = id[i];
-      gate_w[g * K + k] = s[i] > 0.0f ? scale * (s[i] / total) : 0.0f;
+      gate_w[g * K + k] = s[i] * norm;
     }
   }
 }
@@ -339,7 +347,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     }
     return;
   }
-  const double none = Key64::make(kGtMasked, 0);
+  const double none = Key64::make(kGtMasked, 0, 0);
   double key[kVpt];
   float val[kVpt];
   bool bad = false;
@@ -351,10 +359,10 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     bad |= gt_bad(x);
     float f = x + 0.0f;
     if (score && gt_finite(x)) {
-      f = gt_rank_sigmoid(x) + (bias ? bias[e] : 0.0f);
+      f = gt_sigmoid(x) + (bias ? bias[e] : 0.0f);
       bad |= gt_bad(f);
     }
-    key[j] = gt_finite(f) ? Key64::make(f, kGtInv - e) : none;
+    key[j] = gt_finite(f) ? Key64::make(f, kGtInv, e) : none;
   }
   if (ballot(bad) && lane == 0) set_err(err, UEP_ERR_LOGIT);
   int id_mine = -1;
@@ -372,19 +380,19 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
   }
   const bool on = id_mine >= 0;
   const float l = on ? gt_load(logits, g * E + id_mine) : 0.0f;
-  const float s = on ? (score ? gt_sigmoid(l) : expf(l - top)) : 0.0f;
+  const float s = on ? (score ? gt_sigmoid(l) : gt_exp(l - top)) : 0.0f;
   float total = 1.0f;
   if (renorm) {
     total = gt_wave_sum(s);
   } else if (!score) {
     float z = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kVpt; ++j) z += gt_finite(val[j]) ? expf(val[j] - top) : 0.0f;
+    for (int j = 0; j < kVpt; ++j) z += gt_finite(val[j]) ? gt_exp(val[j] - top) : 0.0f;
     total = gt_wave_sum(z);
   }
   if (lane < K) {
     topk_ids[g * K + lane] = id_mine;
-    gate_w[g * K + lane] = s > 0.0f ? scale * (s / total) : 0.0f;
+    gate_w[g * K + lane] = total > 0.0f ? s * (scale / total) : 0.0f;
   }
 }
 
@@ -462,7 +470,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
         for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
         for (int e = lane; e < E; e += kWave) {
           const float x = gt_load(logits, gr * E + e);
-          if (gt_finite(x)) z += expf(x - m);
+          if (gt_finite(x)) z += gt_exp(x - m);
         }
         z = gt_wave_sum(z);
         if (tok == at >> lg_kp) {
@@ -472,7 +480,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
       }
       if (k == 0) par[tok] = f32x4{lr, fmaxf(ur, 0.0f), dot, 0.0f};
     } else if (score) {
-      d = renorm ? u * (1.0f - gt_sigmoid(l)) * (gk - dot) : u * (1.0f - u) * gk;
+      d = renorm ? u * gt_sigmoid(-l) * (gk - dot) : u * (1.0f - u) * gk;
     } else {
       d = u * (gk - dot);
     }
@@ -513,7 +521,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
 #pragma unroll
           for (int j = 0; j < kCe; ++j) {
             if (!vec && j > 0) break;
-            const float s = q[1] * __builtin_amdgcn_exp2f(1.44269504f * (x[j] - q[0]));
+            const float s = q[1] * gt_exp(x[j] - q[0]);
             v[j] = gt_finite(x[j]) ? s * (v[j] - q[2]) : 0.0f;
           }
         }
