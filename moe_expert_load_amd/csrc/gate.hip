@@ -321,16 +321,17 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
 // Any size: one wave per token, kVpt experts per lane (expert j * 64 + lane); K rounds of a
 // wave maximum over the keys left.
 __device__ __forceinline__ double gt_wave_max(double v) {
+  v = Key64::hi(v, Key64::moved<0xB1>(v));            // xor 1, xor 2, mirrored halves and rows
+  v = Key64::hi(v, Key64::moved<0x4E>(v));
+  v = Key64::hi(v, Key64::moved<0x141>(v));
+  v = Key64::hi(v, Key64::moved<0x140>(v));
+  double r[4];
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = Key64::hi(v, __shfl_xor(v, o, kWave));
-  return v;
+  for (int i = 0; i < 4; ++i)
+    r[i] = __hiloint2double(readlane(__double2hiint(v), 16 * i),
+                            readlane(__double2loint(v), 16 * i));
+  return Key64::hi(Key64::hi(r[0], r[1]), Key64::hi(r[2], r[3]));
 }
-__device__ __forceinline__ float gt_wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
-}
-
 template <typename T, int kVpt>
 __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
@@ -383,12 +384,12 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
   const float s = on ? (score ? gt_sigmoid(l) : gt_exp(l - top)) : 0.0f;
   float total = 1.0f;
   if (renorm) {
-    total = gt_wave_sum(s);
+    total = wave_sum_f32(s);
   } else if (!score) {
     float z = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) z += gt_finite(val[j]) ? gt_exp(val[j] - top) : 0.0f;
-    total = gt_wave_sum(z);
+    total = wave_sum_f32(z);
   }
   if (lane < K) {
     topk_ids[g * K + lane] = id_mine;
@@ -472,7 +473,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
           const float x = gt_load(logits, gr * E + e);
           if (gt_finite(x)) z += gt_exp(x - m);
         }
-        z = gt_wave_sum(z);
+        z = wave_sum_f32(z);
         if (tok == at >> lg_kp) {
           ur = 1.0f / z;
           lr = m;
