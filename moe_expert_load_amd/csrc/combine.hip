@@ -25,12 +25,15 @@ namespace uep {
 constexpr int kCbThreads = 256;
 constexpr int kCbTokPerBlock = kCbThreads / kWave;
 constexpr int kCbVec = 4;     // 16-byte vectors per lane per slice (8 bf16 each)
-constexpr int kCbGroup = 4;   // rows loaded together
 // Up to this many tokens, which leave SIMDs without a wave, a token's slices go to up to 16
-// waves instead of one after the other to one.
+// waves instead of one after the other to one (1 token, K = 9, 14 KiB rows: 16.7 -> 6.2 us; 512
+// tokens 26.1 -> 13.9).
 constexpr int64_t kCbFew = 512;
 
-template <bool kWeighted>
+// kVec vectors per lane hold a slice of a row (a whole row where it is shorter than a slice of
+// kCbVec); 4 rows go together, 8 short ones (65536 tokens of eight 512 B rows: 120 -> 53 us
+// against four vectors whatever the row).
+template <bool kWeighted, int kVec>
 __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __restrict__ y_disp,
                                                              const int32_t* __restrict__ dest_row,
                                                              const float* __restrict__ gate_w,
@@ -39,6 +42,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
                                                              int64_t g1, int K, int nvec,
                                                              int parts, int32_t* err) {
 #pragma clang fp contract(off)
+  constexpr int kGroup = kVec == kCbVec ? 4 : 8;
   const int lane = threadIdx.x % kWave;
   const int64_t b = xcd_block(blockIdx.x, gridDim.x);
   // the wave's token, uniform (readfirstlane), so the row spans below live in SGPRs
@@ -48,31 +52,31 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
   if (g >= g1) return;
   const int d_mine = checked_row(lane < K ? dest_row[g * K + lane] : -1, out_rows, err);
   const int w_mine = kWeighted && lane < K ? __float_as_int(gate_w[g * K + lane]) : 0;
-  for (int v0 = part * kCbVec * kWave; v0 < nvec; v0 += parts * kCbVec * kWave) {
-    float acc[kCbVec * 8];
+  for (int v0 = part * kVec * kWave; v0 < nvec; v0 += parts * kVec * kWave) {
+    float acc[kVec * 8];
 #pragma unroll
-    for (int i = 0; i < kCbVec * 8; ++i) acc[i] = 0.0f;
-    for (int k0 = 0; k0 < K; k0 += kCbGroup) {
-      int dq[kCbGroup];
-      float wq[kCbGroup];
-      u32x4 buf[kCbGroup][kCbVec];
+    for (int i = 0; i < kVec * 8; ++i) acc[i] = 0.0f;
+    for (int k0 = 0; k0 < K; k0 += kGroup) {
+      int dq[kGroup];
+      float wq[kGroup];
+      u32x4 buf[kGroup][kVec];
 #pragma unroll
-      for (int q = 0; q < kCbGroup; ++q) {
+      for (int q = 0; q < kGroup; ++q) {
         const int k = k0 + q;
         dq[q] = k < K ? readlane(d_mine, k) : -1;
         wq[q] = k < K ? __int_as_float(readlane(w_mine, k)) : 0.0f;
         if (dq[q] >= 0) {          // a span per row: vectors past its end read as zero
           const span_t src = span_of(y_disp + (int64_t)dq[q] * nvec, (int64_t)nvec * 16);
 #pragma unroll
-          for (int u = 0; u < kCbVec; ++u) buf[q][u] = stream_load(src, (v0 + u * kWave + lane) * 16);
+          for (int u = 0; u < kVec; ++u) buf[q][u] = stream_load(src, (v0 + u * kWave + lane) * 16);
         }
       }
 #pragma unroll
-      for (int q = 0; q < kCbGroup; ++q) {
+      for (int q = 0; q < kGroup; ++q) {
         if (dq[q] < 0) continue;
         const float w = wq[q];
 #pragma unroll
-        for (int u = 0; u < kCbVec; ++u) {
+        for (int u = 0; u < kVec; ++u) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float p0 = kWeighted ? w * bf16_lo(buf[q][u][c]) : bf16_lo(buf[q][u][c]);
@@ -85,7 +89,7 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
     }
     const span_t dst = span_of(y + g * nvec, (int64_t)nvec * 16);
 #pragma unroll
-    for (int u = 0; u < kCbVec; ++u) {           // past the row's end: not written
+    for (int u = 0; u < kVec; ++u) {           // past the row's end: not written
       u32x4 o;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -112,7 +116,11 @@ static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_
   const int slices = (H / 8 + kCbVec * kWave - 1) / (kCbVec * kWave);
   const int parts = g1 - g0 <= kCbFew ? std::min(slices, 16) : 1;
   const int64_t blocks = ((g1 - g0) * parts + kCbTokPerBlock - 1) / kCbTokPerBlock;
-  auto kernel = weighted ? combine_kernel<true> : combine_kernel<false>;
+  const int nv = (H / 8 + kWave - 1) / kWave;       // vectors per lane of a row
+  auto kernel = weighted ? (nv <= 1   ? combine_kernel<true, 1>
+                            : nv <= 2 ? combine_kernel<true, 2> : combine_kernel<true, kCbVec>)
+                         : (nv <= 1   ? combine_kernel<false, 1>
+                            : nv <= 2 ? combine_kernel<false, 2> : combine_kernel<false, kCbVec>);
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kCbThreads), 0, uep_stream(stream),
                      reinterpret_cast<const u32x4*>(rows), dest_row, gate_w,
                      reinterpret_cast<u32x4*>(y), out_rows, g0, g1, K, H / 8, parts,

@@ -4,27 +4,48 @@
 //   dout[d] = bf16(w[g][k] * dy[g]),   dgate_w[g][k] = <dy[g], out[d]>,   d = dest_row[g][k].
 //
 // One wave per token on the XCD-aware block map, as in the combine: the token's gradient
-// is read once into registers, slice by slice (8 x 16 B per lane, 8 KiB per wave), and
-// serves its K rows; lanes 0..K-1 hold rows, weights and the running dot products.  Row k
-// of `out` is read before row k of dout is written, by the same wave, so that both may be
-// one buffer.
+// is read once into registers, slice by slice, and serves its K rows; lanes 0..K-1 hold
+// rows, weights and the running dot products, and the next slots' rows of `out` are on
+// their way while one group is used.  A row of `out` is read before the same row of dout
+// is written, by the same wave, so that both may be one buffer.
+//
+// Two phases.  HBM takes a stream of reads and a stream of writes faster one after the
+// other than mixed, and the two halves of this operator share only dy.  From kRgPhaseBytes of
+// dispatch rows on, the dot products (reads alone) and the scaled rows (writes alone) are
+// therefore launches of their own, over chunks of tokens whose dy stays in the 256 MB
+// last-level cache from the first to the second.  Measured on MI355X (two launches per chunk
+// against one for both): 65536 tokens, K = 8, 8 KiB rows 1760 -> 1503 us (6.08 TB/s of the
+// bytes that have to move; a large copy reaches 5.65), chunks of 16 / 64 / 128 / 224 MB of
+// dy / all in one 1692 / 1561 / 1519 / 1503 / 1570 us; 32 MB of rows 16.6 -> 16.0 us
+// (1 KiB rows) and 16.1 -> 16.9 (4 KiB), 64 MB 32.4 -> 29.3 (512 B), 29.9 -> 27.6 (8 KiB).
+//
+// Short rows: with vectors for 8 KiB per wave whatever the row, 65536 tokens of eight 512 B
+// rows took 293 us; with a row's own vectors and kRgVec of them in flight 116 (one launch).
+#include <algorithm>
+
 #include "common.h"
 
 namespace uep {
 
 constexpr int kRgThreads = 256;
 constexpr int kRgTokPerBlock = kRgThreads / kWave;
-constexpr int kRgVec = 8;     // 16-byte vectors per lane per slice
+constexpr int kRgVec = 8;     // 16-byte vectors in flight per lane for each of the two row groups
 // Up to this many tokens, which leave SIMDs without a wave, a token's slots go to a wave each
-// instead of one after the other to one.
+// instead of one after the other to one (1 token, K = 8, 8 KiB rows: 22.7 -> 4.7 us; 512
+// tokens 27.2 -> 17.1).
 constexpr int64_t kRgFew = 512;
+constexpr int64_t kRgPhaseBytes = 48ll << 20;
+constexpr int64_t kRgChunkBytes = 224ll << 20;
 
-// Rows of slot k: the vectors of [v0, v0 + kRgVec * kWave) of `base`'s row d, none if d < 0.
+// Row d of `base`, an empty span if d < 0: its loads read zeros, its stores go nowhere.
 __device__ __forceinline__ span_t rg_row(const u32x4* base, int d, int nvec) {
   return span_of(base + (int64_t)max(d, 0) * nvec, d < 0 ? 0 : (int64_t)nvec * 16);
 }
 
-template <bool kDot>
+// kDot: the dot products (dout is not touched unless kScale); kScale: the scaled rows.
+// kVec vectors per lane hold a slice of a row (a whole row where it is shorter than a slice of
+// kRgVec), kRgVec / kVec slots go together.
+template <bool kDot, bool kScale, int kVec>
 __global__ __launch_bounds__(kRgThreads) void combine_grad_kernel(
     const u32x4* __restrict__ dy, const u32x4* out, const int32_t* __restrict__ dest_row,
     const float* __restrict__ gate_w, u32x4* dout, float* __restrict__ dgate_w, int64_t out_rows,
@@ -40,51 +61,75 @@ __global__ __launch_bounds__(kRgThreads) void combine_grad_kernel(
   const int w_mine = mine ? __float_as_int(gate_w[g * K + lane]) : 0;
   const span_t src = span_of(dy + g * nvec, (int64_t)nvec * 16);
   float dot_mine = 0.0f;
-  for (int v0 = 0; v0 < nvec; v0 += kRgVec * kWave) {
-    u32x4 grad[kRgVec], y[2][kRgVec];
-    auto fetch = [&](int k, u32x4 (&to)[kRgVec]) {
-      const span_t row = rg_row(out, readlane(d_mine, k), nvec);
+  constexpr int kG = kRgVec / kVec;
+  for (int v0 = 0; v0 < nvec; v0 += kVec * kWave) {
+    u32x4 grad[kVec], y[2][kG][kVec];
+    auto row_of = [&](int k) { return k < k_end ? readlane(d_mine, k) : -1; };
+    auto fetch = [&](int k0, u32x4 (&to)[kG][kVec]) {
 #pragma unroll
-      for (int u = 0; u < kRgVec; ++u) to[u] = stream_load(row, (v0 + u * kWave + lane) * 16);
-    };
-    auto slot = [&](int k, const u32x4 (&from)[kRgVec]) {
-      const float w = __int_as_float(readlane(w_mine, k));
-      if (kDot) {
-        float dot = 0.0f;
+      for (int q = 0; q < kG; ++q) {
+        const span_t row = rg_row(out, row_of(k0 + q), nvec);
 #pragma unroll
-        for (int u = 0; u < kRgVec; ++u)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            dot = fmaf(bf16_lo(grad[u][c]), bf16_lo(from[u][c]), dot);
-            dot = fmaf(bf16_hi(grad[u][c]), bf16_hi(from[u][c]), dot);
-          }
-        dot = wave_sum_f32(dot);
-        if (lane == k) dot_mine += dot;
-      }
-      const span_t dst = rg_row(dout, readlane(d_mine, k), nvec);
-#pragma unroll
-      for (int u = 0; u < kRgVec; ++u) {
-        u32x4 o;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          o[c] = pack_bf16(w * bf16_lo(grad[u][c]), w * bf16_hi(grad[u][c]));
-        stream_store(o, dst, (v0 + u * kWave + lane) * 16);
+        for (int u = 0; u < kVec; ++u) to[q][u] = stream_load(row, (v0 + u * kWave + lane) * 16);
       }
     };
+    auto slots = [&](int k0, const u32x4 (&from)[kG][kVec]) {
 #pragma unroll
-    for (int u = 0; u < kRgVec; ++u) grad[u] = stream_load(src, (v0 + u * kWave + lane) * 16);
+      for (int q = 0; q < kG; ++q) {
+        const int k = k0 + q, d = row_of(k);
+        if (kDot) {
+          float dot = 0.0f;
+#pragma unroll
+          for (int u = 0; u < kVec; ++u)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              dot = fmaf(bf16_lo(grad[u][c]), bf16_lo(from[q][u][c]), dot);
+              dot = fmaf(bf16_hi(grad[u][c]), bf16_hi(from[q][u][c]), dot);
+            }
+          dot = wave_sum_f32(dot);
+          if (lane == k) dot_mine += dot;
+        }
+        if (!kScale || d < 0) continue;
+        const float w = __int_as_float(readlane(w_mine, k));
+        const span_t dst = rg_row(dout, d, nvec);
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) {
+          u32x4 o;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            o[c] = pack_bf16(w * bf16_lo(grad[u][c]), w * bf16_hi(grad[u][c]));
+          stream_store(o, dst, (v0 + u * kWave + lane) * 16);
+        }
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      const int at = (v0 + u * kWave + lane) * 16;      // read again by the scaling: kept
+      grad[u] = kScale ? stream_load(src, at) : __builtin_amdgcn_raw_buffer_load_b128(src, at, 0, 0);
+    }
     if (kDot) fetch(k_begin, y[0]);
-    for (int k = k_begin; k < k_end; k += 2) {       // row k + 1 is on its way while k is used
-      if (kDot && k + 1 < k_end) fetch(k + 1, y[1]);
-      slot(k, y[0]);
-      if (k + 1 < k_end) {
-        if (kDot && k + 2 < k_end) fetch(k + 2, y[0]);
-        slot(k + 1, y[1]);
+    for (int k = k_begin; k < k_end; k += 2 * kG) {  // the next slots are on their way
+      if (kDot && k + kG < k_end) fetch(k + kG, y[1]);
+      slots(k, y[0]);
+      if (k + kG < k_end) {
+        if (kDot && k + 2 * kG < k_end) fetch(k + 2 * kG, y[0]);
+        slots(k + kG, y[1]);
       }
     }
   }
   // a slot without a row read nothing: 0 (0 times an infinite gradient left a NaN)
   if (kDot && mine) dgate_w[g * K + lane] = d_mine < 0 ? 0.0f : dot_mine;
+}
+
+typedef void (*rg_kernel_t)(const u32x4*, const u32x4*, const int32_t*, const float*, u32x4*,
+                            float*, int64_t, int64_t, int64_t, int, int, int, int32_t*);
+struct RgKernels {
+  rg_kernel_t both, dot, scale;
+};
+template <int kVec>
+static RgKernels rg_kernels() {
+  return {combine_grad_kernel<true, true, kVec>, combine_grad_kernel<true, false, kVec>,
+          combine_grad_kernel<false, true, kVec>};
 }
 
 }  // namespace uep
@@ -106,13 +151,27 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   if ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(dout)) % 16 != 0)
     return UEP_EGEOM;
+  const int nv = (H / 8 + kWave - 1) / kWave;       // vectors per lane of a row
   const int parts = g1 - g0 <= kRgFew ? K : 1;
-  const int64_t blocks = ((g1 - g0) * parts + kRgTokPerBlock - 1) / kRgTokPerBlock;
-  auto kernel = out ? combine_grad_kernel<true> : combine_grad_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kRgThreads), 0, uep_stream(stream),
-                     reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(out),
-                     dest_row, gate_w, reinterpret_cast<u32x4*>(dout), dgate_w, out_rows, g0, g1,
-                     K, H / 8, parts, err);
-  UEP_CHECK_LAUNCH();
+  auto launch = [&](rg_kernel_t kernel, int64_t c0, int64_t c1) {
+    const int64_t blocks = ((c1 - c0) * parts + kRgTokPerBlock - 1) / kRgTokPerBlock;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kRgThreads), 0, uep_stream(stream),
+                       reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(out),
+                       dest_row, gate_w, reinterpret_cast<u32x4*>(dout), dgate_w, out_rows, c0, c1,
+                       K, H / 8, parts, err);
+    return hipGetLastError() == hipSuccess;
+  };
+  const RgKernels f = nv <= 1 ? rg_kernels<1>() : nv <= 2 ? rg_kernels<2>()
+                    : nv <= 4 ? rg_kernels<4>() : rg_kernels<8>();
+  if (!out) return launch(f.scale, g0, g1) ? UEP_OK : UEP_EHIP;
+  if ((g1 - g0) * K * (int64_t)H * 2 < kRgPhaseBytes)
+    return launch(f.both, g0, g1) ? UEP_OK : UEP_EHIP;
+  // tokens per pair of phases: equal chunks whose gradients stay in the last-level cache
+  const int64_t cap = std::max<int64_t>(64, kRgChunkBytes / ((int64_t)H * 2));
+  const int64_t n = (g1 - g0 + cap - 1) / cap, chunk = (g1 - g0 + n - 1) / n;
+  for (int64_t c0 = g0; c0 < g1; c0 += chunk) {
+    const int64_t c1 = std::min(g1, c0 + chunk);
+    if (!launch(f.dot, c0, c1) || !launch(f.scale, c0, c1)) return UEP_EHIP;
+  }
   return UEP_OK;
 }

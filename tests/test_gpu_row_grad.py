@@ -83,6 +83,50 @@ def test_combine_grad(case):
     assert np.array_equal(bits(place)[~named], bits(out)[~named])
 
 
+@pytest.mark.parametrize("R,T,K,H", [
+    (3, 4000, 4, 1032),       # 99 MB of rows: two phases, one chunk, a rank range
+    (2, 15000, 2, 4096),      # 246 MB of gradients: two chunks
+    (1, 100, 8, 40000),       # few tokens, long rows, in phases
+])
+def test_combine_grad_in_phases(R, T, K, H):
+    """Large calls run the dot products and the scaled rows apart.  The reference is torch on
+    the device: one fp32 product rounded to bf16, and the dot products in 64 bits."""
+    say("case: combine_grad in phases", R, T, K, H)
+    g = torch.Generator(device=DEV).manual_seed(R * T)
+    n = R * T * K
+    row = torch.randperm(n, generator=g, device=DEV).to(torch.int32)
+    row[torch.rand(n, generator=g, device=DEV) < 0.05] = -1
+    row = row.view(R, T, K)
+    dy = torch.randn(R, T, H, generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.randn(n, H, generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.rand(R, T, K, generator=g, device=DEV)
+    for lo, hi in ((0, R), (R - 1, R)):
+        dout = torch.full((n, H), 77, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+        dw = torch.full((R, T, K), 9.0, device=DEV)
+        place, dw2 = out.clone(), torch.empty_like(dw)
+        U.combine_grad(dy, out, row, w, dout, dw, r_begin=lo, r_end=hi)
+        U.combine_grad(dy, place, row, w, place, dw2, r_begin=lo, r_end=hi)
+        for k in range(K):
+            d = row[lo:hi, :, k].reshape(-1)
+            on = d >= 0
+            rows, grad = d[on].long(), dy[lo:hi].reshape(-1, H)[on]
+            want = (w[lo:hi, :, k].reshape(-1)[on, None] * grad.float()).to(torch.bfloat16)
+            assert torch.equal(dout[rows].view(torch.int16), want.view(torch.int16))
+            assert torch.equal(place[rows].view(torch.int16), want.view(torch.int16))
+            got = dw[lo:hi, :, k].reshape(-1)
+            dot = torch.cat([(grad[a:a + 2000].double() * out[rows[a:a + 2000]].double()).sum(-1)
+                             for a in range(0, len(rows), 2000)])
+            mag = torch.cat([(grad[a:a + 2000].double() * out[rows[a:a + 2000]].double()).abs()
+                             .sum(-1) for a in range(0, len(rows), 2000)])
+            assert ((got[on].double() - dot).abs() <= (H / 64 + 16) * EPS * mag).all()
+            assert (got[~on] == 0).all()
+        assert torch.equal(dw[lo:hi], dw2[lo:hi]) and (dw[:lo] == 9).all()
+        named = torch.zeros(n, dtype=torch.bool, device=DEV)
+        named[row[lo:hi][row[lo:hi] >= 0].long()] = True
+        assert (dout.view(torch.int16)[~named] == 77).all()
+        assert torch.equal(place.view(torch.int16)[~named], out.view(torch.int16)[~named])
+
+
 def test_rank_ranges_and_noops():
     say("case: row gradients, rank ranges")
     dr, dy, out, w = make(11, 4, 50, 4, 8, 512, 0.1)
