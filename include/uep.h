@@ -476,7 +476,7 @@ uep_status uep_lplb_sample(const int32_t* topk_ids, int32_t R, int32_t T, int32_
  *   err                   out  optional; UEP_ERR_LOGIT
  * Returns UEP_EINVAL for null pointers, sizes < 1 (T may be 0), an unknown dtype or
  * score, a bias with softmax, a bad scale; UEP_EGEOM for R > 64, E > 4096, K > 64,
- * K > E or R*T*K >= 2^31.
+ * K > E, R*T >= 2^26 or R*T*K >= 2^31.
  * ------------------------------------------------------------------------- */
 enum { UEP_GATE_SOFTMAX = 0, UEP_GATE_SIGMOID = 1 };
 uep_status uep_gate(const void* logits, int32_t dtype, const float* bias,
@@ -499,7 +499,8 @@ uep_status uep_gate(const void* logits, int32_t dtype, const float* bias,
  *   logits     [R][T][E]       in   as given to uep_gate
  *   topk_ids, gate_w           in   as written by uep_gate with the same score, renorm
  *                                   and scale
- *   dlogits    [R][T][E]       out  the logits' dtype; every element is written
+ *   dlogits    [R][T][E]       out  the logits' dtype; every element is written; not
+ *                                   overlapping logits (UEP_EINVAL)
  *   err                        out  optional; UEP_ERR_ID_RANGE: an id outside [-1, E),
  *                                   taken as -1
  * Returns UEP_EINVAL / UEP_EGEOM like uep_gate.
@@ -520,7 +521,8 @@ uep_status uep_gate_grad(const float* dgate_w, const void* logits, int32_t dtype
  *   dout     [out_rows][H] bf16   in   gradient of the dispatch buffer, 16-byte aligned
  *   dest_row [R][T][K]            in   as given to uep_permute
  *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end) are written
- *   dx       [R][T][H] bf16 bits  out  16-byte aligned; other ranks' rows are untouched
+ *   dx       [R][T][H] bf16 bits  out  16-byte aligned; other ranks' rows are untouched; not
+ *                                      overlapping dout (UEP_EINVAL)
  *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
  * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
  * ------------------------------------------------------------------------- */
@@ -543,7 +545,8 @@ uep_status uep_permute_grad(const uint16_t* dout, int64_t out_rows, const int32_
  *   dest_row [R][T][K]            in   as given to uep_combine (no row named twice)
  *   gate_w   [R][T][K] fp32       in
  *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end)
- *   dout     [out_rows][H] bf16   out  16-byte aligned; may be `out` itself (in place)
+ *   dout     [out_rows][H] bf16   out  16-byte aligned; may be `out` itself (in place), but
+ *                                      overlap it or dy in no other way (UEP_EINVAL)
  *   dgate_w  [R][T][K] fp32       out  slots of other ranks are untouched
  *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
  * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.

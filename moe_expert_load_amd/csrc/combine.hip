@@ -29,6 +29,7 @@ constexpr int kCbVec = 4;     // 16-byte vectors per lane per slice (8 bf16 each
 // waves instead of one after the other to one (1 token, K = 9, 14 KiB rows: 16.7 -> 6.2 us; 512
 // tokens 26.1 -> 13.9).
 constexpr int64_t kCbFew = 512;
+constexpr int64_t kCbLaunch = 1ll << 25;   // tokens of one launch, which holds below 2^32 threads
 
 // kVec vectors per lane hold a slice of a row (a whole row where it is shorter than a slice of
 // kCbVec); 4 rows go together, 8 short ones (65536 tokens of eight 512 B rows: 120 -> 53 us
@@ -113,19 +114,23 @@ static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_
   if (!rows || !dest_row || (weighted && !gate_w) || !y) return UEP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(y)) % 16 != 0)
     return UEP_EGEOM;
+  if (!weighted && uep_overlap(rows, out_rows * H * 2, y, (int64_t)R * T * H * 2))
+    return UEP_EINVAL;
   const int slices = (H / 8 + kCbVec * kWave - 1) / (kCbVec * kWave);
   const int parts = g1 - g0 <= kCbFew ? std::min(slices, 16) : 1;
-  const int64_t blocks = ((g1 - g0) * parts + kCbTokPerBlock - 1) / kCbTokPerBlock;
   const int nv = (H / 8 + kWave - 1) / kWave;       // vectors per lane of a row
   auto kernel = weighted ? (nv <= 1   ? combine_kernel<true, 1>
                             : nv <= 2 ? combine_kernel<true, 2> : combine_kernel<true, kCbVec>)
                          : (nv <= 1   ? combine_kernel<false, 1>
                             : nv <= 2 ? combine_kernel<false, 2> : combine_kernel<false, kCbVec>);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kCbThreads), 0, uep_stream(stream),
-                     reinterpret_cast<const u32x4*>(rows), dest_row, gate_w,
-                     reinterpret_cast<u32x4*>(y), out_rows, g0, g1, K, H / 8, parts,
-                     err);
-  UEP_CHECK_LAUNCH();
+  for (int64_t c0 = g0; c0 < g1; c0 += kCbLaunch) {
+    const int64_t c1 = std::min(g1, c0 + kCbLaunch);
+    const int64_t blocks = ((c1 - c0) * parts + kCbTokPerBlock - 1) / kCbTokPerBlock;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kCbThreads), 0, uep_stream(stream),
+                       reinterpret_cast<const u32x4*>(rows), dest_row, gate_w,
+                       reinterpret_cast<u32x4*>(y), out_rows, c0, c1, K, H / 8, parts, err);
+    UEP_CHECK_LAUNCH();
+  }
   return UEP_OK;
 }
 

@@ -205,4 +205,10 @@ __device__ __forceinline__ int checked_row(int d, int64_t out_rows, int32_t* err
     if (hipGetLastError() != hipSuccess) return UEP_EHIP; \
   } while (0)
 
+// Whether two buffers share a byte.
+static inline bool uep_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 static inline hipStream_t uep_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }

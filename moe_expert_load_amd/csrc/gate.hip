@@ -491,7 +491,8 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
     const int lead = vec ? (int)((g0 * E) % kCe) : 0;
     const int pos = tok * E + id + lead;
     T* dst = dlogits + g0 * E - lead;
-    const T* src = logits + g0 * E - lead;            // not read at `lead` elements
+    const T* src = logits + g0 * E - lead;
+    const int64_t stretch = n_tok * E - g0 * E + lead;   // elements of src up to its end
     for (int o = 0; o < total + lead; o += kGtWin) {
       const bool mine = on && pos >= o && pos < o + kGtWin;
       if (mine) win[pos - o] = d;
@@ -508,20 +509,25 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
         } else {
           v[0] = win[i];
         }
-        if constexpr (kDense) {                       // vec: rows of whole units, lead 0
-          const int row = E == 1 ? at : (int)__umulhi((uint32_t)at, e_magic);
-          const f32x4 q = par[row];
+        if constexpr (kDense) {
+          // a unit holds the end of row r0 and, from element `cut` on, the start of the next
+          const int p0 = max(at - lead, 0);
+          const int r0 = E == 1 ? p0 : (int)__umulhi((uint32_t)p0, e_magic);
+          const int cut = (r0 + 1) * E - (at - lead);
+          const f32x4 q0 = par[r0], q1 = par[min(r0 + 1, tpw - 1)];
           float x[kCe];
-          if (vec) {
+          if (vec && at + kCe <= stretch) {
             const u32x4 w = *reinterpret_cast<const u32x4*>(src + at);
 #pragma unroll
             for (int j = 0; j < kCe; ++j) x[j] = gt_element<T>(w, j);
-          } else {
-            x[0] = gt_load(src, at);
+          } else {                                    // single elements, and the tensor's end
+#pragma unroll
+            for (int j = 0; j < kCe; ++j)
+              x[j] = j < unit && at + j < stretch ? gt_load(src, at + j) : 0.0f;
           }
 #pragma unroll
           for (int j = 0; j < kCe; ++j) {
-            if (!vec && j > 0) break;
+            const f32x4 q = j < cut ? q0 : q1;
             const float s = q[1] * gt_exp(x[j] - q[0]);
             v[j] = gt_finite(x[j]) ? s * (v[j] - q[2]) : 0.0f;
           }
@@ -560,17 +566,12 @@ struct GtCall {
   hipStream_t stream;
 };
 
-// workgroups for n_tok tokens, `per` each; a launch holds below 2^32 threads
-static bool gt_blocks(int64_t n_tok, int per, unsigned* blocks) {
-  const int64_t n = (n_tok + per - 1) / per;
-  *blocks = (unsigned)n;
-  return n < (1ll << 32) / kGtThreads;
-}
+// workgroups for n_tok < 2^26 tokens, at least 4 each: a launch holds below 2^32 threads
+static unsigned gt_blocks(int64_t n_tok, int per) { return (unsigned)((n_tok + per - 1) / per); }
 
 template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
 static uep_status gt_sorted(const GtCall& c) {
-  unsigned blocks;
-  if (!gt_blocks(c.n_tok, kGtThreads / kL, &blocks)) return UEP_EGEOM;
+  const unsigned blocks = gt_blocks(c.n_tok, kGtThreads / kL);
   const int vec = (reinterpret_cast<uintptr_t>(c.logits) | (uintptr_t)c.E * sizeof(T)) % 16 == 0;
   const int vec_bias = (reinterpret_cast<uintptr_t>(c.bias) | (uintptr_t)c.E * 4) % 16 == 0;
   hipLaunchKernelGGL((gate_sort_kernel<T, KY, kSigmoid, kL, kN, kPer>), dim3(blocks), dim3(kGtThreads),
@@ -582,8 +583,7 @@ static uep_status gt_sorted(const GtCall& c) {
 
 template <typename T, int kVpt>
 static uep_status gt_general(const GtCall& c) {
-  unsigned blocks;
-  if (!gt_blocks(c.n_tok, kGtTokPerBlock, &blocks)) return UEP_EGEOM;
+  const unsigned blocks = gt_blocks(c.n_tok, kGtTokPerBlock);
   hipLaunchKernelGGL((gate_kernel<T, kVpt>), dim3(blocks), dim3(kGtThreads), 0, c.stream,
                      static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok, c.T, c.E, c.K,
                      c.score, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
@@ -624,7 +624,8 @@ static uep_status gt_check(const void* logits, int32_t dtype, int32_t R, int32_t
   if (dtype != UEP_F32 && dtype != UEP_BF16) return UEP_EINVAL;
   if (score != UEP_GATE_SOFTMAX && score != UEP_GATE_SIGMOID) return UEP_EINVAL;
   if (!(scale > -__builtin_inff() && scale < __builtin_inff()) || scale == 0.0f) return UEP_EINVAL;
-  if (R > 64 || E > kGtMaxE || K > 64 || K > E || (int64_t)R * T * K >= (1ll << 31))
+  if (R > 64 || E > kGtMaxE || K > 64 || K > E || (int64_t)R * T * K >= (1ll << 31) ||
+      (int64_t)R * T >= (1ll << 26))
     return UEP_EGEOM;
   if (T > 0 && !logits) return UEP_EINVAL;
   return UEP_OK;
@@ -659,6 +660,8 @@ extern "C" uep_status uep_gate_grad(const float* dgate_w, const void* logits, in
   if (T == 0) return UEP_OK;
   if (!dgate_w || !topk_ids || !gate_w || !dlogits) return UEP_EINVAL;
   const int64_t n_tok = (int64_t)R * T;
+  const int64_t bytes = n_tok * E * (dtype == UEP_F32 ? 4 : 2);
+  if (uep_overlap(logits, bytes, dlogits, bytes)) return UEP_EINVAL;
   int lg_kp = 0;
   while ((1 << lg_kp) < K) ++lg_kp;
   const int64_t n_grp = (n_tok + (kWave >> lg_kp) - 1) / (kWave >> lg_kp);
@@ -667,9 +670,9 @@ extern "C" uep_status uep_gate_grad(const float* dgate_w, const void* logits, in
   const uint32_t e_magic = (uint32_t)(((1ull << 32) + E - 1) / E);
   const bool dense = score == UEP_GATE_SOFTMAX && !renorm;
   const uintptr_t size = dtype == UEP_F32 ? 4 : 2;
-  // dense rows are read in the units that are written, so they hold whole ones
+  // a dense gradient reads in the units that it writes, of at most two rows each
   const int vec = reinterpret_cast<uintptr_t>(dlogits) % 16 == 0 &&
-                  (!dense || (reinterpret_cast<uintptr_t>(logits) % 16 == 0 && E * size % 16 == 0));
+                  (!dense || (reinterpret_cast<uintptr_t>(logits) % 16 == 0 && E * size >= 16));
   hipStream_t s = uep_stream(stream);
 #define UEP_GATE_GRAD(T, DENSE)                                                                  \
   hipLaunchKernelGGL((gate_grad_kernel<T, DENSE>), dim3(blocks), dim3(kGtThreads), 0, s, dgate_w, \

@@ -151,6 +151,10 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   if ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(dout)) % 16 != 0)
     return UEP_EGEOM;
+  const int64_t tok_bytes = (int64_t)R * T * H * 2, row_bytes = out_rows * H * 2;
+  if (uep_overlap(dy, tok_bytes, dout, row_bytes) ||
+      (out && out != dout && uep_overlap(out, row_bytes, dout, row_bytes)))
+    return UEP_EINVAL;
   const int nv = (H / 8 + kWave - 1) / kWave;       // vectors per lane of a row
   const int parts = g1 - g0 <= kRgFew ? K : 1;
   auto launch = [&](rg_kernel_t kernel, int64_t c0, int64_t c1) {
@@ -163,15 +167,16 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   };
   const RgKernels f = nv <= 1 ? rg_kernels<1>() : nv <= 2 ? rg_kernels<2>()
                     : nv <= 4 ? rg_kernels<4>() : rg_kernels<8>();
-  if (!out) return launch(f.scale, g0, g1) ? UEP_OK : UEP_EHIP;
-  if ((g1 - g0) * K * (int64_t)H * 2 < kRgPhaseBytes)
+  if (out && (g1 - g0) * K * (int64_t)H * 2 < kRgPhaseBytes)
     return launch(f.both, g0, g1) ? UEP_OK : UEP_EHIP;
-  // tokens per pair of phases: equal chunks whose gradients stay in the last-level cache
-  const int64_t cap = std::max<int64_t>(64, kRgChunkBytes / ((int64_t)H * 2));
+  // tokens per pair of phases: equal chunks whose gradients stay in the last-level cache, and
+  // which a launch holds (below 2^32 threads)
+  const int64_t cap = out ? std::max<int64_t>(64, kRgChunkBytes / ((int64_t)H * 2)) : 1ll << 25;
   const int64_t n = (g1 - g0 + cap - 1) / cap, chunk = (g1 - g0 + n - 1) / n;
   for (int64_t c0 = g0; c0 < g1; c0 += chunk) {
     const int64_t c1 = std::min(g1, c0 + chunk);
-    if (!launch(f.dot, c0, c1) || !launch(f.scale, c0, c1)) return UEP_EHIP;
+    if (out && !launch(f.dot, c0, c1)) return UEP_EHIP;
+    if (!launch(f.scale, c0, c1)) return UEP_EHIP;
   }
   return UEP_OK;
 }

@@ -9,6 +9,7 @@ not built: there is no fallback path.
 
 from __future__ import annotations
 
+import bisect
 import ctypes
 import dataclasses
 import os
@@ -520,6 +521,12 @@ def adamw_prepare(params, grads, m, v, copies=None, tops=None, weight_decay=0.0,
     for a, b in zip(written, written[1:]):
         if b[0] < a[1]:
             raise TypeError(f"{a[2]} and {b[2]} overlap: one step would write them twice")
+    ends = [w[1] for w in written]
+    for i, t in enumerate(grads):
+        at = bisect.bisect_right(ends, t.data_ptr())
+        if t.numel() and at < len(written) and \
+                written[at][0] < t.data_ptr() + t.numel() * t.element_size():
+            raise TypeError(f"grads[{i}] overlaps {written[at][2]}, which the step writes")
     need = int(LIB.uep_adamw_plan_size(table, n))
     dev = params[0].device if n else torch.device("cuda" if device is None else device)
     buf = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)

@@ -173,6 +173,22 @@ def test_second_moments_below_the_normal_range():
                1e-3, 1.0, [0.0], [1.0], (0.9, 0.999), 1e-30, 0)
 
 
+def test_overlapping_tensors_are_refused():
+    """Tensors that one step would write twice, and gradients inside what it writes."""
+    say("case: adamw overlaps")
+    x = torch.zeros(4000, device=DEV)
+    p, m, v, g = x[:1000], x[1000:2000], x[2000:3000], x[3000:]
+    U.adamw_prepare([p], [g], [m], [v])
+    U.adamw_prepare([p[:500], p[500:]], [g[:500], g[:500]], [m[:500], m[500:]], [v[:500], v[500:]])
+    for args, match in ((([p], [g], [x[999:1999]], [v]), "overlap"),
+                        (([p, p], [g, g], [m, m.clone()], [v, v.clone()]), "overlap"),
+                        (([p], [x[2001:3001]], [m], [v]), "grads.0. overlaps v.0."),
+                        (([p], [x[500:1500]], [m], [v]), "grads.0. overlaps"),
+                        (([p], [p], [m], [v]), "grads.0. overlaps params.0.")):
+        with pytest.raises(TypeError, match=match):
+            U.adamw_prepare(*args)
+
+
 def test_plan_errors_leave_everything_alone():
     say("case: adamw plan errors")
     p, g, m, v = (torch.ones(500, device=DEV) for _ in range(4))

@@ -40,7 +40,8 @@ def test_gate_refusals(lib, call):
                 dict(score=2), dict(scale=0.0), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(logits=null)):
         assert call(lib, **bad) == EINVAL, bad
-    for bad in (dict(R=65), dict(E=4097), dict(E=80, K=65), dict(K=9), dict(T=1 << 30)):
+    for bad in (dict(R=65), dict(E=4097), dict(E=80, K=65), dict(K=9), dict(T=1 << 30),
+                dict(T=1 << 25, K=1)):
         assert call(lib, **bad) == EGEOM, bad
 
 
@@ -76,6 +77,19 @@ def test_row_gradient_pointers(lib):
     for bad in (dict(dy=null), dict(w=null), dict(out=null), dict(dw=null)):
         assert combine_grad(lib, **bad) == EINVAL, bad            # out and dw go together
     assert combine_grad(lib, dy=odd) == EGEOM and combine_grad(lib, out=odd) == EGEOM
+
+
+def test_overlapping_buffers_are_refused(lib):
+    """Outputs may not share bytes with inputs, except dout being `out` itself."""
+    at = ctypes.c_void_p
+    far = at(1 << 20)
+    assert gate_grad(lib, logits=at(4096), dl=at(4096)) == EINVAL
+    assert gate_grad(lib, logits=at(4096), dl=at(4096 + 2 * 3 * 8 * 4 - 4)) == EINVAL
+    # R T H = 2 * 4 * 16 bf16 = 256 bytes, P H = 16 * 16 bf16 = 512 bytes
+    assert permute_grad(lib, dout=at(4096), dx=at(4096 + 496)) == EINVAL
+    assert permute_grad(lib, dout=at(4096 + 240), dx=at(4096)) == EINVAL
+    assert combine_grad(lib, dy=at(4096), dout=at(4096 + 240), out=far) == EINVAL
+    assert combine_grad(lib, dy=far, dout=at(4096), out=at(4096 + 496)) == EINVAL
 
 
 class Tensor(ctypes.Structure):
