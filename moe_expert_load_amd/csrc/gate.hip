@@ -3,6 +3,7 @@
 // The selection compares distinct keys that order by (rank, lowest id), so that one maximum
 // names both the winner and its id.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 
@@ -162,22 +163,39 @@ __device__ __forceinline__ float gt_lanes_sum(float v) {
   return v;
 }
 
-// 16 bytes of a row of E elements from element e0 on, -infinity past its end; vec: all or none
-// are there, and aligned.
 template <typename T>
-__device__ __forceinline__ u32x4 gt_load16(const T* p, int e0, int E, bool vec) {
+struct GtLoose;                                       // 16 bytes aligned as one element
+template <>
+struct GtLoose<float> {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <>
+struct GtLoose<uint16_t> {
+  typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
+};
+
+// 16 bytes of a row of E elements (at least as many as they hold) from element e0 on, -infinity
+// past its end.  Rows start at any element: the memory takes vector accesses at the
+// alignment of one.  kRagged: where the row ends inside the 16 bytes its last 16 are read
+// and shifted down; otherwise it ends at none.
+template <bool kRagged, typename T>
+__device__ __forceinline__ u32x4 gt_load16(const T* p, int e0, int E) {
   constexpr uint32_t kFill = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+  constexpr int kCe = 16 / sizeof(T);
   u32x4 w = {kFill, kFill, kFill, kFill};
-  if (vec) {
-    if (e0 < E) w = *reinterpret_cast<const u32x4*>(p + e0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16 / (int)sizeof(T); ++j)
-      if (e0 + j < E) {
-        if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(p[e0 + j]);
-        else w[j / 2] = j & 1 ? (w[j / 2] & 0xFFFFu) | (uint32_t)p[e0 + j] << 16
-                              : (w[j / 2] & 0xFFFF0000u) | p[e0 + j];
-      }
+  const int at = kRagged ? min(e0, E - kCe) : e0;
+  if (e0 < E) w = *reinterpret_cast<const typename GtLoose<T>::type*>(p + at);
+  if (kRagged) {
+    const int shift = e0 < E ? (e0 - at) * (int)sizeof(T) : 0;   // bytes
+    w = shift & 8 ? u32x4{w[2], w[3], kFill, kFill} : w;
+    w = shift & 4 ? u32x4{w[1], w[2], w[3], kFill} : w;
+    if (sizeof(T) == 2) {
+      const int bits = shift & 2 ? 16 : 0;
+      w = u32x4{__builtin_amdgcn_alignbit(w[1], w[0], bits),
+                __builtin_amdgcn_alignbit(w[2], w[1], bits),
+                __builtin_amdgcn_alignbit(w[3], w[2], bits),
+                __builtin_amdgcn_alignbit(kFill, w[3], bits)};
+    }
   }
   return w;
 }
@@ -191,8 +209,8 @@ template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
 __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
     const int32_t* __restrict__ batch_size, int64_t n_tok, int tok_per_rank, int E, int K,
-    int renorm, float scale, int vec, int vec_bias, int32_t* __restrict__ topk_ids,
-    float* __restrict__ gate_w, int32_t* err) {
+    int renorm, float scale, int32_t* __restrict__ topk_ids, float* __restrict__ gate_w,
+    int32_t* err) {
   typedef typename KY::type key_t;
   constexpr int kCe = 16 / sizeof(T);                 // experts of one 16-byte load
   constexpr int kChunks = kPer / kCe;
@@ -201,13 +219,25 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
   bool live = g < n_tok;
   if (live && batch_size) live = (int)(g % tok_per_rank) < batch_size[g / tok_per_rank];
   const T* row = logits + (live ? g : 0) * (int64_t)E;
+  const int e_end = live ? E : 0;
   u32x4 raw[kChunks];
+  if (E % kCe == 0) {
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c)                   // the first is never skipped
-    raw[c] = gt_load16(row, (c * kL + lane) * kCe, live ? E : 0, vec);
+    for (int c = 0; c < kChunks; ++c)
+      raw[c] = gt_load16<false>(row, (c * kL + lane) * kCe, e_end);
+  } else {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      raw[c] = gt_load16<true>(row, (c * kL + lane) * kCe, e_end);
+  }
   bool bad = false, odd_bias = false;
-  if (kSigmoid && bias) {                             // each thread a few of them
-    for (int e = threadIdx.x; e < E; e += kGtThreads) bad |= gt_bad(bias[e]);
+  __shared__ __attribute__((aligned(16))) float bias_lds[kSigmoid ? kL * kPer : 4];
+  if (kSigmoid) {
+    for (int e = threadIdx.x; e < kL * kPer; e += kGtThreads) {
+      const float y = bias && e < E ? bias[e] : 0.0f;
+      bad |= gt_bad(y);
+      bias_lds[e] = y;
+    }
     odd_bias = __syncthreads_or(bad);
   }
   key_t best[kN];
@@ -226,15 +256,11 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     if (kSigmoid) {
       float y[kN];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) y[i] = 0.0f;
-      if (bias) {
+      for (int h = 0; h < kN; h += 4) {
+        const int n = q * kN + h, e = (n / kCe * kL + lane) * kCe + n % kCe;
+        const f32x4 w = *reinterpret_cast<const f32x4*>(bias_lds + e);
 #pragma unroll
-        for (int h = 0; h < kN; h += 4) {
-          const int n = q * kN + h, e = (n / kCe * kL + lane) * kCe + n % kCe;
-          const u32x4 w = gt_load16(bias, e, E, vec_bias);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[h + j] = __uint_as_float(w[j]);
-        }
+        for (int j = 0; j < 4; ++j) y[h + j] = w[j];
       }
 #pragma unroll
       for (int i = 0; i < kN; ++i) y[i] += gt_sigmoid(f[i]);
@@ -572,11 +598,9 @@ static unsigned gt_blocks(int64_t n_tok, int per) { return (unsigned)((n_tok + p
 template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
 static uep_status gt_sorted(const GtCall& c) {
   const unsigned blocks = gt_blocks(c.n_tok, kGtThreads / kL);
-  const int vec = (reinterpret_cast<uintptr_t>(c.logits) | (uintptr_t)c.E * sizeof(T)) % 16 == 0;
-  const int vec_bias = (reinterpret_cast<uintptr_t>(c.bias) | (uintptr_t)c.E * 4) % 16 == 0;
   hipLaunchKernelGGL((gate_sort_kernel<T, KY, kSigmoid, kL, kN, kPer>), dim3(blocks), dim3(kGtThreads),
                      0, c.stream, static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok,
-                     c.T, c.E, c.K, c.renorm, c.scale, vec, vec_bias, c.topk_ids, c.gate_w, c.err);
+                     c.T, c.E, c.K, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }
@@ -608,10 +632,10 @@ static uep_status gt_by_experts(const GtCall& c) {
 
 template <typename T>
 static uep_status gt_launch(const GtCall& c) {
-  if (c.K <= 16 && c.E <= kGtSortE) {
+  if (c.K <= 16 && c.E <= kGtSortE && c.E >= 16 / (int)sizeof(T)) {
     if (c.score == UEP_GATE_SIGMOID) return gt_by_experts<T, Key64, true>(c);
-    if (sizeof(T) == 2) return gt_by_experts<T, Key32, false>(c);
-    return gt_by_experts<T, Key64, false>(c);
+    typedef typename std::conditional<sizeof(T) == 2, Key32, Key64>::type key;
+    return gt_by_experts<T, key, false>(c);
   }
   if (c.E <= 256) return gt_general<T, 4>(c);
   if (c.E <= 1024) return gt_general<T, 16>(c);
