@@ -12,7 +12,7 @@ namespace uep {
 constexpr int kGtThreads = 256;
 constexpr int kGtTokPerBlock = kGtThreads / kWave;
 constexpr int kGtMaxE = 4096;
-constexpr int kGtSortE = 512;         // most experts of the kernel that sorts in registers
+constexpr int kGtSortE = 1024;        // most experts of the kernel that sorts in registers
 // Up to this many tokens a call is bound by its latency and takes 16 lanes per token (the
 // shortest chain); above, by its instructions and takes as few lanes as hold the experts.
 constexpr int64_t kGtFew = 4096;
@@ -551,11 +551,15 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
             for (int j = 0; j < kCe; ++j)
               x[j] = j < unit && at + j < stretch ? gt_load(src, at + j) : 0.0f;
           }
+          auto dense = [](float x, float v, f32x4 q) {
+            return gt_finite(x) ? q[1] * gt_exp(x - q[0]) * (v - q[2]) : 0.0f;
+          };
+          if (E % kCe == 0) {                         // units of one row
 #pragma unroll
-          for (int j = 0; j < kCe; ++j) {
-            const f32x4 q = j < cut ? q0 : q1;
-            const float s = q[1] * gt_exp(x[j] - q[0]);
-            v[j] = gt_finite(x[j]) ? s * (v[j] - q[2]) : 0.0f;
+            for (int j = 0; j < kCe; ++j) v[j] = dense(x[j], v[j], q0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kCe; ++j) v[j] = dense(x[j], v[j], j < cut ? q0 : q1);
           }
         }
         if (vec && at >= lead && at + kCe <= total + lead) {
@@ -563,8 +567,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             w[j] = sizeof(T) == 4 ? __float_as_uint(v[j])
-                                  : f32_to_bf16(v[2 * j & (kCe - 1)]) |
-                                        (f32_to_bf16(v[(2 * j + 1) & (kCe - 1)]) << 16);
+                                  : pack_bf16(v[2 * j & (kCe - 1)], v[(2 * j + 1) & (kCe - 1)]);
           *reinterpret_cast<u32x4*>(dst + at) = w;
         } else {
 #pragma unroll
@@ -624,10 +627,11 @@ static uep_status gt_by_slots(const GtCall& c) {
 
 template <typename T, typename KY, bool kSigmoid>
 static uep_status gt_by_experts(const GtCall& c) {
-  if (c.n_tok <= kGtFew) return gt_by_slots<T, KY, kSigmoid, 16, 32>(c);
+  if (c.n_tok <= kGtFew && c.E <= 16 * 32) return gt_by_slots<T, KY, kSigmoid, 16, 32>(c);
   if (c.E <= 4 * 32) return gt_by_slots<T, KY, kSigmoid, 4, 32>(c);
   if (c.E <= 4 * 64) return gt_by_slots<T, KY, kSigmoid, 4, 64>(c);
-  return gt_by_slots<T, KY, kSigmoid, 8, 64>(c);
+  if (c.E <= 8 * 64) return gt_by_slots<T, KY, kSigmoid, 8, 64>(c);
+  return gt_by_slots<T, KY, kSigmoid, 16, 64>(c);
 }
 
 template <typename T>
@@ -637,7 +641,7 @@ static uep_status gt_launch(const GtCall& c) {
     typedef typename std::conditional<sizeof(T) == 2, Key32, Key64>::type key;
     return gt_by_experts<T, key, false>(c);
   }
-  if (c.E <= 256) return gt_general<T, 4>(c);
+  if (c.E <= 256) return gt_general<T, 4>(c);       // over 16 slots
   if (c.E <= 1024) return gt_general<T, 16>(c);
   return gt_general<T, 64>(c);
 }
