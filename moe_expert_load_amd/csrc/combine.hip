@@ -32,9 +32,10 @@ constexpr int64_t kCbFew = 512;
 constexpr int64_t kCbLaunch = 1ll << 25;   // tokens of one launch, which holds below 2^32 threads
 
 // kVec vectors per lane hold a slice of a row (a whole row where it is shorter than a slice of
-// kCbVec); 4 rows go together, 8 short ones (65536 tokens of eight 512 B rows: 120 -> 53 us
-// against four vectors whatever the row).
-template <bool kWeighted, int kVec>
+// kCbVec); kGroup rows go together: 4, and of short rows (up to 2 KiB) as many as a token has, up
+// to 8.  Against four vectors and four rows whatever the row: 65536 tokens of eight 512 B rows
+// 120 -> 53 us, of one 1072 B row 52 -> 35; one row at a time of 4 KiB rows loses (91 -> 97).
+template <bool kWeighted, int kVec, int kGroup>
 __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __restrict__ y_disp,
                                                              const int32_t* __restrict__ dest_row,
                                                              const float* __restrict__ gate_w,
@@ -43,7 +44,6 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
                                                              int64_t g1, int K, int nvec,
                                                              int parts, int32_t* err) {
 #pragma clang fp contract(off)
-  constexpr int kGroup = kVec == kCbVec ? 4 : 8;
   const int lane = threadIdx.x % kWave;
   const int64_t b = xcd_block(blockIdx.x, gridDim.x);
   // the wave's token, uniform (readfirstlane), so the row spans below live in SGPRs
@@ -100,6 +100,21 @@ __global__ __launch_bounds__(kCbThreads) void combine_kernel(const u32x4* __rest
   }
 }
 
+typedef void (*cb_kernel_t)(const u32x4*, const int32_t*, const float*, u32x4*, int64_t, int64_t,
+                            int64_t, int, int, int, int32_t*);
+template <bool kWeighted, int kVec>
+static cb_kernel_t cb_group(int slots) {
+  return slots > 4   ? combine_kernel<kWeighted, kVec, 8>
+         : slots > 2 ? combine_kernel<kWeighted, kVec, 4>
+         : slots > 1 ? combine_kernel<kWeighted, kVec, 2> : combine_kernel<kWeighted, kVec, 1>;
+}
+// nv: vectors per lane that a row fills
+template <bool kWeighted>
+static cb_kernel_t cb_kernel(int nv, int slots) {
+  return nv <= 1   ? cb_group<kWeighted, 1>(slots)
+         : nv <= 2 ? cb_group<kWeighted, 2>(slots) : combine_kernel<kWeighted, kCbVec, 4>;
+}
+
 // The argument checks and the launch that both entry points share.
 static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_t* dest_row,
                             const float* gate_w, bool weighted, int32_t R, int32_t T, int32_t K,
@@ -119,10 +134,7 @@ static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_
   const int slices = (H / 8 + kCbVec * kWave - 1) / (kCbVec * kWave);
   const int parts = g1 - g0 <= kCbFew ? std::min(slices, 16) : 1;
   const int nv = (H / 8 + kWave - 1) / kWave;       // vectors per lane of a row
-  auto kernel = weighted ? (nv <= 1   ? combine_kernel<true, 1>
-                            : nv <= 2 ? combine_kernel<true, 2> : combine_kernel<true, kCbVec>)
-                         : (nv <= 1   ? combine_kernel<false, 1>
-                            : nv <= 2 ? combine_kernel<false, 2> : combine_kernel<false, kCbVec>);
+  const cb_kernel_t kernel = weighted ? cb_kernel<true>(nv, K) : cb_kernel<false>(nv, K);
   for (int64_t c0 = g0; c0 < g1; c0 += kCbLaunch) {
     const int64_t c1 = std::min(g1, c0 + kCbLaunch);
     const int64_t blocks = ((c1 - c0) * parts + kCbTokPerBlock - 1) / kCbTokPerBlock;

@@ -13,7 +13,8 @@
 // other than mixed, and the two halves of this operator share only dy.  From kRgPhaseBytes of
 // dispatch rows on, the dot products (reads alone) and the scaled rows (writes alone) are
 // therefore launches of their own, over chunks of tokens whose dy stays in the 256 MB
-// last-level cache from the first to the second.  Measured on MI355X (two launches per chunk
+// last-level cache from the first to the second; not for K = 1, where dy, read twice, is as
+// large as the rows (65536 x 4 KiB in one launch 154 us, in two 164).  Measured on MI355X (two launches per chunk
 // against one for both): 65536 tokens, K = 8, 8 KiB rows 1760 -> 1503 us (6.08 TB/s of the
 // bytes that have to move; a large copy reaches 5.65), chunks of 16 / 64 / 128 / 224 MB of
 // dy / all in one 1692 / 1561 / 1519 / 1503 / 1570 us; 32 MB of rows 16.6 -> 16.0 us
@@ -21,6 +22,8 @@
 //
 // Short rows: with vectors for 8 KiB per wave whatever the row, 65536 tokens of eight 512 B
 // rows took 293 us; with a row's own vectors and kRgVec of them in flight 116 (one launch).
+// Registers for no more slots than a token has leave room for more waves: 65536 tokens of one
+// 1072 B row 77 -> 50 us, of two 512 B rows 57 -> 43.
 #include <algorithm>
 
 #include "common.h"
@@ -44,8 +47,8 @@ __device__ __forceinline__ span_t rg_row(const u32x4* base, int d, int nvec) {
 
 // kDot: the dot products (dout is not touched unless kScale); kScale: the scaled rows.
 // kVec vectors per lane hold a slice of a row (a whole row where it is shorter than a slice of
-// kRgVec), kRgVec / kVec slots go together.
-template <bool kDot, bool kScale, int kVec>
+// kRgVec), kG slots go together.
+template <bool kDot, bool kScale, int kVec, int kG>
 __global__ __launch_bounds__(kRgThreads) void combine_grad_kernel(
     const u32x4* __restrict__ dy, const u32x4* out, const int32_t* __restrict__ dest_row,
     const float* __restrict__ gate_w, u32x4* dout, float* __restrict__ dgate_w, int64_t out_rows,
@@ -61,7 +64,6 @@ __global__ __launch_bounds__(kRgThreads) void combine_grad_kernel(
   const int w_mine = mine ? __float_as_int(gate_w[g * K + lane]) : 0;
   const span_t src = span_of(dy + g * nvec, (int64_t)nvec * 16);
   float dot_mine = 0.0f;
-  constexpr int kG = kRgVec / kVec;
   for (int v0 = 0; v0 < nvec; v0 += kVec * kWave) {
     u32x4 grad[kVec], y[2][kG][kVec];
     auto row_of = [&](int k) { return k < k_end ? readlane(d_mine, k) : -1; };
@@ -126,10 +128,18 @@ typedef void (*rg_kernel_t)(const u32x4*, const u32x4*, const int32_t*, const fl
 struct RgKernels {
   rg_kernel_t both, dot, scale;
 };
+template <int kVec, int kG>
+static RgKernels rg_group() {
+  return {combine_grad_kernel<true, true, kVec, kG>, combine_grad_kernel<true, false, kVec, kG>,
+          combine_grad_kernel<false, true, kVec, kG>};
+}
+// slots together: as many as a token has, up to kRgVec vectors
 template <int kVec>
-static RgKernels rg_kernels() {
-  return {combine_grad_kernel<true, true, kVec>, combine_grad_kernel<true, false, kVec>,
-          combine_grad_kernel<false, true, kVec>};
+static RgKernels rg_kernels(int slots) {
+  if (kRgVec / kVec >= 8 && slots > 4) return rg_group<kVec, kRgVec / kVec >= 8 ? 8 : 1>();
+  if (kRgVec / kVec >= 4 && slots > 2) return rg_group<kVec, kRgVec / kVec >= 4 ? 4 : 1>();
+  if (kRgVec / kVec >= 2 && slots > 1) return rg_group<kVec, kRgVec / kVec >= 2 ? 2 : 1>();
+  return rg_group<kVec, 1>();
 }
 
 }  // namespace uep
@@ -165,9 +175,10 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
                        K, H / 8, parts, err);
     return hipGetLastError() == hipSuccess;
   };
-  const RgKernels f = nv <= 1 ? rg_kernels<1>() : nv <= 2 ? rg_kernels<2>()
-                    : nv <= 4 ? rg_kernels<4>() : rg_kernels<8>();
-  if (out && (g1 - g0) * K * (int64_t)H * 2 < kRgPhaseBytes)
+  const int slots = parts == 1 ? K : 1;             // of one wave
+  const RgKernels f = nv <= 1 ? rg_kernels<1>(slots) : nv <= 2 ? rg_kernels<2>(slots)
+                    : nv <= 4 ? rg_kernels<4>(slots) : rg_kernels<8>(slots);
+  if (out && (K == 1 || (g1 - g0) * K * (int64_t)H * 2 < kRgPhaseBytes))
     return launch(f.both, g0, g1) ? UEP_OK : UEP_EHIP;
   // tokens per pair of phases: equal chunks whose gradients stay in the last-level cache, and
   // which a launch holds (below 2^32 threads)
