@@ -52,13 +52,18 @@ __device__ __forceinline__ uint32_t aw_next(uint32_t x) {   // xorshift32 (Marsa
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+// The tensors' pointers come out of the plan, where the compiler cannot see that they are
+// global memory: said here, since flat accesses, which it would make, cost more.
+template <typename T>
+using Global = __attribute__((address_space(1))) T*;
+
 // Four consecutive elements of an array, as loaded; kFull: all there and aligned for one access.
 // Accesses are non-temporal: every byte is used once a step.
 template <bool kFull, typename T>
-__device__ __forceinline__ void aw_load(const T* p, int left, T (&v)[4]) {
+__device__ __forceinline__ void aw_load(Global<const T> p, int left, T (&v)[4]) {
   if constexpr (kFull) {
     typedef T vec __attribute__((ext_vector_type(4)));
-    const vec x = __builtin_nontemporal_load(reinterpret_cast<const vec*>(p));
+    const vec x = __builtin_nontemporal_load((Global<const vec>)p);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = x[j];
   } else {
@@ -67,13 +72,13 @@ __device__ __forceinline__ void aw_load(const T* p, int left, T (&v)[4]) {
   }
 }
 template <bool kFull, typename T>
-__device__ __forceinline__ void aw_store(T* p, int left, const T (&v)[4]) {
+__device__ __forceinline__ void aw_store(Global<T> p, int left, const T (&v)[4]) {
   if constexpr (kFull) {
     typedef T vec __attribute__((ext_vector_type(4)));
     vec x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = v[j];
-    __builtin_nontemporal_store(x, reinterpret_cast<vec*>(p));
+    __builtin_nontemporal_store(x, (Global<vec>)p);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -82,9 +87,9 @@ __device__ __forceinline__ void aw_store(T* p, int left, const T (&v)[4]) {
 }
 // bf16 and codes travel as words: two or four elements of one register.
 template <bool kFull>
-__device__ __forceinline__ void aw_load(const uint16_t* p, int left, uint32_t (&w)[2]) {
+__device__ __forceinline__ void aw_load(Global<const uint16_t> p, int left, uint32_t (&w)[2]) {
   if constexpr (kFull) {
-    const u32x2 x = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+    const u32x2 x = __builtin_nontemporal_load((Global<const u32x2>)p);
     w[0] = x.x;
     w[1] = x.y;
   } else {
@@ -95,9 +100,9 @@ __device__ __forceinline__ void aw_load(const uint16_t* p, int left, uint32_t (&
   }
 }
 template <bool kFull>
-__device__ __forceinline__ void aw_store(uint16_t* p, int left, const uint32_t (&w)[2]) {
+__device__ __forceinline__ void aw_store(Global<uint16_t> p, int left, const uint32_t (&w)[2]) {
   if constexpr (kFull) {
-    __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(p));
+    __builtin_nontemporal_store(u32x2{w[0], w[1]}, (Global<u32x2>)p);
   } else {
     const uint16_t v[4] = {(uint16_t)w[0], (uint16_t)(w[0] >> 16), (uint16_t)w[1],
                            (uint16_t)(w[1] >> 16)};
@@ -105,16 +110,16 @@ __device__ __forceinline__ void aw_store(uint16_t* p, int left, const uint32_t (
   }
 }
 template <bool kFull>
-__device__ __forceinline__ uint32_t aw_load_codes(const uint8_t* p, int left) {
-  if constexpr (kFull) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+__device__ __forceinline__ uint32_t aw_load_codes(Global<const uint8_t> p, int left) {
+  if constexpr (kFull) return __builtin_nontemporal_load((Global<const uint32_t>)p);
   uint8_t v[4];
   aw_load<false>(p, left, v);
   return v[0] | (uint32_t)v[1] << 8 | (uint32_t)v[2] << 16 | (uint32_t)v[3] << 24;
 }
 template <bool kFull>
-__device__ __forceinline__ void aw_store_codes(uint8_t* p, int left, uint32_t w) {
+__device__ __forceinline__ void aw_store_codes(Global<uint8_t> p, int left, uint32_t w) {
   if constexpr (kFull) {
-    __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(p));
+    __builtin_nontemporal_store(w, (Global<uint32_t>)p);
   } else {
     const uint8_t v[4] = {(uint8_t)w, (uint8_t)(w >> 8), (uint8_t)(w >> 16), (uint8_t)(w >> 24)};
     aw_store<false>(p, left, v);
@@ -126,8 +131,8 @@ template <typename T>
 struct AwFour {
   float x[4];
   template <bool kFull>
-  __device__ __forceinline__ void load(const void* p, int64_t i, int left) {
-    aw_load<kFull>(static_cast<const float*>(p) + i, left, x);
+  __device__ __forceinline__ void load(const void* p, int64_t chunk, uint32_t at, int left) {
+    aw_load<kFull>((Global<const float>)p + chunk + at, left, x);
   }
   __device__ __forceinline__ float at(int j) const { return x[j]; }
 };
@@ -135,8 +140,8 @@ template <>
 struct AwFour<uint16_t> {
   uint32_t w[2];
   template <bool kFull>
-  __device__ __forceinline__ void load(const void* p, int64_t i, int left) {
-    aw_load<kFull>(static_cast<const uint16_t*>(p) + i, left, w);
+  __device__ __forceinline__ void load(const void* p, int64_t chunk, uint32_t at, int left) {
+    aw_load<kFull>((Global<const uint16_t>)p + chunk + at, left, w);
   }
   __device__ __forceinline__ float at(int j) const {
     return j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
@@ -150,40 +155,67 @@ struct AwChunk {
   uint32_t mc, vc;                                // 8-bit states
   int tops;
   template <bool kFull>
-  __device__ __forceinline__ void load(const AwTensor& t, int64_t chunk, int64_t i, int left) {
-    p.template load<kFull>(t.t.param, i, left);
-    g.template load<kFull>(t.t.grad, i, left);
+  __device__ __forceinline__ void load(const AwTensor& t, int64_t chunk, uint32_t at, int left) {
+    p.template load<kFull>(t.t.param, chunk, at, left);
+    g.template load<kFull>(t.t.grad, chunk, at, left);
     if constexpr (k8) {
-      mc = aw_load_codes<kFull>(static_cast<const uint8_t*>(t.t.m) + i, left);
-      vc = aw_load_codes<kFull>(static_cast<const uint8_t*>(t.t.v) + i, left);
-      tops = t.t.tops[chunk / kAwChunk];
+      mc = aw_load_codes<kFull>((Global<const uint8_t>)t.t.m + chunk + at, left);
+      vc = aw_load_codes<kFull>((Global<const uint8_t>)t.t.v + chunk + at, left);
+      tops = ((Global<const int32_t>)t.t.tops)[chunk / kAwChunk];
     } else {
-      m.template load<kFull>(t.t.m, i, left);
-      v.template load<kFull>(t.t.v, i, left);
+      m.template load<kFull>(t.t.m, chunk, at, left);
+      v.template load<kFull>(t.t.v, chunk, at, left);
     }
   }
 };
 
+// x + 16 * half, or x + half, of a random word's lower or upper half, in one instruction (a
+// mask or shift of its own for the half would be a tenth of what an element costs).
+template <bool kUpper>
+__device__ __forceinline__ uint32_t aw_add16(uint32_t word, uint32_t x) {
+  uint32_t d;
+  if (kUpper) asm("v_mad_u32_u16 %0, %1, 16, %2 op_sel:[1,0,0,0]" : "=v"(d) : "v"(word), "v"(x));
+  else asm("v_mad_u32_u16 %0, %1, 16, %2" : "=v"(d) : "v"(word), "v"(x));
+  return d;
+}
+template <bool kUpper>
+__device__ __forceinline__ uint32_t aw_add(uint32_t word, uint32_t x) {
+  uint32_t d;
+  if (kUpper) asm("v_mad_u32_u16 %0, %1, 1, %2 op_sel:[1,0,0,0]" : "=v"(d) : "v"(word), "v"(x));
+  else asm("v_mad_u32_u16 %0, %1, 1, %2" : "=v"(d) : "v"(word), "v"(x));
+  return d;
+}
+
 // Value of code j of a word: its level (size - span + top), cut at 0; code 0 is zero.  kPlain:
-// the block's window lies above level 0 (top >= span), so that nothing is cut.
+// the block's window lies above level 0 and the code is not 0.
 template <bool kPlain>
 __device__ __forceinline__ float aw_decode_m(uint32_t codes, int j, int top) {
   const int size = (codes >> (8 * j)) & 127;
   int x = (size << 20) + ((top - 127) << 20);
-  if (!kPlain) x = max(x, 0);
-  return __uint_as_float((size ? (uint32_t)x : 0u) | ((codes << (24 - 8 * j)) & 0x80000000u));
+  if (!kPlain) x = size ? max(x, 0) : 0;
+  return __uint_as_float((uint32_t)x | ((codes << (24 - 8 * j)) & 0x80000000u));
 }
 template <bool kPlain>
 __device__ __forceinline__ float aw_decode_v(uint32_t codes, int j, int top) {
   const int size = (codes >> (8 * j)) & 255;
   int x = (size << 20) + ((top - 255) << 20);
-  if (!kPlain) x = max(x, 0);
-  return __uint_as_float(size ? (uint32_t)x : 0u);
+  if (!kPlain) x = size ? max(x, 0) : 0;
+  return __uint_as_float((uint32_t)x);
 }
-__device__ __forceinline__ void aw_decode(uint32_t mc, uint32_t vc, int tops, float (&m)[4],
+// Whether all four m and v codes are above zero: adding 127 to a byte's lower seven bits sets
+// its top bit unless they are 0.
+__device__ __forceinline__ bool aw_no_zero(uint32_t mc, uint32_t vc) {
+  const uint32_t m = (mc & 0x7F7F7F7Fu) + 0x7F7F7F7Fu;
+  const uint32_t v = ((vc & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | vc;
+  return (m & v & 0x80808080u) == 0x80808080u;
+}
+// The wave's four m and v each; true where the block is an ordinary one: no zeros, and every v
+// at least 2^-125 (level 16), so that one step leaves it a normal number.
+__device__ __forceinline__ bool aw_decode(uint32_t mc, uint32_t vc, int tops, float (&m)[4],
                                           float (&v)[4]) {
   const int top_m = tops & 0xFFFF, top_v = tops >> 16;
-  if (top_m >= 127 && top_v >= 255) {
+  const bool plain = top_m >= 127 && top_v >= 255 + 16 && ballot(!aw_no_zero(mc, vc)) == 0;
+  if (plain) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       m[j] = aw_decode_m<true>(mc, j, top_m);
@@ -196,49 +228,50 @@ __device__ __forceinline__ void aw_decode(uint32_t mc, uint32_t vc, int tops, fl
       v[j] = aw_decode_v<false>(vc, j, top_v);
     }
   }
+  return plain;
 }
 
 // Codes of four new m and v and their block's tops; the whole wave calls it with its chunk.
 // Levels come from the random words r; the common case, in which both windows lie above
-// level 0 and below infinity, needs no check of zeros (their code comes out below 0) and no
-// clamp.
+// level 0 and below infinity, needs no check of zeros (their code comes out as 0 by the
+// saturated difference) and no clamp.
 __device__ __forceinline__ int aw_encode(const float (&m)[4], const float (&v)[4],
                                          const uint32_t* r, int left, uint32_t* mc, uint32_t* vc) {
-  uint32_t bm[4], bv[4];
-  int lm[4], lv[4], top_m = 0, top_v = 0;
+  uint32_t bm[4], bv[4], xm[4], xv[4], max_m = 0, max_v = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const bool on = j < left;
     bm[j] = on ? __float_as_uint(m[j]) & 0x7FFFFFFFu : 0u;
     bv[j] = on ? __float_as_uint(v[j]) : 0u;      // v >= +0
-    lm[j] = (int)((bm[j] + ((r[j] & 0xFFFFu) << 4)) >> 20);
-    lv[j] = (int)((bv[j] + ((r[j] >> 16) << 4)) >> 20);
-    top_m = max(top_m, lm[j]);
-    top_v = max(top_v, lv[j]);
+    xm[j] = aw_add16<false>(r[j], bm[j]);         // the level is x >> 20
+    xv[j] = aw_add16<true>(r[j], bv[j]);
+    max_m = max(max_m, xm[j]);
+    max_v = max(max_v, xv[j]);
   }
-  top_m = wave_max(top_m);
-  top_v = wave_max(top_v);
+  int top_m = wave_max((int)max_m) >> 20, top_v = wave_max((int)max_v) >> 20;
   uint32_t cm[4], cv[4];
   if (top_m > 127 && top_v > 255 && max(top_m, top_v) <= kAwMaxLevel) {
+    const uint32_t low_m = (uint32_t)(top_m - 127) << 20, low_v = (uint32_t)(top_v - 255) << 20;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      cm[j] = (uint32_t)max(lm[j] - top_m + 127, 0);
-      cv[j] = (uint32_t)max(lv[j] - top_v + 255, (int)min(bv[j], 1u));
+      cm[j] = __builtin_elementwise_sub_sat(xm[j], low_m) >> 20;
+      cv[j] = max(__builtin_elementwise_sub_sat(xv[j], low_v) >> 20, min(bv[j], 1u));
     }
   } else {
     top_m = min(top_m, kAwMaxLevel);
     top_v = min(top_v, kAwMaxLevel);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      cm[j] = bm[j] ? (uint32_t)max(min(lm[j], kAwMaxLevel) - top_m + 127, 0) : 0u;
-      cv[j] = bv[j] ? (uint32_t)max(min(lv[j], kAwMaxLevel) - top_v + 255, 1) : 0u;
+      const int lm = min((int)(xm[j] >> 20), kAwMaxLevel), lv = min((int)(xv[j] >> 20), kAwMaxLevel);
+      cm[j] = bm[j] ? (uint32_t)max(lm - top_m + 127, 0) : 0u;
+      cv[j] = bv[j] ? (uint32_t)max(lv - top_v + 255, 1) : 0u;
     }
   }
   *mc = *vc = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t sign = __float_as_uint(m[j]) >> 24 & 128u;
-    *mc |= (cm[j] ? cm[j] | sign : 0u) << (8 * j);
+    const uint32_t signed_code = cm[j] | (__float_as_uint(m[j]) >> 24 & 128u);
+    *mc |= (cm[j] ? signed_code : 0u) << (8 * j);
     *vc |= cv[j] << (8 * j);
   }
   return top_m | top_v << 16;
@@ -272,9 +305,10 @@ __device__ __forceinline__ float aw_correction(double y) {
 // One chunk: step, round, store.
 template <typename P, typename G, bool k8, bool kFull>
 __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, k8>& in,
-                                         int64_t chunk, int64_t i, int left, const AwScalars& c,
+                                         int64_t chunk, uint32_t at, int left, const AwScalars& c,
                                          const AwArgs& a, uint32_t key) {
 #pragma clang fp contract(off)
+  const uint32_t lane_mul = (threadIdx.x % kWave) * 0x9E3779B9u;
   float g[4], m[4], v[4], w[4], root[4];
   bool bad = false, tiny = false;
 #pragma unroll
@@ -286,8 +320,10 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if ((__float_as_uint(g[j]) & 0x7F800000u) == 0x7F800000u) g[j] = 0.0f;
+  bool normal = false;                            // no new v can be subnormal
   if constexpr (k8) {
-    aw_decode(in.mc, in.vc, __builtin_amdgcn_readfirstlane(in.tops), m, v);
+    normal = aw_decode(in.mc, in.vc, __builtin_amdgcn_readfirstlane(in.tops), m, v) &&
+             a.b2 >= 0.5f;
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -302,11 +338,14 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
     // root and reciprocal by the hardware's approximations, each within a unit in the last
     // place; the root takes a subnormal number for 0, so those go the long way
     root[j] = __builtin_amdgcn_sqrtf(v[j]);
-    tiny |= __builtin_amdgcn_classf(v[j], 1 << 7);
   }
-  if (ballot(tiny))
+  if (!normal) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) root[j] = sqrtf(v[j]);
+    for (int j = 0; j < 4; ++j) tiny |= __builtin_amdgcn_classf(v[j], 1 << 7);
+    if (ballot(tiny))
+#pragma unroll
+      for (int j = 0; j < 4; ++j) root[j] = sqrtf(v[j]);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float q = m[j] * __builtin_amdgcn_rcpf(fmaf(root[j], c.root2, a.eps));
@@ -314,7 +353,8 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
   }
   uint32_t r[6] = {0};
   if constexpr (k8 || sizeof(P) == 2) {
-    r[0] = aw_mix((uint32_t)(i >> 2) * 0x9E3779B9u ^ key);
+    // the group's number times the constant, the chunk's part of it uniform
+    r[0] = aw_mix(((uint32_t)(chunk >> 2) * 0x9E3779B9u + lane_mul) ^ key);
 #pragma unroll
     for (int j = 1; j < (k8 ? 6 : 2); ++j) r[j] = aw_next(r[j - 1]);
   }
@@ -323,29 +363,29 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t bits = __float_as_uint(w[j]);
-      const uint32_t d = j & 1 ? r[j / 2] >> 16 : r[j / 2] & 0xFFFFu;
+      o[j] = j & 1 ? aw_add<true>(r[j / 2], bits) : aw_add<false>(r[j / 2], bits);
       // a NaN is cut as it is.  With 8-bit states it needs no check: it was made here or came
       // from a bf16 parameter, so its lower half is zero and nothing carries
-      o[j] = !k8 && (bits & 0x7FFFFFFFu) > 0x7F800000u ? bits : bits + d;
+      if (!k8 && (bits & 0x7FFFFFFFu) > 0x7F800000u) o[j] = bits;
     }
     const uint32_t word[2] = {o[0] >> 16 | (o[1] & 0xFFFF0000u), o[2] >> 16 | (o[3] & 0xFFFF0000u)};
-    aw_store<kFull>(static_cast<uint16_t*>(t.t.param) + i, left, word);
+    aw_store<kFull>((Global<uint16_t>)t.t.param + chunk + at, left, word);
   } else {
-    aw_store<kFull>(static_cast<float*>(t.t.param) + i, left, w);
+    aw_store<kFull>((Global<float>)t.t.param + chunk + at, left, w);
     if (t.t.copy) {
       const uint32_t word[2] = {pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
-      aw_store<kFull>(t.t.copy + i, left, word);
+      aw_store<kFull>((Global<uint16_t>)t.t.copy + chunk + at, left, word);
     }
   }
   if constexpr (k8) {
     uint32_t mc, vc;
     const int tops = aw_encode(m, v, r + 2, kFull ? 4 : left, &mc, &vc);
-    aw_store_codes<kFull>(static_cast<uint8_t*>(t.t.m) + i, left, mc);
-    aw_store_codes<kFull>(static_cast<uint8_t*>(t.t.v) + i, left, vc);
-    if (threadIdx.x % kWave == 0) t.t.tops[chunk / kAwChunk] = tops;
+    aw_store_codes<kFull>((Global<uint8_t>)t.t.m + chunk + at, left, mc);
+    aw_store_codes<kFull>((Global<uint8_t>)t.t.v + chunk + at, left, vc);
+    if (threadIdx.x % kWave == 0) ((Global<int32_t>)t.t.tops)[chunk / kAwChunk] = tops;
   } else {
-    aw_store<kFull>(static_cast<float*>(t.t.m) + i, left, m);
-    aw_store<kFull>(static_cast<float*>(t.t.v) + i, left, v);
+    aw_store<kFull>((Global<float>)t.t.m + chunk + at, left, m);
+    aw_store<kFull>((Global<float>)t.t.v + chunk + at, left, v);
   }
   return bad;
 }
@@ -355,7 +395,7 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
 template <typename P, typename G, bool k8, int kU, bool kFull>
 __device__ __forceinline__ bool aw_tile(const AwTensor& t, int64_t base, const AwScalars& c,
                                         const AwArgs& a, uint32_t key) {
-  const int lane = threadIdx.x % kWave;
+  const uint32_t at = threadIdx.x % kWave * 4;    // the lane's elements in a chunk
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   bool bad = false;
   constexpr int kAhead = kFull ? kU : 1;
@@ -365,15 +405,13 @@ __device__ __forceinline__ bool aw_tile(const AwTensor& t, int64_t base, const A
 #pragma unroll
     for (int h = 0; h < kAhead; ++h) {
       const int64_t chunk = base + (int64_t)((u + h) * kAwWaves + wave) * kAwChunk;
-      const int64_t i = chunk + lane * 4;
-      in[h].template load<kFull>(t, chunk, i, (int)min((int64_t)4, t.t.n - i));
+      in[h].template load<kFull>(t, chunk, at, (int)min((int64_t)4, t.t.n - chunk - at));
     }
 #pragma unroll
     for (int h = 0; h < kAhead; ++h) {
       const int64_t chunk = base + (int64_t)((u + h) * kAwWaves + wave) * kAwChunk;
-      const int64_t i = chunk + lane * 4;
-      bad |= aw_chunk<P, G, k8, kFull>(t, in[h], chunk, i, (int)min((int64_t)4, t.t.n - i), c, a,
-                                       key);
+      bad |= aw_chunk<P, G, k8, kFull>(t, in[h], chunk, at,
+                                       (int)min((int64_t)4, t.t.n - chunk - at), c, a, key);
     }
   }
   return bad;
@@ -431,27 +469,29 @@ __global__ __launch_bounds__(kAwThreads) void adamw_decode_kernel(
   if (i >= n) return;
   const int top = tops[i / kAwChunk], left = (int)min((int64_t)4, n - i);
   const bool full = vec && left == 4;
-  const uint32_t cm = full ? aw_load_codes<true>(mc + i, 4) : aw_load_codes<false>(mc + i, left);
-  const uint32_t cv = full ? aw_load_codes<true>(vc + i, 4) : aw_load_codes<false>(vc + i, left);
+  const uint32_t cm = full ? aw_load_codes<true>((Global<const uint8_t>)mc + i, 4)
+                           : aw_load_codes<false>((Global<const uint8_t>)mc + i, left);
+  const uint32_t cv = full ? aw_load_codes<true>((Global<const uint8_t>)vc + i, 4)
+                           : aw_load_codes<false>((Global<const uint8_t>)vc + i, left);
   float a[4], b[4];
   aw_decode(cm, cv, __builtin_amdgcn_readfirstlane(top), a, b);   // a wave is one block
   if constexpr (sizeof(T) == 4) {
     if (full) {
-      aw_store<true>(m + i, 4, a);
-      aw_store<true>(v + i, 4, b);
+      aw_store<true>((Global<T>)m + i, 4, a);
+      aw_store<true>((Global<T>)v + i, 4, b);
     } else {
-      aw_store<false>(m + i, left, a);
-      aw_store<false>(v + i, left, b);
+      aw_store<false>((Global<T>)m + i, left, a);
+      aw_store<false>((Global<T>)v + i, left, b);
     }
   } else {
     const uint32_t wa[2] = {pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3])};
     const uint32_t wb[2] = {pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3])};
     if (full) {
-      aw_store<true>(m + i, 4, wa);
-      aw_store<true>(v + i, 4, wb);
+      aw_store<true>((Global<T>)m + i, 4, wa);
+      aw_store<true>((Global<T>)v + i, 4, wb);
     } else {
-      aw_store<false>(m + i, left, wa);
-      aw_store<false>(v + i, left, wb);
+      aw_store<false>((Global<T>)m + i, left, wa);
+      aw_store<false>((Global<T>)v + i, left, wb);
     }
   }
 }
