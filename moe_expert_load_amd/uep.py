@@ -494,41 +494,47 @@ def adamw_prepare(params, grads, m, v, copies=None, tops=None, weight_decay=0.0,
     if copies is not None and pd != F32:
         raise TypeError("copies go with float32 params")
     wd, ls = _per_tensor(weight_decay, n, "weight_decay"), _per_tensor(lr_scale, n, "lr_scale")
-    table = (AdamWTensor * max(n, 1))()
-    written = []
-    for i in range(n):
-        k = params[i].numel()
-        want = [(params[i], params[0].dtype, k, "params"), (grads[i], grads[0].dtype, k, "grads"),
-                (m[i], state, k, "m"), (v[i], state, k, "v")]
-        if bits == 8:
-            want.append((tops[i], torch.int32, -(-k // ADAMW_BLOCK), "tops"))
-        if copies is not None:
-            want.append((copies[i], torch.bfloat16, k, "copies"))
-        for t, dt, size, name in want:
-            if t.dtype != dt or t.numel() != size or t.device != params[0].device:
-                raise TypeError(f"{name}[{i}] must be {dt} with {size} elements on "
-                                f"{params[0].device}, got {t.dtype}, {t.numel()}, {t.device}")
-        for t, dt, size, name in want:
-            _p(t)
-            if name != "grads" and size:
-                written.append((t.data_ptr(), t.data_ptr() + size * t.element_size(),
-                                f"{name}[{i}]"))
-        table[i] = AdamWTensor(params[i].data_ptr(), grads[i].data_ptr(), m[i].data_ptr(),
-                               v[i].data_ptr(), tops[i].data_ptr() if bits == 8 else None,
-                               copies[i].data_ptr() if copies is not None else None, k, wd[i],
-                               ls[i])
-    written.sort()
-    for a, b in zip(written, written[1:]):
-        if b[0] < a[1]:
-            raise TypeError(f"{a[2]} and {b[2]} overlap: one step would write them twice")
-    ends = [w[1] for w in written]
-    for i, t in enumerate(grads):
-        at = bisect.bisect_right(ends, t.data_ptr())
-        if t.numel() and at < len(written) and \
-                written[at][0] < t.data_ptr() + t.numel() * t.element_size():
-            raise TypeError(f"grads[{i}] overlaps {written[at][2]}, which the step writes")
-    need = int(LIB.uep_adamw_plan_size(table, n))
+    sizes = [p.numel() for p in params]
     dev = params[0].device if n else torch.device("cuda" if device is None else device)
+    lists = [("params", params, params[0].dtype if n else None, sizes),
+             ("grads", grads, grads[0].dtype if n else None, sizes), ("m", m, state, sizes),
+             ("v", v, state, sizes)]
+    if bits == 8:
+        lists.append(("tops", tops, torch.int32, [-(-k // ADAMW_BLOCK) for k in sizes]))
+    if copies is not None:
+        lists.append(("copies", copies, torch.bfloat16, sizes))
+    for name, tensors, dt, want in lists:
+        for i, t in enumerate(tensors):
+            if t.dtype != dt or t.numel() != want[i] or t.device != dev:
+                raise TypeError(f"{name}[{i}] must be {dt} with {want[i]} elements on {dev}, got "
+                                f"{t.dtype}, {t.numel()}, {t.device}")
+    if n and not params[0].is_cuda:
+        raise TypeError("the library takes device memory: got tensors on " + str(dev))
+    at, written = {}, []
+    for name, tensors, _, want in lists:
+        if not all(t.is_contiguous() for t in tensors):
+            raise TypeError(f"{name}: the library takes contiguous tensors")
+        at[name] = [t.data_ptr() for t in tensors]
+        if name != "grads" and n:
+            size = tensors[0].element_size()
+            written += [(p, p + k * size, name, i)
+                        for i, (p, k) in enumerate(zip(at[name], want)) if k]
+    written.sort()
+    for x, y in zip(written, written[1:]):
+        if y[0] < x[1]:
+            raise TypeError(f"{x[2]}[{x[3]}] and {y[2]}[{y[3]}] overlap: one step would write "
+                            "them twice")
+    ends = [w[1] for w in written]
+    for i, p in enumerate(at["grads"]):
+        k = bisect.bisect_right(ends, p)
+        if sizes[i] and k < len(written) and written[k][0] < p + sizes[i] * grads[i].element_size():
+            raise TypeError(f"grads[{i}] overlaps {written[k][2]}[{written[k][3]}], which the step "
+                            "writes")
+    none = [None] * n
+    rows = zip(at["params"], at["grads"], at["m"], at["v"], at.get("tops", none),
+               at.get("copies", none), sizes, wd, ls)
+    table = (AdamWTensor * max(n, 1))(*[AdamWTensor(*row) for row in rows])
+    need = int(LIB.uep_adamw_plan_size(table, n))
     buf = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
     tiles = ctypes.c_int64(0)
     _check(LIB.uep_adamw_prepare(table, n, pd, gd, bits, _p(buf), buf.numel(),
