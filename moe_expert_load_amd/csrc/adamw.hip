@@ -1,20 +1,34 @@
 // AdamW over many tensors in one launch, states in fp32 or 8 bits (uep.h: AdamW).
 //
-// HBM-bound: every element's parameter, gradient and states are read once and written
-// once.  The plan lists the work as tiles of 1024 or 4096 elements of one tensor each; a
-// 256-thread workgroup takes one tile, each wave one or four chunks of 256 consecutive elements
-// (four per lane: 16-byte accesses for fp32, 8 for bf16, 4 for the codes).  A chunk is a
-// block of the 8-bit states, so a block's largest level is one reduction over a wave.
+// Every element's parameter, gradient and states are read once and written once.  The plan
+// lists the work as tiles of 1024 or 4096 elements of one tensor each; a 256-thread workgroup
+// takes one tile, each wave one or four chunks of 256 consecutive elements (four per lane:
+// 16-byte accesses for fp32, 8 for bf16, 4 for the codes).  A chunk is a block of the 8-bit
+// states, so a block's largest level is one reduction over a wave.
+//
+// Measured on MI355X, 302 M elements in 16 tensors: fp32 states, fp32 parameters and gradients
+// with bf16 copies (30 bytes an element) 1520-1650 us by the buffers' placement, 5.5-5.9 TB/s,
+// bound by HBM: a large copy reaches 5.65.  bf16 parameters and gradients with 8-bit states
+// (10 bytes an element) 560-610 us, bound by its instructions: 72 for every element, of which
+// the random words take 10, the codes' way in 12 and out 20.  The decode 325 us, 5.6 TB/s.
+// Non-temporal accesses are worth 5 % with fp32 states (1700 -> 1610 us, each byte is used
+// once a step), one chunk per wave against four 1-2 % there and 28 % of a small call
+// (1.5 M elements in 96 tensors 13.9 -> 9.9 us); with 8-bit states four chunks per wave against
+// one 12 % (1084 -> 954 us with the decode), since a tile's own work counts beside them.
 #include <stdlib.h>
 
 #include "common.h"
+#include "numeric.h"
 
 namespace uep {
 
 constexpr int kAwThreads = 256;
 constexpr int kAwWaves = kAwThreads / kWave;
 constexpr int kAwChunk = 4 * kWave;               // elements of a wave's chunk = state block
-constexpr int kAwLong = 4;                        // chunks per wave of a long tile
+// Chunks per wave of a long tile, and the elements from which on 8-bit states take them.  Four
+// chunks against one, bf16 parameters and gradients: 64 K elements 7.2 against 4.9 us, 2 M 9.8 /
+// 9.2, 4 M 13.9 / 14.1, 8 M 21.0 / 24.2, 32 M 68.9 / 80.6.
+constexpr int kAwLong = 4;
 constexpr int64_t kAwLongFrom = 4ll << 20;
 constexpr int32_t kAwMagic = 0x41645757;
 constexpr int kAwMaxLevel = 0x7F7;                // largest finite: exponent 254, mantissa 7

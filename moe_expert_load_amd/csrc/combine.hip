@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "common.h"
+#include "numeric.h"
 
 namespace uep {
 
@@ -26,9 +27,9 @@ constexpr int kCbThreads = 256;
 constexpr int kCbTokPerBlock = kCbThreads / kWave;
 constexpr int kCbVec = 4;     // 16-byte vectors per lane per slice (8 bf16 each)
 // Up to this many tokens, which leave SIMDs without a wave, a token's slices go to up to 16
-// waves instead of one after the other to one (1 token, K = 9, 14 KiB rows: 16.7 -> 6.2 us; 512
-// tokens 26.1 -> 13.9).
-constexpr int64_t kCbFew = 512;
+// waves instead of one after the other to one.  Apart against together (K = 9, 14 KiB rows, in a
+// graph): 128 tokens 7.2 against 16.0 us, 512 13.8 / 20.7, 1024 27.8 / 28.6, 2048 58.7 / 56.3.
+constexpr int64_t kCbFew = 1024;
 constexpr int64_t kCbLaunch = 1ll << 25;   // tokens of one launch, which holds below 2^32 threads
 
 // kVec vectors per lane hold a slice of a row (a whole row where it is shorter than a slice of

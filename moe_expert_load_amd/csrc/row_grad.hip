@@ -27,6 +27,7 @@
 #include <algorithm>
 
 #include "common.h"
+#include "numeric.h"
 
 namespace uep {
 
@@ -34,8 +35,8 @@ constexpr int kRgThreads = 256;
 constexpr int kRgTokPerBlock = kRgThreads / kWave;
 constexpr int kRgVec = 8;     // 16-byte vectors in flight per lane for each of the two row groups
 // Up to this many tokens, which leave SIMDs without a wave, a token's slots go to a wave each
-// instead of one after the other to one (1 token, K = 8, 8 KiB rows: 22.7 -> 4.7 us; 512
-// tokens 27.2 -> 17.1).
+// instead of one after the other to one.  Apart against together (K = 8, 8 KiB rows, in a
+// graph): 128 tokens 5.5 against 10.6 us, 512 17.1 / 19.7, 1024 28.7 / 27.0.
 constexpr int64_t kRgFew = 512;
 constexpr int64_t kRgPhaseBytes = 48ll << 20;
 constexpr int64_t kRgChunkBytes = 224ll << 20;
