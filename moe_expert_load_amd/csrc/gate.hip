@@ -46,7 +46,7 @@ __device__ __forceinline__ bool gt_bad(float x) {
   return !gt_finite(x) && __float_as_uint(x) != 0xFF800000u;
 }
 
-// exp(x) for x <= 0 in units of 2^-24: the argument, rounded twice, is 2 |x| off, exp2 two more.
+// exp(x); in units of 2^-24 the argument, rounded twice, is 2 |x| off, exp2 two more.
 __device__ __forceinline__ float gt_exp(float x) {
   return __builtin_amdgcn_exp2f(1.44269504f * x);
 }
@@ -343,13 +343,14 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     }
     total = gt_lanes_sum<kL>(z);
   }
-  const float norm = total > 0.0f ? scale / total : 0.0f;
+  // sums of sigmoids go down to 2^-126: the reciprocal before the scale, which could overflow it
+  const float norm = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int k = lane * kSlots + i;
     if (g < n_tok && k < K) {
       topk_ids[g * K + k] = id[i];
-      gate_w[g * K + k] = s[i] * norm;
+      gate_w[g * K + k] = s[i] * norm * scale;
     }
   }
 }
@@ -430,7 +431,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
   }
   if (lane < K) {
     topk_ids[g * K + lane] = id_mine;
-    gate_w[g * K + lane] = total > 0.0f ? s * (scale / total) : 0.0f;
+    gate_w[g * K + lane] = total > 0.0f ? s * (1.0f / total) * scale : 0.0f;
   }
 }
 

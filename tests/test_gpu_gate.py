@@ -171,6 +171,17 @@ def test_special_logits(dtype):
     assert np.isfinite(w).all()
 
 
+@pytest.mark.parametrize("E,K", [(16, 1), (16, 4), (40, 20)])
+def test_renormalised_weights_of_tiny_scores(E, K):
+    """Sigmoid scores near the smallest fp32 number still share out the scale."""
+    say("case: gate tiny scores", E, K)
+    x = torch.full((1, 3, E), -87.0)
+    x[0, 1] = -86.5
+    x[0, 2, ::2] = -86.9
+    _, w, err = run_gate(x, K, score=1, renorm=True, scale=50.0)
+    assert err == 0 and np.abs(w.sum(-1) - 50.0).max() < 50.0 * (K + 40) * EPS
+
+
 def test_bias_may_mask_experts():
     say("case: gate bias masks")
     x = torch.arange(12, dtype=torch.float32).view(1, 1, 12) / 4
