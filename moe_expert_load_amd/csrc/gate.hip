@@ -484,7 +484,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
     const bool on = id >= 0;
     const float gk = on ? scale * dgate_w[g * K + k] : 0.0f;
     const float u = on ? gate_w[g * K + k] / scale : 0.0f;
-    const float l = on && (kDense || (score && renorm)) ? gt_load(logits, g * E + id) : 0.0f;
+    const float l = on && (kDense || score) ? gt_load(logits, g * E + id) : 0.0f;
     float dot = u * gk;
     for (int o = kp / 2; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
     float d;
@@ -519,7 +519,8 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
       }
       if (k == 0) par[tok] = f32x4{lr, fmaxf(ur, 0.0f), dot, 0.0f};
     } else if (score) {
-      d = renorm ? u * gt_sigmoid(-l) * (gk - dot) : u * (1.0f - u) * gk;
+      // 1 - s as the score of -l: the difference would lose its digits near s = 1
+      d = u * gt_sigmoid(-l) * (renorm ? gk - dot : gk);
     } else {
       d = u * (gk - dot);
     }

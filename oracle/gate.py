@@ -65,19 +65,21 @@ def gate(logits, K, bias=None, batch_size=None, score=SOFTMAX, renorm=True, scal
 def gate_grad(dgate_w, logits, topk_ids, gate_w, score=SOFTMAX, renorm=True, scale=1.0):
     """dlogits float64 [R][T][E]: the chain rule through gate's weights with the selection
     held fixed (gate_w as gate returned it)."""
-    s, _ = _scores(logits, score)
+    s, able = _scores(logits, score)
     ids = np.asarray(topk_ids)
     on = ids >= 0
     at = np.where(on, ids, 0)
+    picked = np.take_along_axis(np.where(able, np.asarray(logits, dtype=np.float64), 0.0), at, -1)
+    rest = _sigmoid(-picked)                # 1 - s, which as a difference loses digits near 1
     g = np.where(on, np.asarray(dgate_w, dtype=np.float64) * scale, 0.0)
     u = np.where(on, np.asarray(gate_w, dtype=np.float64) / scale, 0.0)
     dot = (u * g).sum(-1, keepdims=True)
     if renorm:
         d = u * (g - dot)
         if score == SIGMOID:
-            d = d * (1.0 - np.take_along_axis(s, at, -1))
+            d = d * rest
     else:
-        d = u * (1.0 - u) * g if score == SIGMOID else g
+        d = u * rest * g if score == SIGMOID else g
     out = np.zeros(s.shape)
     for k in range(ids.shape[-1]):
         r, t = np.nonzero(on[..., k])

@@ -250,3 +250,33 @@ def test_captured_graph_replays():
         i2, w2 = U.gate(x, 8)
         assert torch.equal(ids, i2) and torch.equal(w, w2)
         assert torch.equal(dl, U.gate_grad(dw, x, i2, w2))
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_gradient_keeps_its_digits(dtype, renorm):
+    """Scores near 1, where the difference 1 - s loses its digits (at a logit of 12 it is 1 % off,
+    from 17 on it is 0).  The bound is relative to the gradient: 1 - s by its exponential
+    |l| + 2 <= 82 units of 2^-24, its sum and reciprocal 3, the weight without its scale 1, the
+    scaled dw 1, the dot product K + 1, the products 3; the four weights are alike, so that no
+    difference of theirs cancels by more than two bits (4 + 4).  104 in all."""
+    say("case: gate_grad, scores near one", dtype, renorm)
+    E, K = 64, 4
+    x = torch.full((1, 12, E), -20.0)
+    for t, top in enumerate((3.0, 8.0, 10.0, 12.0, 14.0, 16.0, 17.0, 18.0, 22.0, 30.0, 50.0, 80.0)):
+        x[0, t, torch.tensor([9, 33, 5, 60])] = torch.tensor([top, top - 0.5, top - 1.0, top - 2.0])
+    x = x.to(dtype)
+    ids, w, err = run_gate(x, K, score=1, renorm=renorm, scale=2.5)
+    assert err == 0 and sorted(ids[0, 0].tolist()) == [5, 9, 33, 60]
+    ids = np.broadcast_to(np.array([9, 33, 5, 60], np.int32), ids.shape)
+    s = 1.0 / (1.0 + np.exp(-np.take_along_axis(x.double().numpy(), ids, -1)))
+    w = (2.5 * (s / s.sum(-1, keepdims=True) if renorm else s)).astype(np.float32)
+    for k in range(K):
+        dw = np.zeros((1, 12, K), np.float32)
+        dw[..., k] = 1.25
+        d = host(U.gate_grad(to_dev(dw, torch.float32), x.to(DEV), to_dev(ids),
+                             to_dev(w, torch.float32), score=1, renorm=renorm, scale=2.5).float())
+        want = O.gate_grad(dw, x.double().numpy(), ids, w, 1, renorm, 2.5)
+        tol = EPS * 104 + (2.0 ** -8 if dtype == B else 0.0)
+        assert (np.abs(d - want) <= tol * np.abs(want)).all()
+        assert (d != 0).sum() == 12 * (K if renorm else 1)

@@ -92,3 +92,18 @@ def test_row_gradients_against_differences():
     for r, t in np.ndindex(R, T):
         rows = [j for j in d[r, t] if j >= 0]
         assert np.array_equal(dx[r, t], f32_to_bf16_bits(o64[rows].sum(0).astype(np.float32)))
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_gradient_keeps_its_digits_near_one(renorm):
+    """ds/dl = exp(-l) / (1 + exp(-l))^2, for one slot without renormalisation and, with it, of
+    s0 / (s0 + s1) in s0; products and quotients of a few terms in 64 bits."""
+    for top in (12.0, 30.0, 45.0):
+        x = np.array([[[top, 0.5, -3.0]]])
+        ids, w = O.gate(x, 2, score=SIGMOID, renorm=renorm)
+        assert ids.tolist() == [[[0, 1]]]
+        d = O.gate_grad(np.array([[[1.0, 0.0]]]), x, ids, w, SIGMOID, renorm)[0, 0]
+        e0, e1 = np.exp(-top), np.exp(-0.5)
+        ds, s0, s1 = e0 / (1 + e0) ** 2, 1 / (1 + e0), 1 / (1 + e1)
+        want = ds * s1 / (s0 + s1) ** 2 if renorm else ds
+        assert abs(d[0] / want - 1) < 1e-13 and d[2] == 0
