@@ -457,8 +457,8 @@ uep_status uep_lplb_sample(const int32_t* topk_ids, int32_t R, int32_t T, int32_
  * this is that Gate, so that a layer goes from router logits to the load matrix
  * (topk_ids) and the combine (gate_w) without leaving the library.
  *   scores     softmax: s_e = exp(l_e) / sum_j exp(l_j);  sigmoid: s_e = 1/(1 + exp(-l_e))
- *   selection  the K largest of l_e (softmax) or of s_e + bias_e (sigmoid), in descending
- *              order, ties to the lowest expert id
+ *   selection  the K largest of l_e, or of s_e + bias_e (fp32) where a bias is given, in
+ *              descending order, ties to the lowest expert id
  *   weights    w_k = scale * s_k, or with renorm scale * s_k / sum over the selected s
  *              (all weights 0 if that sum is 0)
  * Only finite logits are eligible (and enter the softmax's sum): -infinity, of the logit

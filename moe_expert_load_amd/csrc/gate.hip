@@ -216,12 +216,14 @@ __device__ __forceinline__ float gt_element(u32x4 w, int j) {
   return j & 1 ? bf16_hi(w[j / 2 & 3]) : bf16_lo(w[j / 2 & 3]);
 }
 
-template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
+// kBias: ranked by sigmoid score plus bias; otherwise by the logits, whose order is that of
+// either score (fp32 scores of different logits can be the same number: 1 above a logit of 17).
+template <typename T, typename KY, bool kBias, int kL, int kN, int kPer>
 __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
     const int32_t* __restrict__ batch_size, int64_t n_tok, int tok_per_rank, int E, int K,
-    int renorm, float scale, int32_t* __restrict__ topk_ids, float* __restrict__ gate_w,
-    int32_t* err) {
+    int score, int renorm, float scale, int32_t* __restrict__ topk_ids,
+    float* __restrict__ gate_w, int32_t* err) {
   typedef typename KY::type key_t;
   constexpr int kCe = 16 / sizeof(T);                 // experts of one 16-byte load
   constexpr int kChunks = kPer / kCe;
@@ -242,10 +244,10 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
       raw[c] = gt_load16<true>(row, (c * kL + lane) * kCe, e_end);
   }
   bool bad = false, odd_bias = false;
-  __shared__ __attribute__((aligned(16))) float bias_lds[kSigmoid ? kL * kPer : 4];
-  if (kSigmoid) {
+  __shared__ __attribute__((aligned(16))) float bias_lds[kBias ? kL * kPer : 4];
+  if (kBias) {
     for (int e = threadIdx.x; e < kL * kPer; e += kGtThreads) {
-      const float y = bias && e < E ? bias[e] : 0.0f;
+      const float y = e < E ? bias[e] : 0.0f;
       bad |= gt_bad(y);
       bias_lds[e] = y;
     }
@@ -261,10 +263,10 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     for (int i = 0; i < kN; ++i) {
       const int n = q * kN + i;
       f[i] = gt_element<T>(raw[n / kCe], n % kCe);
-      // softmax: NaN and +infinity (bits 0, 1, 9); -infinity is ranked as it is
-      odd |= kSigmoid ? !gt_finite(f[i]) : __builtin_amdgcn_classf(f[i], 0x203);
+      // by logits: NaN and +infinity (bits 0, 1, 9); -infinity is ranked as it is
+      odd |= kBias ? !gt_finite(f[i]) : __builtin_amdgcn_classf(f[i], 0x203);
     }
-    if (kSigmoid) {
+    if (kBias) {
       float y[kN];
 #pragma unroll
       for (int h = 0; h < kN; h += 4) {
@@ -315,7 +317,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
   if (kL >= 16) gt_merge_lanes<KY, 0x140>(best);      // the other half of 16 (row_mirror)
 
   constexpr int kSlots = kN > kL ? kN / kL : 1;       // a lane's slots, consecutive
-  const float top = KY::rank(best[0]);                // softmax: the largest logit
+  const float top = KY::rank(best[0]);                // by logits: the largest
   int id[kSlots];
   float s[kSlots], mine = 0.0f;
 #pragma unroll
@@ -328,13 +330,13 @@ __global__ __launch_bounds__(kGtThreads) void gate_sort_kernel(
     const bool on = f > kGtMasked && lane * kSlots + i < K;
     id[i] = on ? KY::id(k) : -1;
     s[i] = 0.0f;
-    if (on) s[i] = kSigmoid ? gt_sigmoid(gt_load(row, id[i])) : gt_exp(f - top);
+    if (on) s[i] = kBias ? gt_sigmoid(gt_load(row, id[i])) : score ? gt_sigmoid(f) : gt_exp(f - top);
     mine += s[i];
   }
   float total = 1.0f;
   if (renorm) {
     total = gt_lanes_sum<kL>(mine);
-  } else if (!kSigmoid) {
+  } else if (!kBias && !score) {
     float z = 0.0f;
 #pragma unroll
     for (int n = 0; n < kPer; ++n) {
@@ -397,8 +399,8 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     val[j] = x;
     bad |= gt_bad(x);
     float f = x + 0.0f;
-    if (score && gt_finite(x)) {
-      f = gt_sigmoid(x) + (bias ? bias[e] : 0.0f);
+    if (bias && gt_finite(x)) {                       // ranked as in the sorting kernel
+      f = gt_sigmoid(x) + bias[e];
       bad |= gt_bad(f);
     }
     key[j] = gt_finite(f) ? Key64::make(f, kGtInv, e) : none;
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     if (m == none) break;
 #pragma unroll
     for (int j = 0; j < kVpt; ++j) key[j] = key[j] == m ? none : key[j];
-    if (k == 0) top = Key64::rank(m);                 // softmax: the largest logit
+    if (k == 0) top = Key64::rank(m);                 // by logits: the largest
     if (lane == k) id_mine = Key64::id(m);
   }
   const bool on = id_mine >= 0;
@@ -611,12 +613,12 @@ struct GtCall {
 // workgroups for n_tok < 2^26 tokens, at least 4 each: a launch holds below 2^32 threads
 static unsigned gt_blocks(int64_t n_tok, int per) { return (unsigned)((n_tok + per - 1) / per); }
 
-template <typename T, typename KY, bool kSigmoid, int kL, int kN, int kPer>
+template <typename T, typename KY, bool kBias, int kL, int kN, int kPer>
 static uep_status gt_sorted(const GtCall& c) {
   const unsigned blocks = gt_blocks(c.n_tok, kGtThreads / kL);
-  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kSigmoid, kL, kN, kPer>), dim3(blocks), dim3(kGtThreads),
+  hipLaunchKernelGGL((gate_sort_kernel<T, KY, kBias, kL, kN, kPer>), dim3(blocks), dim3(kGtThreads),
                      0, c.stream, static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok,
-                     c.T, c.E, c.K, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
+                     c.T, c.E, c.K, c.score, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }
@@ -631,26 +633,26 @@ static uep_status gt_general(const GtCall& c) {
   return UEP_OK;
 }
 
-template <typename T, typename KY, bool kSigmoid, int kL, int kPer>
+template <typename T, typename KY, bool kBias, int kL, int kPer>
 static uep_status gt_by_slots(const GtCall& c) {
-  return c.K <= 4   ? gt_sorted<T, KY, kSigmoid, kL, 4, kPer>(c)
-         : c.K <= 8 ? gt_sorted<T, KY, kSigmoid, kL, 8, kPer>(c)
-                    : gt_sorted<T, KY, kSigmoid, kL, 16, kPer>(c);
+  return c.K <= 4   ? gt_sorted<T, KY, kBias, kL, 4, kPer>(c)
+         : c.K <= 8 ? gt_sorted<T, KY, kBias, kL, 8, kPer>(c)
+                    : gt_sorted<T, KY, kBias, kL, 16, kPer>(c);
 }
 
-template <typename T, typename KY, bool kSigmoid>
+template <typename T, typename KY, bool kBias>
 static uep_status gt_by_experts(const GtCall& c) {
-  if (c.n_tok <= kGtFew && c.E <= 16 * 32) return gt_by_slots<T, KY, kSigmoid, 16, 32>(c);
-  if (c.E <= 4 * 32) return gt_by_slots<T, KY, kSigmoid, 4, 32>(c);
-  if (c.E <= 4 * 64) return gt_by_slots<T, KY, kSigmoid, 4, 64>(c);
-  if (c.E <= 8 * 64) return gt_by_slots<T, KY, kSigmoid, 8, 64>(c);
-  return gt_by_slots<T, KY, kSigmoid, 16, 64>(c);
+  if (c.n_tok <= kGtFew && c.E <= 16 * 32) return gt_by_slots<T, KY, kBias, 16, 32>(c);
+  if (c.E <= 4 * 32) return gt_by_slots<T, KY, kBias, 4, 32>(c);
+  if (c.E <= 4 * 64) return gt_by_slots<T, KY, kBias, 4, 64>(c);
+  if (c.E <= 8 * 64) return gt_by_slots<T, KY, kBias, 8, 64>(c);
+  return gt_by_slots<T, KY, kBias, 16, 64>(c);
 }
 
 template <typename T>
 static uep_status gt_launch(const GtCall& c) {
   if (c.K <= 16 && c.E <= kGtSortE && c.E >= 16 / (int)sizeof(T)) {
-    if (c.score == UEP_GATE_SIGMOID) return gt_by_experts<T, Key64, true>(c);
+    if (c.bias) return gt_by_experts<T, Key64, true>(c);
     typedef typename std::conditional<sizeof(T) == 2, Key32, Key64>::type key;
     return gt_by_experts<T, key, false>(c);
   }

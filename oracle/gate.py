@@ -6,7 +6,8 @@ reading here is the standard one of the layers they measure (softmax over all ex
 sigmoid with a selection bias, top-k, optionally renormalised weights):
 
   * scores s_e = exp(l_e) / sum_j exp(l_j), or s_e = 1 / (1 + exp(-l_e));
-  * selection by l_e, or by s_e + bias_e, descending, ties to the lowest id;
+  * selection by l_e, or by s_e + bias_e where a bias is given, descending, ties to the lowest
+    id (a sigmoid without a bias orders like its logits, also where its scores round alike);
   * w_k = scale * s_k, or scale * s_k / (sum over the selected s), 0 if that sum is 0;
   * only finite logits (and finite s_e + bias_e) are eligible; slots past the eligible
     experts, and absent tokens, hold id -1 and weight 0.
@@ -41,8 +42,8 @@ def _scores(logits, score):
 def gate_keys(logits, bias=None, score=SOFTMAX):
     """What the selection orders by; -inf where an expert is not eligible."""
     s, able = _scores(logits, score)
-    key = np.asarray(logits, dtype=np.float64) if score == SOFTMAX else \
-        s + (0.0 if bias is None else np.asarray(bias, dtype=np.float64))
+    key = np.asarray(logits, dtype=np.float64) if score == SOFTMAX or bias is None else \
+        s + np.asarray(bias, dtype=np.float64)
     return np.where(able & np.isfinite(key), key, -np.inf)
 
 

@@ -280,3 +280,34 @@ def test_sigmoid_gradient_keeps_its_digits(dtype, renorm):
         tol = EPS * 104 + (2.0 ** -8 if dtype == B else 0.0)
         assert (np.abs(d - want) <= tol * np.abs(want)).all()
         assert (d != 0).sum() == 12 * (K if renorm else 1)
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("R,T,E,K", [
+    (1, 9, 64, 1), (2, 300, 40, 4), (1, 50, 300, 8), (1, 21, 40, 20), (1, 17, 1100, 8),
+    (3, 3001, 128, 8), (2, 4500, 256, 16),                       # more than 8192 tokens
+])
+def test_sigmoid_without_a_bias_orders_by_the_logits(dtype, R, T, E, K):
+    """Without a bias the scores' order is the logits' order, also where scores that differ are
+    the same fp32 number: 1 above a logit of 17, 0 below -88."""
+    say("case: gate, sigmoid without a bias", dtype, R, T, E, K)
+    g = torch.Generator().manual_seed(70 + E)
+    x = 40.0 * torch.randn(R, T, E, generator=g)
+    x[0, 0, :2] = torch.tensor([17.5, 30.0])
+    x[0, 0, 2:] = 1.0
+    x[0, 1] = -90.0 - torch.arange(E)
+    x[0, 2] = 20.0 + torch.arange(E)
+    x[0, 3, ::2] = -float("inf")
+    x[0, 4, :] = torch.tensor([0.0, -0.0] * (E // 2))
+    x = x.to(dtype)
+    x64 = x.double().numpy()
+    for renorm in (True, False):
+        ids, w, err = run_gate(x, K, score=1, renorm=renorm, scale=1.5)
+        ids_o, w_o = O.gate(x64, K, score=1, renorm=renorm, scale=1.5)
+        assert err == 0
+        assert np.array_equal(ids, ids_o)
+        top = np.take_along_axis(x64, np.maximum(ids_o, 0), -1).max(-1)
+        near = top > -80                            # scores below 2^-126 count as 0
+        tol = EPS * (2 * 88 + 40) * np.abs(w_o) + 1e-37
+        assert (np.abs(w - w_o) <= tol)[near].all()
+        assert np.isfinite(w).all()

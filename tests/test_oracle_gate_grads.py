@@ -107,3 +107,9 @@ def test_sigmoid_gradient_keeps_its_digits_near_one(renorm):
         ds, s0, s1 = e0 / (1 + e0) ** 2, 1 / (1 + e0), 1 / (1 + e1)
         want = ds * s1 / (s0 + s1) ** 2 if renorm else ds
         assert abs(d[0] / want - 1) < 1e-13 and d[2] == 0
+
+
+def test_sigmoid_without_a_bias_orders_by_the_logits():
+    x = np.array([[[40.0, 800.0, -900.0, -800.0, 41.0]]])        # scores 1, 1, 0, 0, 1 in 64 bits
+    assert O.gate(x, 5, score=SIGMOID)[0].tolist() == [[[1, 4, 0, 3, 2]]]
+    assert O.gate(x, 3, bias=np.zeros(5), score=SIGMOID)[0].tolist() == [[[0, 1, 4]]]
