@@ -319,21 +319,29 @@ def permute(x, dest_row, out, row_src=None, r_begin=0, r_end=None, stream=None, 
     return out, row_src
 
 
+def _bf16_rows(t: torch.Tensor, shape, name: str) -> None:
+    """bf16 rows that a call computes with, of exactly this shape (the kernels index them by
+    the geometry): bfloat16, or their bits in 16-bit integers.  float16 would be misread."""
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"{name} must hold 16-bit elements, bfloat16 or its bits as int16 or "
+                        f"uint16, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise TypeError(f"{name} must be of shape {list(shape)}, got {list(t.shape)}")
+
+
 def combine(out, dest_row, gate_w, y, r_begin=0, r_end=None, stream=None, err=None):
-    """out [P][H] 16-bit dispatch buffer; dest_row [R][T][K] int32; gate_w [R][T][K]
-    float32; y [R][T][H] 16-bit (rows of ranks in [r_begin, r_end) are written)."""
+    """out [P][H] bf16 dispatch buffer; dest_row [R][T][K] int32; gate_w [R][T][K]
+    float32; y [R][T][H] bf16 (rows of ranks in [r_begin, r_end) are written)."""
     _i32(dest_row, "dest_row")
     if out.dim() != 2 or dest_row.dim() != 3:
         raise TypeError("out must be [P][H] and dest_row [R][T][K]")
     R, T, K = dest_row.shape
     H = out.shape[1]
     r_end = R if r_end is None else r_end
-    if out.element_size() != 2 or y.element_size() != 2:
-        raise TypeError("out and y must hold 16-bit elements")
+    _bf16_rows(out, (out.shape[0], H), "out")
     if gate_w.dtype != torch.float32 or tuple(gate_w.shape) != (R, T, K):
         raise TypeError("gate_w must be float32 [R][T][K]")
-    if tuple(y.shape) != (R, T, H):
-        raise TypeError("y must be [R][T][H]")
+    _bf16_rows(y, (R, T, H), "y")
     _check(LIB.uep_combine(_p(out), out.shape[0], _p(dest_row), _p(gate_w), R, T, K, H, r_begin,
                            r_end, _p(y), _p(err), _s(stream)), "uep_combine")
     return y
@@ -345,13 +353,6 @@ def _dtype(t: torch.Tensor, name: str) -> int:
     if t.dtype == torch.bfloat16:
         return BF16
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-
-
-def _rows16(t: torch.Tensor, shape, name: str) -> None:
-    """A 16-bit tensor of exactly this shape (the row moves index it by the geometry)."""
-    if t.element_size() != 2 or tuple(t.shape) != tuple(shape):
-        raise TypeError(f"{name} must hold 16-bit elements of shape {list(shape)}, got "
-                        f"{t.dtype} {list(t.shape)}")
 
 
 def gate(logits, K, bias=None, batch_size=None, score=GATE_SOFTMAX, renorm=True, scale=1.0,
@@ -409,8 +410,8 @@ def permute_grad(dout, dest_row, dx, r_begin=0, r_end=None, stream=None, err=Non
     R, T, K = dest_row.shape
     P, H = dout.shape
     r_end = R if r_end is None else r_end
-    _rows16(dout, (P, H), "dout")
-    _rows16(dx, (R, T, H), "dx")
+    _bf16_rows(dout, (P, H), "dout")
+    _bf16_rows(dx, (R, T, H), "dx")
     _buf(err, 1, "err")
     _check(LIB.uep_permute_grad(_p(dout), P, _p(dest_row), R, T, K, H, r_begin, r_end, _p(dx),
                                 _p(err), _s(stream)), "uep_permute_grad")
@@ -428,15 +429,15 @@ def combine_grad(dy, out, dest_row, gate_w, dout, dgate_w=None, r_begin=0, r_end
     R, T, K = dest_row.shape
     P, H = dout.shape
     r_end = R if r_end is None else r_end
-    _rows16(dy, (R, T, H), "dy")
-    _rows16(dout, (P, H), "dout")
+    _bf16_rows(dy, (R, T, H), "dy")
+    _bf16_rows(dout, (P, H), "dout")
     if gate_w.dtype != torch.float32 or tuple(gate_w.shape) != (R, T, K):
         raise TypeError("gate_w must be float32 [R][T][K]")
     if out is None:
         if dgate_w is not None:
             raise TypeError("dgate_w needs the expert outputs `out`")
     else:
-        _rows16(out, (P, H), "out")
+        _bf16_rows(out, (P, H), "out")
         dgate_w = _new((R, T, K), dy, torch.float32) if dgate_w is None else dgate_w
         if dgate_w.dtype != torch.float32 or tuple(dgate_w.shape) != (R, T, K):
             raise TypeError("dgate_w must be float32 [R][T][K]")

@@ -214,3 +214,33 @@ def test_adamw_binding_checks_its_lists(lib):
         U.adamw(p, tops, m)
     with pytest.raises(TypeError, match="tops"):
         U.adamw_decode(m8, v8, tops[:2])
+
+
+def test_float16_rows_are_refused(lib):
+    """The row calls that compute read bf16; float16 elements would be taken for others."""
+    import torch
+    from moe_expert_load_amd import uep as U
+    ids = torch.zeros(2, 3, 2, dtype=torch.int32)
+    w = torch.zeros(2, 3, 2)
+
+    def tensors(dtype):
+        return torch.zeros(9, 16, dtype=dtype), torch.zeros(2, 3, 16, dtype=dtype)
+
+    for dtype in (torch.bfloat16, torch.int16, torch.uint16):       # up to the device check
+        rows, tok = tensors(dtype)
+        for call in (lambda: U.permute_grad(rows, ids, tok), lambda: U.combine(rows, ids, w, tok),
+                     lambda: U.combine_grad(tok, rows, ids, w, rows)):
+            with pytest.raises(TypeError, match="device memory"):
+                call()
+    b_rows, b_tok = tensors(torch.bfloat16)
+    for dtype in (torch.float16, torch.float32):
+        rows, tok = tensors(dtype)
+        for call, name in ((lambda: U.permute_grad(rows, ids, b_tok), "dout"),
+                           (lambda: U.permute_grad(b_rows, ids, tok), "dx"),
+                           (lambda: U.combine(rows, ids, w, b_tok), "out"),
+                           (lambda: U.combine(b_rows, ids, w, tok), "y"),
+                           (lambda: U.combine_grad(tok, b_rows, ids, w, b_rows), "dy"),
+                           (lambda: U.combine_grad(b_tok, rows, ids, w, b_rows), "out"),
+                           (lambda: U.combine_grad(b_tok, b_rows, ids, w, rows), "dout")):
+            with pytest.raises(TypeError, match=name + " must hold"):
+                call()
