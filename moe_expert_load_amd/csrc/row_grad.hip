@@ -40,6 +40,7 @@ constexpr int kRgVec = 8;     // 16-byte vectors in flight per lane for each of 
 constexpr int64_t kRgFew = 512;
 constexpr int64_t kRgPhaseBytes = 48ll << 20;
 constexpr int64_t kRgChunkBytes = 224ll << 20;
+constexpr int64_t kRgLaunch = 1ll << 25;   // tokens of one launch, which holds below 2^32 threads
 
 // Row d of `base`, an empty span if d < 0: its loads read zeros, its stores go nowhere.
 __device__ __forceinline__ span_t rg_row(const u32x4* base, int d, int nvec) {
@@ -179,14 +180,18 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   const int slots = parts == 1 ? K : 1;             // of one wave
   const RgKernels f = nv <= 1 ? rg_kernels<1>(slots) : nv <= 2 ? rg_kernels<2>(slots)
                     : nv <= 4 ? rg_kernels<4>(slots) : rg_kernels<8>(slots);
-  if (out && (K == 1 || (g1 - g0) * K * (int64_t)H * 2 < kRgPhaseBytes))
-    return launch(f.both, g0, g1) ? UEP_OK : UEP_EHIP;
-  // tokens per pair of phases: equal chunks whose gradients stay in the last-level cache, and
-  // which a launch holds (below 2^32 threads)
-  const int64_t cap = out ? std::max<int64_t>(64, kRgChunkBytes / ((int64_t)H * 2)) : 1ll << 25;
+  const bool phases = out && K > 1 && (g1 - g0) * K * (int64_t)H * 2 >= kRgPhaseBytes;
+  // equal chunks of tokens that a launch holds; in phases, whose gradients stay in the
+  // last-level cache
+  const int64_t cap = std::min(
+      kRgLaunch, phases ? std::max<int64_t>(64, kRgChunkBytes / ((int64_t)H * 2)) : kRgLaunch);
   const int64_t n = (g1 - g0 + cap - 1) / cap, chunk = (g1 - g0 + n - 1) / n;
   for (int64_t c0 = g0; c0 < g1; c0 += chunk) {
     const int64_t c1 = std::min(g1, c0 + chunk);
+    if (out && !phases) {
+      if (!launch(f.both, c0, c1)) return UEP_EHIP;
+      continue;
+    }
     if (out && !launch(f.dot, c0, c1)) return UEP_EHIP;
     if (!launch(f.scale, c0, c1)) return UEP_EHIP;
   }

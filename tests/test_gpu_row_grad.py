@@ -212,3 +212,29 @@ def test_gradients_match_torchs_autograd():
     assert (np.abs(host(dx.double()) - xa.grad.numpy()) <= 3 * 2.0 ** -8 * mag + 1e-30).all()
     m2 = (xa.detach().abs() * dy.double().cpu().abs()).sum(-1, keepdim=True).numpy()
     assert (np.abs(host(dw) - wa.grad.numpy()) <= 18 * EPS * m2).all()
+
+
+def test_combine_grad_of_one_slot_and_many_tokens():
+    """K = 1 and 2^26 + 5 tokens: more than one launch holds."""
+    n, H = 2 ** 26 + 5, 8
+    say("case: combine_grad, K = 1, 2^26 + 5 tokens")
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    g = torch.Generator(device=DEV).manual_seed(15)
+    dy = torch.randn(1, n, H, generator=g, device=DEV, dtype=torch.bfloat16)
+    out = torch.randn(n, H, generator=g, device=DEV, dtype=torch.bfloat16)
+    row = torch.arange(n - 1, -1, -1, device=DEV, dtype=torch.int32).view(1, n, 1)
+    row[0, ::1000] = -1
+    w = torch.rand(1, n, 1, generator=g, device=DEV)
+    dout = torch.full((n, H), 77, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+    dout, dw = U.combine_grad(dy, out, row, w, dout)
+    on = row[0] >= 0                                             # [n][1]
+    want = torch.where(on, (w[0] * dy[0].float()).to(torch.bfloat16).view(torch.int16), 77)
+    assert torch.equal(dout.flip(0).view(torch.int16), want)
+    del want, dout
+    terms = dy[0].float() * out.flip(0).float()                  # exact
+    dot = torch.where(on, terms.double().sum(-1, keepdim=True), 0)
+    bound = (H / 64 + 16) * EPS * terms.abs().sum(-1, keepdim=True)
+    assert bool(((dw[0].double() - dot).abs() <= bound).all())
+    del dy, out, row, w, dw, terms, dot, bound, on
+    torch.cuda.empty_cache()
