@@ -375,12 +375,12 @@ __device__ __forceinline__ double gt_wave_max(double v) {
 template <typename T, int kVpt>
 __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias,
-    const int32_t* __restrict__ batch_size, int64_t n_tok, int tok_per_rank, int E, int K,
-    int score, int renorm, float scale, int32_t* __restrict__ topk_ids,
+    const int32_t* __restrict__ batch_size, int64_t g0, int64_t g1, int tok_per_rank, int E,
+    int K, int score, int renorm, float scale, int32_t* __restrict__ topk_ids,
     float* __restrict__ gate_w, int32_t* err) {
   const int lane = threadIdx.x % kWave;
-  const int64_t g = (int64_t)blockIdx.x * kGtTokPerBlock + threadIdx.x / kWave;
-  if (g >= n_tok) return;
+  const int64_t g = g0 + (int64_t)blockIdx.x * kGtTokPerBlock + threadIdx.x / kWave;
+  if (g >= g1) return;
   if (batch_size && (int)(g % tok_per_rank) >= batch_size[g / tok_per_rank]) {
     if (lane < K) {
       topk_ids[g * K + lane] = -1;
@@ -610,9 +610,9 @@ struct GtCall {
   hipStream_t stream;
 };
 
-// workgroups for n_tok < 2^26 tokens, at least 4 each: a launch holds below 2^32 threads
 static unsigned gt_blocks(int64_t n_tok, int per) { return (unsigned)((n_tok + per - 1) / per); }
 
+// n_tok < 2^26 tokens, at most 16 lanes each: below the 2^32 threads that a launch holds
 template <typename T, typename KY, bool kBias, int kL, int kN, int kPer>
 static uep_status gt_sorted(const GtCall& c) {
   const unsigned blocks = gt_blocks(c.n_tok, kGtThreads / kL);
@@ -623,13 +623,17 @@ static uep_status gt_sorted(const GtCall& c) {
   return UEP_OK;
 }
 
+constexpr int64_t kGtLaunch = 1ll << 25;  // a wave each: half of what a launch holds
 template <typename T, int kVpt>
 static uep_status gt_general(const GtCall& c) {
-  const unsigned blocks = gt_blocks(c.n_tok, kGtTokPerBlock);
-  hipLaunchKernelGGL((gate_kernel<T, kVpt>), dim3(blocks), dim3(kGtThreads), 0, c.stream,
-                     static_cast<const T*>(c.logits), c.bias, c.batch_size, c.n_tok, c.T, c.E, c.K,
-                     c.score, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
-  UEP_CHECK_LAUNCH();
+  for (int64_t g0 = 0; g0 < c.n_tok; g0 += kGtLaunch) {
+    const int64_t g1 = std::min(c.n_tok, g0 + kGtLaunch);
+    const unsigned blocks = gt_blocks(g1 - g0, kGtTokPerBlock);
+    hipLaunchKernelGGL((gate_kernel<T, kVpt>), dim3(blocks), dim3(kGtThreads), 0, c.stream,
+                       static_cast<const T*>(c.logits), c.bias, c.batch_size, g0, g1, c.T, c.E,
+                       c.K, c.score, c.renorm, c.scale, c.topk_ids, c.gate_w, c.err);
+    UEP_CHECK_LAUNCH();
+  }
   return UEP_OK;
 }
 

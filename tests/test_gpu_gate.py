@@ -311,3 +311,21 @@ def test_sigmoid_without_a_bias_orders_by_the_logits(dtype, R, T, E, K):
         tol = EPS * (2 * 88 + 40) * np.abs(w_o) + 1e-37
         assert (np.abs(w - w_o) <= tol)[near].all()
         assert np.isfinite(w).all()
+
+
+def test_the_most_tokens():
+    """2^26 - 1 tokens, the documented limit, by the kernel that takes a wave for each."""
+    n = 2 ** 26 - 1
+    say("case: gate, 2^26 - 1 tokens")
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GiB of device memory")
+    g = torch.Generator(device=DEV).manual_seed(90)
+    x = torch.randn(1, n, 2, generator=g, device=DEV)
+    bs = to_dev(np.array([n - 3]))
+    ids, w = U.gate(x, 1, batch_size=bs)
+    want = (x[..., 1:] > x[..., :1]).to(torch.int32)
+    assert torch.equal(ids[:, :n - 3], want[:, :n - 3])
+    assert bool((w[:, :n - 3] == 1).all())
+    assert bool((ids[:, n - 3:] == -1).all()) and bool((w[:, n - 3:] == 0).all())
+    del x, ids, w, want
+    torch.cuda.empty_cache()
