@@ -472,10 +472,11 @@ uep_status uep_lplb_sample(const int32_t* topk_ids, int32_t R, int32_t T, int32_
  *   score                      UEP_GATE_SOFTMAX or UEP_GATE_SIGMOID
  *   scale                      finite, not 0
  *   topk_ids   [R][T][K]  out
- *   gate_w     [R][T][K]  out  fp32; sums and exponentials are fp32
+ *   gate_w     [R][T][K]  out  fp32; sums and exponentials are fp32 (a sigmoid score below
+ *                              2^-126 counts as 0).  Neither may overlap another array
  *   err                   out  optional; UEP_ERR_LOGIT
  * Returns UEP_EINVAL for null pointers, sizes < 1 (T may be 0), an unknown dtype or
- * score, a bias with softmax, a bad scale; UEP_EGEOM for R > 64, E > 4096, K > 64,
+ * score, a bias with softmax, a bad scale, overlapping outputs; UEP_EGEOM for R > 64, E > 4096, K > 64,
  * K > E, R*T >= 2^26 or R*T*K >= 2^31.
  * ------------------------------------------------------------------------- */
 enum { UEP_GATE_SOFTMAX = 0, UEP_GATE_SIGMOID = 1 };
@@ -501,7 +502,7 @@ uep_status uep_gate(const void* logits, int32_t dtype, const float* bias,
  *   topk_ids, gate_w           in   as written by uep_gate with the same score, renorm
  *                                   and scale
  *   dlogits    [R][T][E]       out  the logits' dtype; every element is written; not
- *                                   overlapping logits (UEP_EINVAL)
+ *                                   overlapping an input (UEP_EINVAL)
  *   err                        out  optional; UEP_ERR_ID_RANGE: an id outside [-1, E),
  *                                   taken as -1
  * Returns UEP_EINVAL / UEP_EGEOM like uep_gate.
@@ -523,7 +524,7 @@ uep_status uep_gate_grad(const float* dgate_w, const void* logits, int32_t dtype
  *   dest_row [R][T][K]            in   as given to uep_permute
  *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end) are written
  *   dx       [R][T][H] bf16 bits  out  16-byte aligned; other ranks' rows are untouched; not
- *                                      overlapping dout (UEP_EINVAL)
+ *                                      overlapping an input (UEP_EINVAL)
  *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
  * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
  * ------------------------------------------------------------------------- */
@@ -547,8 +548,9 @@ uep_status uep_permute_grad(const uint16_t* dout, int64_t out_rows, const int32_
  *   gate_w   [R][T][K] fp32       in
  *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end)
  *   dout     [out_rows][H] bf16   out  16-byte aligned; may be `out` itself (in place), but
- *                                      overlap it or dy in no other way (UEP_EINVAL)
- *   dgate_w  [R][T][K] fp32       out  slots of other ranks are untouched
+ *                                      overlap it or another array in no other way (UEP_EINVAL)
+ *   dgate_w  [R][T][K] fp32       out  slots of other ranks are untouched; not overlapping any
+ *                                      other array, gate_w among them (UEP_EINVAL)
  *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
  * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
  * ------------------------------------------------------------------------- */

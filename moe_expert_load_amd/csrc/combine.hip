@@ -130,7 +130,8 @@ static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_
   if (!rows || !dest_row || (weighted && !gate_w) || !y) return UEP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(y)) % 16 != 0)
     return UEP_EGEOM;
-  if (!weighted && uep_overlap(rows, out_rows * H * 2, y, (int64_t)R * T * H * 2))
+  const int64_t tok = (int64_t)R * T, used = std::min<int64_t>(out_rows, 1ll << 31);
+  if (!weighted && uep_overlap({y, tok * H * 2}, {{rows, used * H * 2}, {dest_row, tok * K * 4}}))
     return UEP_EINVAL;
   const int slices = (H / 8 + kCbVec * kWave - 1) / (kCbVec * kWave);
   const int parts = g1 - g0 <= kCbFew ? std::min(slices, 16) : 1;

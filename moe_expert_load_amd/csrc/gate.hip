@@ -692,6 +692,10 @@ extern "C" uep_status uep_gate(const void* logits, int32_t dtype, const float* b
   if (T == 0) return UEP_OK;
   if (!topk_ids || !gate_w) return UEP_EINVAL;
   const int64_t n_tok = (int64_t)R * T;
+  const UepBytes rows{logits, n_tok * E * (dtype == UEP_F32 ? 4 : 2)}, lift{bias, E * 4ll};
+  const UepBytes sizes{batch_size, R * 4ll}, ids{topk_ids, n_tok * K * 4}, w{gate_w, n_tok * K * 4};
+  if (uep_overlap(ids, {rows, lift, sizes, w}) || uep_overlap(w, {rows, lift, sizes}))
+    return UEP_EINVAL;
   const GtCall c{logits, bias, batch_size, n_tok, T, E, K, score, renorm, scale, topk_ids, gate_w,
                  err, uep_stream(stream)};
   return dtype == UEP_F32 ? gt_launch<float>(c) : gt_launch<uint16_t>(c);
@@ -707,8 +711,10 @@ extern "C" uep_status uep_gate_grad(const float* dgate_w, const void* logits, in
   if (T == 0) return UEP_OK;
   if (!dgate_w || !topk_ids || !gate_w || !dlogits) return UEP_EINVAL;
   const int64_t n_tok = (int64_t)R * T;
-  const int64_t bytes = n_tok * E * (dtype == UEP_F32 ? 4 : 2);
-  if (uep_overlap(logits, bytes, dlogits, bytes)) return UEP_EINVAL;
+  const int64_t bytes = n_tok * E * (dtype == UEP_F32 ? 4 : 2), slots = n_tok * K * 4;
+  if (uep_overlap({dlogits, bytes},
+                  {{logits, bytes}, {dgate_w, slots}, {topk_ids, slots}, {gate_w, slots}}))
+    return UEP_EINVAL;
   int lg_kp = 0;
   while ((1 << lg_kp) < K) ++lg_kp;
   const int64_t n_grp = (n_tok + (kWave >> lg_kp) - 1) / (kWave >> lg_kp);

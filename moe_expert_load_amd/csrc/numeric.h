@@ -2,6 +2,8 @@
 // overlap check of the calls whose outputs may not touch their inputs.
 #pragma once
 
+#include <initializer_list>
+
 #include "common.h"
 
 namespace uep {
@@ -39,8 +41,17 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
 
 }  // namespace uep
 
-// Whether two buffers share a byte.
-static inline bool uep_overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+// Whether a buffer shares a byte with one of the others (absent ones are NULL).
+struct UepBytes {
+  const void* p;
+  int64_t n;
+};
+static inline bool uep_overlap(UepBytes a, std::initializer_list<UepBytes> others) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p);
+  for (const UepBytes& b : others) {
+    const uintptr_t y = reinterpret_cast<uintptr_t>(b.p);
+    if (x && y && a.n > 0 && b.n > 0 && x < y + (uintptr_t)b.n && y < x + (uintptr_t)a.n)
+      return true;
+  }
+  return false;
 }

@@ -163,9 +163,13 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   if ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(dout)) % 16 != 0)
     return UEP_EGEOM;
-  const int64_t tok_bytes = (int64_t)R * T * H * 2, row_bytes = out_rows * H * 2;
-  if (uep_overlap(dy, tok_bytes, dout, row_bytes) ||
-      (out && out != dout && uep_overlap(out, row_bytes, dout, row_bytes)))
+  // dgate_w is written while gate_w, dout while dy and the others are still to be read
+  const int64_t rows_used = std::min<int64_t>(out_rows, 1ll << 31);     // rows are int32
+  const UepBytes grad{dy, (int64_t)R * T * H * 2}, rows{out, rows_used * H * 2};
+  const UepBytes row_of{dest_row, (int64_t)R * T * K * 4}, weight{gate_w, (int64_t)R * T * K * 4};
+  const UepBytes to{dout, rows.n}, dot{dgate_w, weight.n};
+  if (uep_overlap(to, {grad, row_of, weight}) || (out != dout && uep_overlap(to, {rows})) ||
+      uep_overlap(dot, {grad, rows, row_of, weight, to}))
     return UEP_EINVAL;
   const int nv = (H / 8 + kWave - 1) / kWave;       // vectors per lane of a row
   const int parts = g1 - g0 <= kRgFew ? K : 1;

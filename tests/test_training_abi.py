@@ -244,3 +244,53 @@ def test_float16_rows_are_refused(lib):
                            (lambda: U.combine_grad(b_tok, b_rows, ids, w, rows), "dout")):
             with pytest.raises(TypeError, match=name + " must hold"):
                 call()
+
+
+def test_outputs_may_not_share_memory_with_any_other_array(lib):
+    """Every output against every other array of its call; 2 * 3 * 2 int32 or fp32 slots are 48
+    bytes, 2 * 4 * 2 of the row calls 64."""
+    at = ctypes.c_void_p
+    base = 1 << 20
+
+    def refused(call, args, out, allowed=()):
+        for other in args:
+            if other == out or other in allowed:
+                continue
+            for off in (0, args[other] - 4, 4 - args[out]):
+                ptrs = {a: at(base * (i + 1)) for i, a in enumerate(args)}
+                ptrs[out] = at(ptrs[other].value + off)
+                assert call(ptrs) == EINVAL, (out, other, off)
+
+    def call_gate(p):
+        return lib.uep_gate(p["logits"], i32(0), p["bias"], p["bs"], i32(2), i32(3), i32(8), i32(2),
+                            i32(1), i32(1), f32(1.0), p["ids"], p["w"], null, null)
+
+    args = dict(logits=192, bias=32, bs=8, ids=48, w=48)
+    refused(call_gate, args, "ids")
+    refused(call_gate, args, "w")
+
+    def call_gate_grad(p):
+        return lib.uep_gate_grad(p["dw"], p["logits"], i32(0), p["ids"], p["w"], i32(2), i32(3),
+                                 i32(8), i32(2), i32(1), i32(1), f32(1.0), p["dl"], null, null)
+
+    refused(call_gate_grad, dict(dw=48, logits=192, ids=48, w=48, dl=192), "dl")
+
+    def call_permute(p):
+        return permute_grad(lib, dout=p["dout"], drow=p["drow"], dx=p["dx"])
+
+    def call_combine(p):
+        return combine_grad(lib, dy=p["dy"], out=p["out"], drow=p["drow"], w=p["w"],
+                            dout=p["dout"], dw=p["dw"])
+
+    # rows lie on 16 bytes: offsets of 4 are refused as geometry, so whole rows here
+    for other, off in (("dout", 0), ("dout", 496), ("drow", 0), ("drow", 48)):
+        p = {a: at(base * (i + 1)) for i, a in enumerate(("dout", "drow", "dx"))}
+        p["dx"] = at(p[other].value + off)
+        assert call_permute(p) == EINVAL, (other, off)
+    names = ("dy", "out", "drow", "w", "dout", "dw")
+    for other, off in (("dy", 0), ("dy", 240), ("drow", 0), ("drow", 48), ("w", 0), ("w", 48),
+                       ("out", 496)):
+        p = {a: at(base * (i + 1)) for i, a in enumerate(names)}
+        p["dout"] = at(p[other].value + off)
+        assert call_combine(p) == EINVAL, (other, off)
+    refused(call_combine, dict(dy=256, out=512, drow=64, w=64, dout=512, dw=64), "dw")
