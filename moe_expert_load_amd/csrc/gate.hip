@@ -399,9 +399,10 @@ __global__ __launch_bounds__(kGtThreads) void gate_kernel(
     val[j] = x;
     bad |= gt_bad(x);
     float f = x + 0.0f;
-    if (bias && gt_finite(x)) {                       // ranked as in the sorting kernel
-      f = gt_sigmoid(x) + bias[e];
-      bad |= gt_bad(f);
+    if (bias && e < E) {                              // ranked as in the sorting kernel
+      const float y = bias[e];
+      bad |= gt_bad(y);
+      if (gt_finite(x)) f = gt_sigmoid(x) + y;
     }
     key[j] = gt_finite(f) ? Key64::make(f, kGtInv, e) : none;
   }

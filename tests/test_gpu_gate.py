@@ -329,3 +329,18 @@ def test_the_most_tokens():
     assert bool((ids[:, n - 3:] == -1).all()) and bool((w[:, n - 3:] == 0).all())
     del x, ids, w, want
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("E,K", [(40, 4), (40, 20), (1100, 3)])
+def test_a_bias_is_checked_behind_a_masked_logit(E, K):
+    """A bias that is not a number is flagged whatever its expert's logit, at every size."""
+    say("case: gate, bias behind a masked logit", E, K)
+    x = draw_logits(80, 1, 3, E, F)
+    x[..., 7] = -float("inf")
+    for value, want in ((float("nan"), U.ERR_LOGIT), (float("inf"), U.ERR_LOGIT),
+                        (-float("inf"), 0), (0.5, 0)):
+        bias = np.zeros(E, np.float32)
+        bias[7] = value
+        ids, w, err = run_gate(x, K, bias=bias, score=1)
+        assert err == want, value
+        assert (ids != 7).all() and (ids >= 0).all() and np.isfinite(w).all()
