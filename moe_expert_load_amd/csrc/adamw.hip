@@ -378,8 +378,8 @@ __device__ __forceinline__ bool aw_chunk(const AwTensor& t, const AwChunk<P, G, 
     for (int j = 0; j < 4; ++j) {
       const uint32_t bits = __float_as_uint(w[j]);
       o[j] = j & 1 ? aw_add<true>(r[j / 2], bits) : aw_add<false>(r[j / 2], bits);
-      // a NaN is cut as it is.  With 8-bit states it needs no check: it was made here or came
-      // from a bf16 parameter, so its lower half is zero and nothing carries
+      // a NaN is cut as it is.  With 8-bit states it needs no check: it was made here, came from
+      // a bf16 parameter or is the learning rate's, so its lower half is zero and nothing carries
       if (!k8 && (bits & 0x7FFFFFFFu) > 0x7F800000u) o[j] = bits;
     }
     const uint32_t word[2] = {o[0] >> 16 | (o[1] & 0xFFFF0000u), o[2] >> 16 | (o[3] & 0xFFFF0000u)};
@@ -457,7 +457,9 @@ __global__ __launch_bounds__(kAwThreads) void adamw_kernel(const char* __restric
   const int32_t* tiles = reinterpret_cast<const int32_t*>(tensors + h.count);
   const int q = tiles[blockIdx.x];
   const AwTensor& x = tensors[q];
-  const float lr = sched[0] * x.t.lr_scale;
+  float lr = sched[0] * x.t.lr_scale;
+  // any NaN as the one whose lower half is zero, which the random cut of bf16 parameters keeps
+  if (lr != lr) lr = __builtin_nanf("");
   // both corrections at once: even lanes the first, odd lanes the second
   const float bc = aw_correction(t * (threadIdx.x & 1 ? a.log_b2 : a.log_b1));
   const float bc1 = __int_as_float(readlane(__float_as_int(bc), 0));

@@ -287,3 +287,20 @@ def test_offsets_past_32_bits():
     assert float(p[:512].float().abs().min()) > 0 and float(p[600:1 << 20].float().abs().max()) == 0
     del p, g, m, v, tops, plan
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("param", [F, B])
+@pytest.mark.parametrize("eight", [False, True])
+def test_a_rate_that_is_not_a_number_shows(param, eight):
+    """Every kind of NaN as the learning rate leaves NaN parameters, not zeros."""
+    say("case: adamw, learning rate NaN", param, eight)
+    n = 3000
+    for word in (0x7FC00000, 0x7FFFFFFF, -1, 0x7FFFC001):
+        rng = np.random.default_rng(106)
+        p, g, m, v, tops = draw(rng, n, param, param, eight, 0)
+        plan = U.adamw_prepare([p], [g], [m], [v], tops=[tops] if eight else None,
+                               weight_decay=0.1)
+        sched = torch.tensor([word, 0x3F800000], dtype=torch.int64).to(torch.int32)
+        sched = sched.to(DEV).view(torch.float32)
+        U.adamw(plan, torch.ones(1, dtype=torch.int32, device=DEV), sched, seed=3)
+        assert bool(torch.isnan(p).all()), hex(word)
