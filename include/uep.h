@@ -279,7 +279,7 @@ uep_status uep_permute(const uint16_t* x, const int32_t* dest_row, int32_t R, in
  * no fused multiply-add, then nearest-even rounding to bf16 (a NaN stays a NaN).
  *
  *   out      [out_rows][H] bf16   in   dispatch buffer (layout of uep_permute's out),
- *                                      16-byte aligned
+ *                                      16-byte aligned; NULL is taken if out_rows is 0
  *   dest_row [R][T][K]            in   from uep_reroute_assign
  *   gate_w   [R][T][K] fp32       in   combine weights
  *   r_begin, r_end                     only tokens of ranks in [r_begin, r_end) are written
@@ -526,7 +526,7 @@ uep_status uep_gate_grad(const float* dgate_w, const void* logits, int32_t dtype
  *   dx       [R][T][H] bf16 bits  out  16-byte aligned; other ranks' rows are untouched; not
  *                                      overlapping an input (UEP_EINVAL)
  *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
- * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
+ * Returns UEP_EINVAL / UEP_EGEOM like uep_permute; dout may be NULL if out_rows is 0.
  * ------------------------------------------------------------------------- */
 uep_status uep_permute_grad(const uint16_t* dout, int64_t out_rows, const int32_t* dest_row,
                             int32_t R, int32_t T, int32_t K, int32_t H, int32_t r_begin,
@@ -552,7 +552,8 @@ uep_status uep_permute_grad(const uint16_t* dout, int64_t out_rows, const int32_
  *   dgate_w  [R][T][K] fp32       out  slots of other ranks are untouched; not overlapping any
  *                                      other array, gate_w among them (UEP_EINVAL)
  *   err                           out  optional; UEP_ERR_ROW_RANGE, taken as no row
- * Returns UEP_EINVAL / UEP_EGEOM like uep_permute.
+ * Returns UEP_EINVAL / UEP_EGEOM like uep_permute; out and dout may be NULL if out_rows is 0
+ * (dgate_w, if given, gets its zeros).
  * ------------------------------------------------------------------------- */
 uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, int64_t out_rows,
                             const int32_t* dest_row, const float* gate_w, int32_t R, int32_t T,

@@ -127,7 +127,7 @@ static uep_status cb_launch(const uint16_t* rows, int64_t out_rows, const int32_
     return UEP_EGEOM;
   const int64_t g0 = (int64_t)r_begin * T, g1 = (int64_t)r_end * T;
   if (g1 == g0) return UEP_OK;
-  if (!rows || !dest_row || (weighted && !gate_w) || !y) return UEP_EINVAL;
+  if ((!rows && out_rows > 0) || !dest_row || (weighted && !gate_w) || !y) return UEP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(y)) % 16 != 0)
     return UEP_EGEOM;
   const int64_t tok = (int64_t)R * T, used = std::min<int64_t>(out_rows, 1ll << 31);

@@ -159,7 +159,10 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
     return UEP_EGEOM;
   const int64_t g0 = (int64_t)r_begin * T, g1 = (int64_t)r_end * T;
   if (g1 == g0) return UEP_OK;
-  if (!dy || !dest_row || !gate_w || !dout || !out != !dgate_w) return UEP_EINVAL;
+  // a buffer without rows has no address either: dgate_w says whether its zeros are wanted
+  if (!dy || !dest_row || !gate_w || (!dout && out_rows > 0) ||
+      (out ? !dgate_w : dgate_w && out_rows > 0))
+    return UEP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(out) |
        reinterpret_cast<uintptr_t>(dout)) % 16 != 0)
     return UEP_EGEOM;
@@ -184,7 +187,7 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   const int slots = parts == 1 ? K : 1;             // of one wave
   const RgKernels f = nv <= 1 ? rg_kernels<1>(slots) : nv <= 2 ? rg_kernels<2>(slots)
                     : nv <= 4 ? rg_kernels<4>(slots) : rg_kernels<8>(slots);
-  const bool phases = out && K > 1 && (g1 - g0) * K * (int64_t)H * 2 >= kRgPhaseBytes;
+  const bool phases = dgate_w && K > 1 && (g1 - g0) * K * (int64_t)H * 2 >= kRgPhaseBytes;
   // equal chunks of tokens that a launch holds; in phases, whose gradients stay in the
   // last-level cache
   const int64_t cap = std::min(
@@ -192,11 +195,11 @@ extern "C" uep_status uep_combine_grad(const uint16_t* dy, const uint16_t* out, 
   const int64_t n = (g1 - g0 + cap - 1) / cap, chunk = (g1 - g0 + n - 1) / n;
   for (int64_t c0 = g0; c0 < g1; c0 += chunk) {
     const int64_t c1 = std::min(g1, c0 + chunk);
-    if (out && !phases) {
+    if (dgate_w && !phases) {
       if (!launch(f.both, c0, c1)) return UEP_EHIP;
       continue;
     }
-    if (out && !launch(f.dot, c0, c1)) return UEP_EHIP;
+    if (dgate_w && !launch(f.dot, c0, c1)) return UEP_EHIP;
     if (!launch(f.scale, c0, c1)) return UEP_EHIP;
   }
   return UEP_OK;

@@ -238,3 +238,29 @@ def test_combine_grad_of_one_slot_and_many_tokens():
     assert bool(((dw[0].double() - dot).abs() <= bound).all())
     del dy, out, row, w, dw, terms, dot, bound, on
     torch.cuda.empty_cache()
+
+
+def test_dispatch_buffers_without_rows():
+    """No row at all (every token absent): zeros for dx and the weights' gradient."""
+    say("case: row gradients, no dispatch rows")
+    R, T, K, H = 2, 30, 4, 64
+    none = to_dev(np.full((R, T, K), -1))
+    rows = torch.empty(0, H, dtype=torch.bfloat16, device=DEV)
+    tok = torch.full((R, T, H), 77, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+    w = torch.ones(R, T, K, device=DEV)
+    assert (bits(U.permute_grad(rows, none, tok.clone())) == 0).all()
+    assert (bits(U.combine(rows, none, w, tok.clone())) == 0).all()
+    dw = torch.full((R, T, K), 9.0, device=DEV)
+    dout, got = U.combine_grad(tok, rows, none, w, torch.empty_like(rows), dw)
+    assert got is dw and dout.shape == (0, H) and (host(dw) == 0).all()
+    U.combine_grad(tok, rows, none, w, rows, dw)
+    assert U.combine_grad(tok, None, none, w, rows)[1] is None
+    bad = none.clone()
+    bad[1, 3, 2] = 0
+    for call in (lambda e: U.permute_grad(rows, bad, tok.clone(), err=e),
+                 lambda e: U.combine(rows, bad, w, tok.clone(), err=e),
+                 lambda e: U.combine_grad(tok, rows, bad, w, rows, dw, err=e)):
+        err = err_word()
+        call(err)
+        assert int(host(err)[0]) == U.ERR_ROW_RANGE
+    assert (host(dw) == 0).all()
