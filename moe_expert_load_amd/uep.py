@@ -2,8 +2,10 @@
 
 Argument marshalling only: torch supplies device memory and the HIP stream; every
 step of the balancing path runs in the library's HIP kernels.  Output tensors the
-caller does not pass are allocated with torch on the input's device.  A non-zero
-status raises UEPError.  Importing this module fails loudly when the library is
+caller does not pass are allocated with torch on the input's device.  With `stream` a
+call works on that stream, which the caller orders with the streams that make its inputs
+and use its outputs (what the call allocates is safe by itself).  A non-zero status
+raises UEPError.  Importing this module fails loudly when the library is
 not built: there is no fallback path.
 """
 
@@ -136,8 +138,19 @@ def _i32(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _new(shape, like: torch.Tensor, dtype=torch.int32) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _fresh(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory that a call allocates and writes on `stream`.  It is the current stream's, which
+    may still have work queued for whoever held it last: another stream waits for that, and the
+    memory is not given away again before that stream has passed the call."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.is_cuda and stream.cuda_stream != (_s(None).value or 0):
+        stream.wait_stream(torch.cuda.current_stream())
+        t.record_stream(stream)
+    return t
+
+
+def _new(shape, like: torch.Tensor, stream, dtype=torch.int32) -> torch.Tensor:
+    return _fresh(shape, dtype, like.device, stream)
 
 
 def _buf(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.int32):
@@ -163,16 +176,16 @@ def load_matrix(topk_ids, E, counts=None, bucket_pos=None, err=None, ws=None, st
     not computed and None is returned in their place."""
     _i32(topk_ids, "topk_ids")
     R, T, K = topk_ids.shape
-    counts = _new((R, E), topk_ids) if counts is None else _buf(counts, R * E, "counts")
+    counts = _new((R, E), topk_ids, stream) if counts is None else _buf(counts, R * E, "counts")
     if counts_only:
         bucket_pos = None
     elif bucket_pos is None:
-        bucket_pos = _new((R, T, K), topk_ids)
+        bucket_pos = _new((R, T, K), topk_ids, stream)
     else:
         _buf(bucket_pos, R * T * K, "bucket_pos")
     _buf(err, 1, "err")
     n = load_matrix_workspace_size(R, T, K, E)
-    ws = _new((max(n, 4),), topk_ids, torch.uint8) if ws is None else ws
+    ws = _new((max(n, 4),), topk_ids, stream, torch.uint8) if ws is None else ws
     _check(LIB.uep_load_matrix(_p(topk_ids), R, T, K, E, _p(counts), _p(bucket_pos), _p(err),
                                _p(ws), ws.numel() * ws.element_size(), _s(stream)),
            "uep_load_matrix")
@@ -185,11 +198,11 @@ def load_matrix_noalloc(topk_ids, E, counts=None, bucket_pos=None, err=None, str
     instead of a workspace (pass counts / bucket_pos to allocate nothing here either)."""
     _i32(topk_ids, "topk_ids")
     R, T, K = topk_ids.shape
-    counts = _new((R, E), topk_ids) if counts is None else _buf(counts, R * E, "counts")
+    counts = _new((R, E), topk_ids, stream) if counts is None else _buf(counts, R * E, "counts")
     if counts_only:
         bucket_pos = None
     elif bucket_pos is None:
-        bucket_pos = _new((R, T, K), topk_ids)
+        bucket_pos = _new((R, T, K), topk_ids, stream)
     else:
         _buf(bucket_pos, R * T * K, "bucket_pos")
     _buf(err, 1, "err")
@@ -203,11 +216,10 @@ def solve_quota(counts, S, q_min, out=None, stream=None):
     R, E = counts.shape
     ipr = E // R + S
     o = out or {}
-    slot_expert = o.get("slot_expert", _new((R, max(S, 1)), counts))
-    inst_expert = o.get("inst_expert", _new((R * ipr,), counts))
-    inst_quota = o.get("inst_quota", _new((R * ipr,), counts))
-    rank_load = o.get("rank_load", _new((R,), counts))
-    stats = o.get("stats", _new((4,), counts))
+    slot_expert, inst_expert, inst_quota, rank_load, stats = (
+        o[name] if name in o else _new(shape, counts, stream)
+        for name, shape in (("slot_expert", (R, max(S, 1))), ("inst_expert", (R * ipr,)),
+                            ("inst_quota", (R * ipr,)), ("rank_load", (R,)), ("stats", (4,))))
     for name, t, n in (("slot_expert", slot_expert, R * S), ("inst_expert", inst_expert, R * ipr),
                        ("inst_quota", inst_quota, R * ipr), ("rank_load", rank_load, R),
                        ("stats", stats, 4)):
@@ -225,7 +237,8 @@ def identity_quota(counts, inst_expert, inst_quota=None, stream=None):
     R, E = counts.shape
     _i32(inst_expert, "inst_expert")
     n = inst_expert.numel()
-    inst_quota = _new((n,), counts) if inst_quota is None else _buf(inst_quota, n, "inst_quota")
+    inst_quota = _new((n,), counts, stream) if inst_quota is None \
+        else _buf(inst_quota, n, "inst_quota")
     _check(LIB.uep_identity_quota(_p(counts), R, E, n, _p(inst_expert), _p(inst_quota),
                                   _s(stream)), "uep_identity_quota")
     return inst_quota
@@ -248,15 +261,15 @@ def reroute_assign(counts, topk_ids, bucket_pos, inst_per_rank, inst_expert, ins
     _buf(inst_expert, I, "inst_expert")
     _buf(inst_quota, I, "inst_quota")
     _buf(err, 1, "err")
-    xfer = _new((R, I), counts) if xfer is None else _buf(xfer, R * I, "xfer")
-    inst_offset = _new((I + 1,), counts) if inst_offset is None else _buf(inst_offset, I + 1,
-                                                                           "inst_offset")
-    dest_inst = _new((R, T, K), counts) if dest_inst is None else _buf(dest_inst, R * T * K,
-                                                                       "dest_inst")
-    dest_row = _new((R, T, K), counts) if dest_row is None else _buf(dest_row, R * T * K,
-                                                                     "dest_row")
+    xfer = _new((R, I), counts, stream) if xfer is None else _buf(xfer, R * I, "xfer")
+    inst_offset = _new((I + 1,), counts, stream) if inst_offset is None \
+        else _buf(inst_offset, I + 1, "inst_offset")
+    dest_inst = _new((R, T, K), counts, stream) if dest_inst is None \
+        else _buf(dest_inst, R * T * K, "dest_inst")
+    dest_row = _new((R, T, K), counts, stream) if dest_row is None \
+        else _buf(dest_row, R * T * K, "dest_row")
     n = reroute_workspace_size(R, E, inst_per_rank)
-    ws = _new((max(n, 4),), counts, torch.uint8) if ws is None else ws
+    ws = _new((max(n, 4),), counts, stream, torch.uint8) if ws is None else ws
     _check(LIB.uep_reroute_assign(_p(counts), _p(topk_ids), _p(bucket_pos), R, T, K, E,
                                   inst_per_rank, _p(inst_expert), _p(inst_quota), r_begin, r_end,
                                   _p(xfer), _p(inst_offset), _p(dest_inst), _p(dest_row),
@@ -286,10 +299,10 @@ def plan(topk_ids, E, S, q_min, r_begin=0, r_end=None, out=None, err=None, ws=No
         n = 1
         for d in shp:
             n *= d
-        o[k] = _new(shp, topk_ids) if o.get(k) is None else _buf(o[k], n, k)
+        o[k] = _new(shp, topk_ids, stream) if o.get(k) is None else _buf(o[k], n, k)
     _buf(err, 1, "err")
     need = plan_workspace_size(R, T, K, E, S)
-    ws = _new((max(need, 4),), topk_ids, torch.uint8) if ws is None else ws
+    ws = _new((max(need, 4),), topk_ids, stream, torch.uint8) if ws is None else ws
     _check(LIB.uep_plan(_p(topk_ids), R, T, K, E, S, q_min, r_begin, r_end, _p(o["counts"]),
                         _p(o["bucket_pos"]), _p(o["slot_expert"]), _p(o["inst_expert"]),
                         _p(o["inst_quota"]), _p(o["rank_load"]), _p(o["stats"]), _p(o["xfer"]),
@@ -367,8 +380,9 @@ def gate(logits, K, bias=None, batch_size=None, score=GATE_SOFTMAX, renorm=True,
     _buf(batch_size, R, "batch_size")
     _buf(err, 1, "err")
     n = R * T * K
-    topk_ids = _new((R, T, K), logits) if topk_ids is None else _buf(topk_ids, n, "topk_ids")
-    gate_w = _new((R, T, K), logits, torch.float32) if gate_w is None \
+    topk_ids = _new((R, T, K), logits, stream) if topk_ids is None \
+        else _buf(topk_ids, n, "topk_ids")
+    gate_w = _new((R, T, K), logits, stream, torch.float32) if gate_w is None \
         else _buf(gate_w, n, "gate_w", torch.float32)
     _check(LIB.uep_gate(_p(logits), dt, _p(bias), _p(batch_size), R, T, E, K, score,
                         1 if renorm else 0, scale, _p(topk_ids), _p(gate_w), _p(err), _s(stream)),
@@ -391,7 +405,7 @@ def gate_grad(dgate_w, logits, topk_ids, gate_w, score=GATE_SOFTMAX, renorm=True
     _buf(gate_w, R * T * K, "gate_w", torch.float32)
     _buf(dgate_w, R * T * K, "dgate_w", torch.float32)
     _buf(err, 1, "err")
-    dlogits = _new((R, T, E), logits, logits.dtype) if dlogits is None \
+    dlogits = _new((R, T, E), logits, stream, logits.dtype) if dlogits is None \
         else _buf(dlogits, R * T * E, "dlogits", logits.dtype)
     if dlogits.dtype != logits.dtype:
         raise TypeError("dlogits must have the logits' dtype")
@@ -438,7 +452,7 @@ def combine_grad(dy, out, dest_row, gate_w, dout, dgate_w=None, r_begin=0, r_end
             raise TypeError("dgate_w needs the expert outputs `out`")
     else:
         _bf16_rows(out, (P, H), "out")
-        dgate_w = _new((R, T, K), dy, torch.float32) if dgate_w is None else dgate_w
+        dgate_w = _new((R, T, K), dy, stream, torch.float32) if dgate_w is None else dgate_w
         if dgate_w.dtype != torch.float32 or tuple(dgate_w.shape) != (R, T, K):
             raise TypeError("dgate_w must be float32 [R][T][K]")
     _buf(err, 1, "err")
@@ -536,7 +550,7 @@ def adamw_prepare(params, grads, m, v, copies=None, tops=None, weight_decay=0.0,
                at.get("copies", none), sizes, wd, ls)
     table = (AdamWTensor * max(n, 1))(*[AdamWTensor(*row) for row in rows])
     need = int(LIB.uep_adamw_plan_size(table, n))
-    buf = torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    buf = _fresh((max(need, 16),), torch.uint8, dev, stream)
     tiles = ctypes.c_int64(0)
     _check(LIB.uep_adamw_prepare(table, n, pd, gd, bits, _p(buf), buf.numel(),
                                  ctypes.byref(tiles), _s(stream)), "uep_adamw_prepare")
@@ -565,8 +579,8 @@ def adamw_decode(m_codes, v_codes, tops, m=None, v=None, dtype=torch.float32, st
     _buf(m_codes, n, "m_codes", torch.uint8)
     _buf(v_codes, n, "v_codes", torch.uint8)
     _buf(tops, -(-n // ADAMW_BLOCK), "tops")
-    m = _new(m_codes.shape, m_codes, dtype) if m is None else m
-    v = _new(m_codes.shape, m_codes, dtype) if v is None else v
+    m = _new(m_codes.shape, m_codes, stream, dtype) if m is None else m
+    v = _new(m_codes.shape, m_codes, stream, dtype) if v is None else v
     dt = _dtype(m, "m")
     _buf(m, n, "m", m.dtype)
     _buf(v, n, "v", m.dtype)
@@ -617,13 +631,13 @@ def waterfill(counts, topk_ids, batch_size, seed, layer, local_pref_shift=4, sha
     R, E = counts.shape
     _, T, K = topk_ids.shape
     _buf(batch_size, R, "batch_size")
-    shared_rank = _new((R, T), counts) if shared_rank is None else _buf(shared_rank, R * T,
-                                                                       "shared_rank")
-    waterline = _new((1,), counts) if waterline is None else _buf(waterline, 1, "waterline")
-    slack = _new((R,), counts) if slack is None else _buf(slack, R, "slack")
-    rank_load = _new((R,), counts) if rank_load is None else _buf(rank_load, R, "rank_load")
+    shared_rank = _new((R, T), counts, stream) if shared_rank is None \
+        else _buf(shared_rank, R * T, "shared_rank")
+    waterline = _new((1,), counts, stream) if waterline is None else _buf(waterline, 1, "waterline")
+    slack = _new((R,), counts, stream) if slack is None else _buf(slack, R, "slack")
+    rank_load = _new((R,), counts, stream) if rank_load is None else _buf(rank_load, R, "rank_load")
     if ext_topk is None and want_ext:
-        ext_topk = _new((R, T, K + 1), counts)
+        ext_topk = _new((R, T, K + 1), counts, stream)
     else:
         _buf(ext_topk, R * T * (K + 1), "ext_topk")
     _check(LIB.uep_waterfill(_p(counts), _p(topk_ids), _p(batch_size), R, T, K, E,
@@ -661,7 +675,7 @@ def lplb_prepare(inst_expert_host, R, E, inst_per_rank, device, stream=None) -> 
     if ie.size != R * inst_per_rank:
         raise TypeError(f"inst_expert must have R * inst_per_rank = {R * inst_per_rank} entries")
     n = lplb_struct_size(R, E, inst_per_rank)
-    buf = torch.empty((max(n, 16),), dtype=torch.uint8, device=device)
+    buf = _fresh((max(n, 16),), torch.uint8, device, stream)
     _check(LIB.uep_lplb_prepare(ie.ctypes.data_as(ctypes.c_void_p), R, E, inst_per_rank,
                                 _p(buf), buf.numel(), _s(stream)), "uep_lplb_prepare")
     copies = np.bincount(ie[(ie >= 0) & (ie < E)], minlength=E)
@@ -689,13 +703,13 @@ def lplb(counts, lp, n_copies=None, n_inst=None, iters=30, x=None, m=None, inst_
         raise TypeError(f"n_copies {n_copies} != the structure's {lp.n} copies")
     if n_inst is not None and n_inst != lp.I:
         raise TypeError(f"n_inst {n_inst} != the structure's {lp.I} instances")
-    x = torch.empty((max(lp.n, 1),), dtype=torch.float32, device=counts.device) if x is None \
+    x = _new((max(lp.n, 1),), counts, stream, torch.float32) if x is None \
         else _buf(x, max(lp.n, 1), "x", torch.float32)
-    m = torch.empty((1,), dtype=torch.float32, device=counts.device) if m is None \
+    m = _new((1,), counts, stream, torch.float32) if m is None \
         else _buf(m, 1, "m", torch.float32)
-    inst_quota = _new((lp.I,), counts) if inst_quota is None else _buf(inst_quota, lp.I,
-                                                                        "inst_quota")
-    stats = _new((4,), counts) if stats is None else _buf(stats, 4, "stats")
+    inst_quota = _new((lp.I,), counts, stream) if inst_quota is None \
+        else _buf(inst_quota, lp.I, "inst_quota")
+    stats = _new((4,), counts, stream) if stats is None else _buf(stats, 4, "stats")
     _buf(err, 1, "err")
     _check(LIB.uep_lplb(_p(counts), _p(lp.buf), iters, _p(x), _p(m), _p(inst_quota), _p(stats),
                         _p(err), _s(stream)), "uep_lplb")
@@ -729,10 +743,10 @@ def lplb_plan(topk_ids, lp, inst_expert, iters=30, r_begin=0, r_end=None, out=No
         n = 1
         for d in shp:
             n *= d
-        o[k] = _new(shp, topk_ids, dt) if o.get(k) is None else _buf(o[k], n, k, dt)
+        o[k] = _new(shp, topk_ids, stream, dt) if o.get(k) is None else _buf(o[k], n, k, dt)
     _buf(err, 1, "err")
     need = lplb_plan_workspace_size(R, T, K, E, lp.inst_per_rank)
-    ws = _new((max(need, 4),), topk_ids, torch.uint8) if ws is None else ws
+    ws = _new((max(need, 4),), topk_ids, stream, torch.uint8) if ws is None else ws
     _check(LIB.uep_lplb_plan(_p(topk_ids), R, T, K, E, _p(lp.buf), lp.inst_per_rank,
                              _p(inst_expert), iters, r_begin, r_end, _p(o["counts"]),
                              _p(o["bucket_pos"]), _p(o["x"]), _p(o["m"]), _p(o["inst_quota"]),
@@ -751,8 +765,8 @@ def lplb_sample(topk_ids, lp, x, seed, layer, dest_inst=None, err=None, stream=N
     if R != lp.R:
         raise TypeError(f"topk_ids has {R} ranks, the LP structure {lp.R}")
     _buf(x, lp.n, "x", torch.float32)
-    dest_inst = _new((R, T, K), topk_ids) if dest_inst is None else _buf(dest_inst, R * T * K,
-                                                                         "dest_inst")
+    dest_inst = _new((R, T, K), topk_ids, stream) if dest_inst is None \
+        else _buf(dest_inst, R * T * K, "dest_inst")
     _buf(err, 1, "err")
     _check(LIB.uep_lplb_sample(_p(topk_ids), R, T, K, _p(lp.buf), _p(x),
                                ctypes.c_uint64(seed & (2 ** 64 - 1)),

@@ -304,3 +304,26 @@ def test_a_rate_that_is_not_a_number_shows(param, eight):
         sched = sched.to(DEV).view(torch.float32)
         U.adamw(plan, torch.ones(1, dtype=torch.int32, device=DEV), sched, seed=3)
         assert bool(torch.isnan(p).all()), hex(word)
+
+
+def busy():
+    """Work on the current stream that takes some 20 ms, and no answer from the device."""
+    x = torch.empty(1 << 28, device=DEV)
+    for _ in range(100):
+        x.fill_(1.0)
+
+
+def test_a_plan_made_on_another_stream_is_whole():
+    """The table of tensors outlives what the current stream still does with its memory."""
+    say("case: adamw, a plan made on another stream")
+    p, g, m, v = (torch.ones(5000, device=DEV) for _ in range(4))
+    want = U.adamw_prepare([p], [g], [m], [v]).buf.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    old = torch.empty_like(want)
+    busy()
+    old.fill_(7)
+    old = None                                                   # freed, the fill still queued
+    plan = U.adamw_prepare([p], [g], [m], [v], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(plan.buf, want)

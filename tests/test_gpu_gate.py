@@ -344,3 +344,31 @@ def test_a_bias_is_checked_behind_a_masked_logit(E, K):
         ids, w, err = run_gate(x, K, bias=bias, score=1)
         assert err == want, value
         assert (ids != 7).all() and (ids >= 0).all() and np.isfinite(w).all()
+
+
+def busy():
+    """Work on the current stream that takes some 20 ms, and no answer from the device."""
+    x = torch.empty(1 << 28, device=DEV)
+    for _ in range(100):
+        x.fill_(1.0)
+
+
+def test_outputs_for_another_stream():
+    """Outputs that a call allocates for `stream` are not touched by what the current stream
+    still has to do with the same memory."""
+    say("case: gate, outputs for another stream")
+    x = draw_logits(95, 1, 4000, 64, F).to(DEV)
+    ids0, w0 = U.gate(x, 8)
+    d0 = U.gate_grad(w0, x, ids0, w0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, want in ((lambda: U.gate(x, 8, stream=side), (ids0, w0)),
+                       (lambda: (U.gate_grad(w0, x, ids0, w0, stream=side),), (d0,))):
+        old = [torch.empty_like(t) for t in want]
+        busy()
+        for t in old:
+            t.fill_(7)
+        t = old = None                                           # freed, the fills still queued
+        got = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
