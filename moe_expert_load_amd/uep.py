@@ -153,6 +153,16 @@ def _new(shape, like: torch.Tensor, stream, dtype=torch.int32) -> torch.Tensor:
     return _fresh(shape, dtype, like.device, stream)
 
 
+def _table_stream(buf: torch.Tensor, home: int, stream) -> ctypes.c_void_p:
+    """The stream of a call that reads `buf`, a table made while `home` was current: on any
+    other, the table's memory is not given away before that stream has passed the call, so the
+    table may be dropped while it runs."""
+    s = _s(stream)
+    if (s.value or 0) != home:
+        buf.record_stream(torch.cuda.current_stream() if stream is None else stream)
+    return s
+
+
 def _buf(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.int32):
     """A caller's buffer for the library to read or write: contiguous, of `dtype` (any
     16-bit type for torch.int16), with at least n elements, since the kernels index it
@@ -472,7 +482,9 @@ class AdamWTensor(ctypes.Structure):
 @dataclasses.dataclass(frozen=True)
 class AdamWPlan:
     """A table of tensors from adamw_prepare: the device buffer, the sizes and types every
-    step passes back, and the tensors themselves, which the plan points into."""
+    step passes back, the tensors themselves, which the plan points into, and the stream that
+    was current (`home`).  It may be dropped while a step runs; tensors that are dropped with it
+    have to be recorded on the step's stream like any others."""
 
     buf: torch.Tensor
     n_tiles: int
@@ -480,6 +492,7 @@ class AdamWPlan:
     grad_dtype: int
     state_bits: int
     tensors: tuple
+    home: int = 0
 
 
 def _per_tensor(x, n, name):
@@ -555,7 +568,7 @@ def adamw_prepare(params, grads, m, v, copies=None, tops=None, weight_decay=0.0,
     _check(LIB.uep_adamw_prepare(table, n, pd, gd, bits, _p(buf), buf.numel(),
                                  ctypes.byref(tiles), _s(stream)), "uep_adamw_prepare")
     keep = tuple(tuple(x) for x in (params, grads, m, v, copies or (), tops or ()))
-    return AdamWPlan(buf, tiles.value, pd, gd, bits, keep)
+    return AdamWPlan(buf, tiles.value, pd, gd, bits, keep, _s(None).value or 0)
 
 
 def adamw(plan, step, sched, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, err=None, stream=None):
@@ -569,7 +582,8 @@ def adamw(plan, step, sched, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, err=None,
     _buf(err, 1, "err")
     _check(LIB.uep_adamw(_p(plan.buf), plan.n_tiles, plan.param_dtype, plan.grad_dtype,
                          plan.state_bits, _p(step), _p(sched), beta1, beta2, eps,
-                         seed & 0xFFFFFFFF, _p(err), _s(stream)), "uep_adamw")
+                         seed & 0xFFFFFFFF, _p(err), _table_stream(plan.buf, plan.home, stream)),
+           "uep_adamw")
 
 
 def adamw_decode(m_codes, v_codes, tops, m=None, v=None, dtype=torch.float32, stream=None):
@@ -666,6 +680,7 @@ class LPStruct:
     I: int
     G: int
     n: int
+    home: int = 0       # the stream that was current when the buffer was made
 
 
 def lplb_prepare(inst_expert_host, R, E, inst_per_rank, device, stream=None) -> LPStruct:
@@ -681,7 +696,7 @@ def lplb_prepare(inst_expert_host, R, E, inst_per_rank, device, stream=None) -> 
     copies = np.bincount(ie[(ie >= 0) & (ie < E)], minlength=E)
     rep = copies >= 2
     return LPStruct(buf, R, E, inst_per_rank, R * inst_per_rank, int(rep.sum()),
-                    int(copies[rep].sum()))
+                    int(copies[rep].sum()), _s(None).value or 0)
 
 
 def _lp(lp) -> LPStruct:
@@ -712,7 +727,7 @@ def lplb(counts, lp, n_copies=None, n_inst=None, iters=30, x=None, m=None, inst_
     stats = _new((4,), counts, stream) if stats is None else _buf(stats, 4, "stats")
     _buf(err, 1, "err")
     _check(LIB.uep_lplb(_p(counts), _p(lp.buf), iters, _p(x), _p(m), _p(inst_quota), _p(stats),
-                        _p(err), _s(stream)), "uep_lplb")
+                        _p(err), _table_stream(lp.buf, lp.home, stream)), "uep_lplb")
     return x[:lp.n], m, inst_quota, stats
 
 
@@ -752,7 +767,8 @@ def lplb_plan(topk_ids, lp, inst_expert, iters=30, r_begin=0, r_end=None, out=No
                              _p(o["bucket_pos"]), _p(o["x"]), _p(o["m"]), _p(o["inst_quota"]),
                              _p(o["stats"]), _p(o["xfer"]), _p(o["inst_offset"]),
                              _p(o["dest_inst"]), _p(o["dest_row"]), _p(err), _p(ws),
-                             ws.numel() * ws.element_size(), _s(stream)), "uep_lplb_plan")
+                             ws.numel() * ws.element_size(),
+                             _table_stream(lp.buf, lp.home, stream)), "uep_lplb_plan")
     o["inst_per_rank"] = lp.inst_per_rank
     return o
 
@@ -771,5 +787,5 @@ def lplb_sample(topk_ids, lp, x, seed, layer, dest_inst=None, err=None, stream=N
     _check(LIB.uep_lplb_sample(_p(topk_ids), R, T, K, _p(lp.buf), _p(x),
                                ctypes.c_uint64(seed & (2 ** 64 - 1)),
                                ctypes.c_uint64(layer & (2 ** 64 - 1)), _p(dest_inst), _p(err),
-                               _s(stream)), "uep_lplb_sample")
+                               _table_stream(lp.buf, lp.home, stream)), "uep_lplb_sample")
     return dest_inst

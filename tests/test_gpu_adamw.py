@@ -327,3 +327,30 @@ def test_a_plan_made_on_another_stream_is_whole():
     plan = U.adamw_prepare([p], [g], [m], [v], stream=side)
     torch.cuda.synchronize()
     assert torch.equal(plan.buf, want)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_a_plan_may_be_dropped_while_a_step_runs(given):
+    """A step waits on another stream (given, or the current one then) while its plan is dropped:
+    the memory of its table is not handed out again before."""
+    say("case: adamw, a plan dropped while a step runs", given)
+    n = 50000
+    sets = [[torch.full((n,), 0.5, device=DEV) for _ in range(4)] for _ in range(2)]
+    step = torch.ones(1, dtype=torch.int32, device=DEV)
+    sched = torch.tensor([1e-3, 1.0], device=DEV)
+    U.adamw(U.adamw_prepare(*[[x] for x in sets[0]]), step, sched)
+    plan = U.adamw_prepare(*[[x] for x in sets[1]])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    where, size = plan.buf.data_ptr(), plan.buf.numel()
+    with torch.cuda.stream(side):
+        busy()
+        if not given:
+            U.adamw(plan, step, sched)
+    if given:
+        U.adamw(plan, step, sched, stream=side)
+    plan = None
+    others = [torch.empty(size, dtype=torch.uint8, device=DEV) for _ in range(20)]
+    assert all(x.data_ptr() != where for x in others)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*sets))
