@@ -537,6 +537,9 @@ __global__ __launch_bounds__(kGtThreads) void gate_grad_kernel(
     const int64_t stretch = n_tok * E - g0 * E + lead;   // elements of src up to its end
     for (int o = 0; o < total + lead; o += kGtWin) {
       const bool mine = on && pos >= o && pos < o + kGtWin;
+      // zeros of other lanes (the first ones, or those put back) before values in their places
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
       if (mine) win[pos - o] = d;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();

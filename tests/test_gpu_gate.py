@@ -372,3 +372,21 @@ def test_outputs_for_another_stream():
         got = call()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("R,T,E,K,dtype,score,renorm,masked", [
+    (1, 70001, 27, 8, F, 0, True, 0.1),         # a wave's second group of 8 tokens
+    (1, 70001, 27, 8, B, 0, False, 0.0),        # the same, dense
+    (1, 70001, 30, 7, F, 1, False, 0.0),
+    (1, 70001, 30, 7, B, 1, True, 0.3),
+    (3, 11003, 61, 9, F, 0, False, 0.2),        # second and third groups of 4 tokens
+    (3, 11003, 61, 9, B, 1, True, 0.0),
+    (1, 20001, 70, 33, F, 0, True, 0.0),        # a token a wave, up to three turns
+    (1, 20001, 70, 33, B, 0, False, 0.1),
+    (1, 8200, 1111, 40, F, 0, False, 0.0),      # rows over more than one window
+    (1, 8200, 1111, 40, B, 1, False, 0.0),
+])
+def test_gradient_of_many_tokens(R, T, E, K, dtype, score, renorm, masked):
+    """More groups of tokens than waves, which take the next with the window of the last."""
+    say("case: gate_grad, many tokens", R, T, E, K, dtype, score, renorm, masked)
+    check(200 + E + K, R, T, E, K, dtype, score, renorm, 1.0, masked)
