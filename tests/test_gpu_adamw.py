@@ -354,3 +354,53 @@ def test_a_plan_may_be_dropped_while_a_step_runs(given):
     assert all(x.data_ptr() != where for x in others)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(*sets))
+
+
+@pytest.mark.parametrize("param,eight", [(B, True), (F, True), (B, False)])
+def test_steps_repeat_their_bits(param, eight):
+    """The same states, seed and gradients give the same bits, step after step; another seed
+    gives others."""
+    say("case: adamw, repeated", param, eight)
+    n = 70001
+
+    def train(seed):
+        rng = np.random.default_rng(107)
+        p, g, m, v, tops = draw(rng, n, param, param, eight, 0)
+        plan = U.adamw_prepare([p], [g], [m], [v], tops=[tops] if eight else None,
+                               weight_decay=0.1)
+        step, sched = torch.zeros(1, dtype=torch.int32, device=DEV), torch.tensor([1e-3, 1.0],
+                                                                                 device=DEV)
+        for _ in range(6):
+            step += 1
+            U.adamw(plan, step, sched, seed=seed)
+        return [p, m, v] + ([tops] if eight else [])
+
+    a, b, c = train(5), train(5), train(6)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert not torch.equal(a[0], c[0])
+
+
+def test_bf16_copies_of_every_parameter():
+    """All 2^32 words as parameters, a step that changes none (signalling NaNs become quiet): the
+    copy is the nearest bf16, ties to even, a NaN its upper half."""
+    say("case: adamw, bf16 copies of every word")
+    n = 1 << 28
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GiB of device memory")
+    g = torch.zeros(n, device=DEV)
+    p, copy = torch.empty(n, device=DEV), torch.empty(n, dtype=B, device=DEV)
+    m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    plan = U.adamw_prepare([p], [g], [m], [v], copies=[copy])
+    one = torch.ones(1, dtype=torch.int32, device=DEV)
+    sched = torch.tensor([0.0, 1.0], device=DEV)
+    for k in range(16):
+        word = torch.arange(n, dtype=torch.int32, device=DEV) + (k - 8) * n
+        p.view(torch.int32).copy_(word)
+        U.adamw(plan, one, sched)
+        nan = (word & 0x7FFFFFFF) > 0x7F800000
+        word = torch.where(nan, word | 0x400000, word)
+        assert torch.equal(p.view(torch.int32), word), k
+        near = torch.where(nan, word, word + 0x7FFF + ((word >> 16) & 1)) >> 16
+        assert torch.equal(copy.view(torch.int16), near.to(torch.int16)), k
+    del g, p, copy, m, v, plan, word, nan, near
+    torch.cuda.empty_cache()

@@ -390,3 +390,80 @@ def test_gradient_of_many_tokens(R, T, E, K, dtype, score, renorm, masked):
     """More groups of tokens than waves, which take the next with the window of the last."""
     say("case: gate_grad, many tokens", R, T, E, K, dtype, score, renorm, masked)
     check(200 + E + K, R, T, E, K, dtype, score, renorm, 1.0, masked)
+
+
+# The sorting kernel's forms above 8192 tokens: 4 lanes of 32 or 64 experts and 8 of 64, with
+# lists of 4, 8 and 16 (above 512 experts 16 lanes of 64 at any number of tokens); 61, 324 and
+# 702 end inside a 16-byte vector of at least one type.
+@pytest.mark.parametrize("E", [61, 128, 200, 256, 324, 512, 702])
+@pytest.mark.parametrize("K", [3, 8, 16])
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("score", [0, 1])
+def test_gate_of_many_tokens(E, K, dtype, score):
+    say("case: gate, many tokens", E, K, dtype, score)
+    seed, T = E * 64 + K * 4 + score, 2801 if E <= 512 else 301
+    check(seed, 3, T, E, K, dtype, score, True, 2.5, 0.0)
+    check(seed + 1, 3, T, E, K, dtype, score, False, 1.0, 0.97 if E > 200 else 0.6,
+          bs=np.array([T, 0, T - 77], np.int32))
+
+
+@pytest.mark.parametrize("E", [60, 128, 256, 384, 512, 1024])
+@pytest.mark.parametrize("K", [1, 8, 13])
+@pytest.mark.parametrize("dtype", [F, B])
+def test_ties_and_special_logits_of_many_tokens(E, K, dtype):
+    """Whole numbers tie often; ids are those of the oracle to the last, with -0, -infinity, the
+    type's lowest value, +infinity and NaN among them, by the logits and with a bias that only
+    masks (scores of whole numbers below 9 are far apart)."""
+    say("case: gate, ties of many tokens", E, K, dtype)
+    rng = np.random.default_rng(E + K)
+    T = 4600 if E <= 512 else 600
+    x = torch.from_numpy(rng.integers(-8, 9, (2, T, E)).astype(np.float32))
+    x[0, 0], x[0, 1], x[0, 2] = 0.0, -float("inf"), torch.finfo(dtype).min
+    x[0, 3] = torch.tensor([0.0, -0.0] * (E // 2))
+    x[0, 4, 5:] = -float("inf")
+    x[1, :, 3] = -float("inf")
+    x = x.to(dtype)
+    bias = np.where(np.arange(E) % 5 == 1, -np.inf, 0.0).astype(np.float32)
+    for score, b in ((0, None), (1, None), (1, bias)):
+        ids, w, err = run_gate(x, K, bias=b, score=score)
+        y = x.double()
+        if b is not None:                # the lowest value's score is 0, and 0 ties with 0
+            y = y.clamp(min=-100.0).masked_fill(x == -float("inf"), -float("inf"))
+        assert err == 0 and np.array_equal(ids, O.gate(y.numpy(), K, b, score=score)[0])
+        assert np.isfinite(w).all() and ((ids >= 0) | (w == 0)).all()
+    bad = x.clone()
+    bad[1, 77, 1], bad[1, T - 1, E - 1] = float("nan"), float("inf")
+    ids, w, err = run_gate(bad, K)
+    assert err == U.ERR_LOGIT and np.array_equal(ids, O.gate(bad.double().numpy(), K)[0])
+    assert np.isfinite(w).all()
+
+
+@pytest.mark.parametrize("E,K", [(40, 17), (256, 24), (300, 20), (1000, 33), (1024, 64), (1025, 1),
+                                 (7, 5), (3, 2)])
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("score", [0, 1])
+def test_gate_of_many_slots_or_few_experts(E, K, dtype, score):
+    say("case: gate, many slots", E, K, dtype, score)
+    for renorm in (True, False):
+        check(E + K, 2, 90, E, K, dtype, score, renorm, 1.5, 0.3, bs=np.array([90, 31], np.int32))
+
+
+def test_calls_follow_the_current_stream(monkeypatch):
+    """Without `stream` a call goes to the current one, by either way of asking torch for it."""
+    say("case: gate, the current stream")
+    assert U._RAW_STREAM is not None
+    x = draw_logits(97, 1, 3000, 128, F).to(DEV)
+    want = U.gate(x, 8)
+    side = torch.cuda.Stream()
+    for raw in (U._RAW_STREAM, None):
+        monkeypatch.setattr(U, "_RAW_STREAM", raw)
+        assert (U._s(None).value or 0) == torch.cuda.current_stream().cuda_stream
+        late = torch.zeros_like(x)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            assert U._s(None).value == side.cuda_stream
+            busy()
+            late.copy_(x)                                        # queued on `side` before the call
+            got = U.gate(late, 8)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -264,3 +264,29 @@ def test_dispatch_buffers_without_rows():
         call(err)
         assert int(host(err)[0]) == U.ERR_ROW_RANGE
     assert (host(dw) == 0).all()
+
+
+# More tokens than the calls spread over waves, slots in pairs, fours and eights, and rows of 1,
+# 2, 4 and 8 vectors a lane, whole and ragged, up to more than one slice of 8 KiB.
+@pytest.mark.parametrize("K", [1, 2, 3, 5, 9])
+@pytest.mark.parametrize("H", [64, 256, 512, 520, 1024, 1032, 2048, 7168])
+def test_row_calls_of_many_tokens(K, H):
+    say("case: row calls, many tokens", K, H)
+    test_combine_grad((300 + K, 2, 520, K, 12, H, 0.1))
+    test_permute_grad((400 + K, 2, 520, K, 12, H, 0.1))
+    dr, dy, out, w = make(500 + K, 2, 520, K, 12, H, 0.1)
+    for toks in (520, 30):                               # many tokens, and few
+        d, wt = np.ascontiguousarray(dr[:, :toks]), np.ascontiguousarray(w[:, :toks])
+        y = torch.full((2, toks, H), 77, dtype=torch.int16, device=DEV).view(torch.bfloat16)
+        U.combine(out, to_dev(d), to_dev(wt, torch.float32), y)
+        assert np.array_equal(bits(y), O.combine(bits(out), d, wt))
+
+
+@pytest.mark.parametrize("R,T,K,H", [
+    (1, 13000, 8, 256),       # eight 512 B rows together
+    (2, 9000, 5, 1024),       # four 2 KiB rows together
+    (1, 20000, 3, 512),
+    (1, 9000, 3, 1032),
+])
+def test_combine_grad_of_short_rows_in_phases(R, T, K, H):
+    test_combine_grad_in_phases(R, T, K, H)
