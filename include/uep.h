@@ -493,7 +493,7 @@ uep_status uep_gate(const void* logits, int32_t dtype, const float* bias,
  *   softmax           dl_e = s_e (g_e - sum_j u_j g_j), g_e = 0 unless e is selected
  *   sigmoid, renorm   dl_k = u_k (1 - s_k) (g_k - sum_j u_j g_j)
  *   sigmoid           dl_k = u_k (1 - s_k) g_k
- * with 1 - s_k = 1/(1 + exp(l_k)) taken from the logit, so that it keeps its digits near s_k = 1,
+ * with 1 - s_k = 1/(1 + exp(l_k)), which keeps its digits near s_k = 1,
  * and 0 for every other expert.  Slots with id -1 take no part; a token whose slots are
  * all -1 gets zeros.
  *

@@ -467,3 +467,24 @@ def test_calls_follow_the_current_stream(monkeypatch):
             got = U.gate(late, 8)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+def test_sigmoid_gradient_where_its_two_forms_meet(dtype):
+    """Logits from -8 to 12 without renormalisation, with the library's own weights: 1 - s by the
+    weight, whose 6 units of 2^-24 are at most 6 * 64 of it (6 * 256 for bf16), or by the logit (17
+    units up to 12), and 18 for the other factors, relative to the gradient."""
+    say("case: gate_grad, sigmoid from -8 to 12", dtype)
+    E, K, T = 16, 4, 2000
+    x = torch.linspace(-8, 12, T).view(1, T, 1) - 0.01 * torch.arange(E).view(1, 1, E)
+    x = x.to(dtype)
+    ids, w, err = run_gate(x, K, score=1, renorm=False, scale=2.5)
+    dw = np.random.default_rng(99).uniform(0.5, 1.5, (1, T, K)).astype(np.float32)
+    d = host(U.gate_grad(to_dev(dw, torch.float32), x.to(DEV), to_dev(ids),
+                         to_dev(w, torch.float32), score=1, renorm=False, scale=2.5).float())
+    x64 = x.double().numpy()
+    s = 1 / (1 + np.exp(-np.take_along_axis(x64, ids, -1)))
+    want = O.gate_grad(dw, x64, ids, 2.5 * s, 1, False, 2.5)
+    tol = EPS * (6 * 64 + 18) if dtype == F else EPS * (6 * 256 + 18) + 2.0 ** -8
+    assert err == 0 and (np.abs(d - want) <= tol * np.abs(want)).all()
+    assert ((d != 0).sum(-1) == K).all()
