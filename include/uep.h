@@ -462,8 +462,10 @@ uep_status uep_lplb_sample(const int32_t* topk_ids, int32_t R, int32_t T, int32_
  *   weights    w_k = scale * s_k, or with renorm scale * s_k / sum over the selected s
  *              (all weights 0 if that sum is 0)
  * Only finite logits are eligible (and enter the softmax's sum): -infinity, of the logit
- * or of the bias, masks an expert; NaN and +infinity do too and are flagged.  A token with fewer than K eligible experts
- * gets id -1 and weight 0 in the remaining slots.
+ * or of the bias, masks an expert; NaN and +infinity do too and are flagged.  A token with
+ * fewer than K eligible experts gets id -1 and weight 0 in the remaining slots.  The selection is
+ * over all experts; a selection by groups of experts (some routers take the best groups first)
+ * is the caller's, as -infinity in the logits of the groups left out.
  *
  *   logits     [R][T][E]  in   dtype UEP_F32 or UEP_BF16
  *   bias       [E] fp32   in   optional, sigmoid only: enters the selection, not the weights

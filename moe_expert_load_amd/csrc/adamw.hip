@@ -9,7 +9,7 @@
 // Measured on MI355X, 302 M elements in 16 tensors: fp32 states, fp32 parameters and gradients
 // with bf16 copies (30 bytes an element) 1520-1650 us by the buffers' placement, 5.5-5.9 TB/s,
 // bound by HBM: a large copy reaches 5.65.  bf16 parameters and gradients with 8-bit states
-// (10 bytes an element) 560-610 us, bound by its instructions: 72 for every element, of which
+// (10 bytes an element) 556-614 us, bound by its instructions: 77 for every element, of which
 // the random words take 10, the codes' way in 12 and out 20.  The decode 325 us, 5.6 TB/s.
 // Non-temporal accesses are worth 5 % with fp32 states (1700 -> 1610 us, each byte is used
 // once a step), one chunk per wave against four 1-2 % there and 28 % of a small call

@@ -4,9 +4,10 @@
 // (rank, lowest id), so that one maximum names both the winner and its id.  A large call has
 // to move few bytes (262144 tokens of 128 fp32 logits 151 MB, 27 us at the 5.65 TB/s of a
 // large copy) and to compare many numbers: K rounds of a wave maximum per token took 273 us
-// there, the sorting networks below take 30.  With sigmoid scores the instructions bound it:
-// 262144 tokens of 256 bf16 logits and a bias 302 -> 47.5 us, 27 of them memory, about 20
-// instructions for every expert of which 9 sort.  A small call is one launch's latency (2.4 us).
+// there, the sorting networks below take 30.  With a bias on sigmoid scores the instructions bound
+// it: 262144 tokens of 256 bf16 logits 302 -> 47.5 us, 27 of them memory, 90 instructions a token
+// or 23 for every expert, of which 9 sort; ranked by the logits, without a bias, 36.3.  A small
+// call is one launch's latency (2.3 us).
 //
 // Gradient.  Bound by its stores, 134 MB in 34 us for the first of those layers.
 #include <algorithm>
