@@ -67,7 +67,9 @@ enum {
   UEP_ERR_ROW_RANGE = 128,  /* a dest_row entry outside [-1, out_rows) */
   UEP_ERR_LOGIT = 256,      /* a router logit (or logit's bias) that is NaN or +infinity */
   UEP_ERR_GRAD = 512,       /* AdamW: a gradient element that is not finite */
-  UEP_ERR_PLAN = 1024       /* AdamW: not a plan for this call, or a step below 1 */
+  UEP_ERR_PLAN = 1024,      /* AdamW: not a plan for this call, or a step below 1 */
+  UEP_ERR_OFFSET = 2048,    /* an offset table that falls or leaves its rows or tokens */
+  UEP_ERR_VALUE = 4096      /* rows to 8 bits: an element that is NaN or infinite */
 };
 
 /* element types of the calls that take more than one */
@@ -631,6 +633,131 @@ uep_status uep_adamw(const void* plan, int64_t n_tiles, int32_t param_dtype,
 uep_status uep_adamw_decode(const uint8_t* m_codes, const uint8_t* v_codes,
                             const int32_t* tops, int64_t n, int32_t dtype, void* m, void* v,
                             void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_balance_loss -- the router's balance loss over sequences of tokens, with the per-expert
+ * counts and mean scores it is made of.  [UEP] section "在 Gate 之后获取当前层真实负载" balances
+ * the load that the Gate produced; the auxiliary loss that keeps that load near even is the
+ * page's point of comparison, not written out there; this is the standard one.  Over the
+ * tokens of sequence g, of which n_g are present (some id is not -1):
+ *   p_te       softmax: exp(l_e) / sum_j exp(l_j);  sigmoid: s_e / sum_j s_j, s = 1/(1 + exp(-l))
+ *   counts_ge  ids of expert e;   prob_ge = (sum of p_te over the present tokens) / n_g
+ *   loss_g     E / (K n_g) * sum_e counts_ge prob_ge     (1 where both are even; 0 if n_g is 0)
+ * A call without seq_offset has n_seq equal sequences of the R*T tokens in order (n_seq = R: a
+ * loss for each rank's microbatch; 1: for the whole group).  -infinity masks an expert; NaN
+ * and +infinity do too and are flagged; a token without a finite logit has p = 0.  A
+ * sigmoid score below 2^-126 counts as 0.
+ *
+ *   logits     [R][T][E]    in   dtype UEP_F32 or UEP_BF16
+ *   topk_ids   [R][T][K]    in   -1: empty slot
+ *   seq_offset [n_seq + 1]  in   optional: sequence g is the tokens r*T + t in
+ *                                [seq_offset[g], seq_offset[g+1]), may be empty; tokens outside
+ *                                of all belong to none.  Not falling, within [0, R*T]
+ *   score                        UEP_GATE_SOFTMAX or UEP_GATE_SIGMOID
+ *   loss [n_seq] fp32, counts [n_seq][E], prob [n_seq][E] fp32, tokens [n_seq]    out
+ *                                (n_g).  None may overlap another array
+ *   err                     out  optional; UEP_ERR_LOGIT, UEP_ERR_ID_RANGE (such an id is taken
+ *                                as -1), UEP_ERR_OFFSET
+ *   ws, ws_bytes                 uep_balance_loss_workspace_size(), 16-byte aligned
+ * Sums over tokens are fp32 within a block of tokens and 64 bits across blocks, in an order that
+ * depends on the geometry and seq_offset alone (the same call gives the same bits).
+ * Returns UEP_EINVAL for null pointers, sizes < 1 (T may be 0: every output is 0), an unknown
+ * dtype or score, overlapping outputs; UEP_EGEOM for R > 64, E > 4096, K > 64, n_seq > 65535,
+ * n_seq*E >= 2^31, R*T >= 2^26, R*T*K >= 2^31, or R*T no multiple of n_seq without seq_offset.
+ * ------------------------------------------------------------------------- */
+size_t uep_balance_loss_workspace_size(int32_t R, int32_t T, int32_t E, int32_t n_seq);
+uep_status uep_balance_loss(const void* logits, int32_t dtype, const int32_t* topk_ids,
+                            const int32_t* seq_offset, int32_t n_seq, int32_t R, int32_t T,
+                            int32_t E, int32_t K, int32_t score, float* loss, int32_t* counts,
+                            float* prob, int32_t* tokens, int32_t* err, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_balance_loss_grad -- gradient of uep_balance_loss with respect to the logits (the
+ * counts are piecewise constant).  For a present token of sequence g
+ *   dl_e = dloss_g E / (K n_g^2) p_e (counts_ge - sum_j counts_gj p_j)      softmax
+ *   the same times 1 - s_e                                                  sigmoid
+ * and 0 for other tokens.  With counts and tokens summed over more microbatches than the
+ * logits' own, dloss is scaled by their ratio n_own / n_all by the caller.
+ *
+ *   dloss      [n_seq] fp32    in   gradient of each sequence's loss (device memory)
+ *   logits, topk_ids, seq_offset, score    as given to uep_balance_loss
+ *   counts [n_seq][E], tokens [n_seq]      as written by it
+ *   add        [R][T][E]       in   optional: what the gradient is added to, e.g. that of
+ *                                   uep_gate_grad; the logits' dtype; may be `dlogits` itself
+ *   dlogits    [R][T][E]       out  the logits' dtype; every element is written (one rounding);
+ *                                   overlapping an input in no other way (UEP_EINVAL)
+ *   err                        out  optional; UEP_ERR_LOGIT, UEP_ERR_ID_RANGE, UEP_ERR_OFFSET
+ * Returns UEP_EINVAL / UEP_EGEOM like uep_balance_loss.
+ * ------------------------------------------------------------------------- */
+uep_status uep_balance_loss_grad(const float* dloss, const void* logits, int32_t dtype,
+                                 const int32_t* topk_ids, const int32_t* counts,
+                                 const int32_t* tokens, const int32_t* seq_offset,
+                                 int32_t n_seq, int32_t R, int32_t T, int32_t E, int32_t K,
+                                 int32_t score, const void* add, void* dlogits, int32_t* err,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * Rows in 8 bits.  A bf16 row x becomes integers q in [-127, 127] and one fp32 scale:
+ *   scale = max(fp32(max_h |x_h| / 127), 2^-126),   q_h = x_h / scale to the nearest integer,
+ * the exact quotient, ties to even.  A NaN becomes 0 and an infinity +-127, are flagged and
+ * take no part in the maximum.
+ *
+ * uep_quant_rows: rows in place of each other (expert outputs between two products; the output
+ *   channels of a weight matrix, once).
+ *     x [rows][H] bf16   in   16-byte aligned, H % 16 == 0, H <= 65536
+ *     live_rows [1]      in   optional, device memory: rows at or past it are neither read nor
+ *                             written (inst_offset[I] of uep_reroute_assign)
+ *     q [rows][H] int8, scale [rows] fp32   out   q 16-byte aligned; not overlapping each other
+ *                             or an input
+ * uep_permute_quant: the dispatch in 8 bits, uep_permute with half the bytes written: every
+ *   token's row is put into 8 bits once and goes to each of its K dispatch rows.
+ *     x, dest_row, R, T, K, r_begin, r_end   as uep_permute
+ *     q [out_rows][H], scale [out_rows]      out; rows that no slot names are left as they are
+ * err   optional; UEP_ERR_VALUE, UEP_ERR_ROW_RANGE (such an entry is taken as no row)
+ * Returns UEP_EINVAL for null pointers, negative sizes, overlaps; UEP_EGEOM for H or an
+ * alignment that does not fit, and the limits above.
+ * ------------------------------------------------------------------------- */
+uep_status uep_quant_rows(const uint16_t* x, int64_t rows, int32_t H, const int32_t* live_rows,
+                          int8_t* q, float* scale, int32_t* err, void* stream);
+uep_status uep_permute_quant(const uint16_t* x, const int32_t* dest_row, int32_t R, int32_t T,
+                             int32_t K, int32_t H, int32_t r_begin, int32_t r_end, int8_t* q,
+                             float* scale, int64_t out_rows, int32_t* err, void* stream);
+
+/* ------------------------------------------------------------------------- *
+ * uep_expert_product -- the experts' matrix product over the dispatch buffer, in 8-bit
+ * integers with a scale for each row and each output channel.  [UEP] section "共享冗余 slot
+ * 管理动态专家副本": an instance is its rank's main or a replica in a redundant slot, each with
+ * weights of its own; this runs all of them on the rows that the plan gave them.
+ *   z[p][n] = sum_d q[p][d] w[n][d]  (exact, int32);  y[p][n] = z w_scale[n] q_scale[p]  in fp32
+ *   UEP_PRODUCT_PLAIN    out[p][n] = bf16(y[p][n])                                      n < N
+ *   UEP_PRODUCT_SWIGLU   out[p][n] = bf16(silu(y[p][n]) y[p][N/2 + n])                n < N/2
+ * with silu(g) = g / (1 + exp(-g)) (hardware exp2 and reciprocal, each within a unit in the last
+ * place) and w those of the row's instance i = r * (E/R + S) + j: main r*E/R + j for j < E/R,
+ * slot (r, j - E/R) otherwise.  S = 0 and R = 1: one matrix per expert; E = 1 then: a plain
+ * product of all rows (a shared expert).
+ *
+ *   q [rows][D] int8, q_scale [rows] fp32    in   from uep_quant_rows or uep_permute_quant
+ *   inst_offset [I+1]         in   first row of every instance, I = R * (E/R + S); from
+ *                                  uep_reroute_assign.  NULL if I is 1: all rows.  Rows outside
+ *                                  [inst_offset[0], inst_offset[I]) are left as they are
+ *   main_w [E][N][D] int8, main_scale [E][N] fp32    in
+ *   slot_w [R][S][N][D], slot_scale [R][S][N]        in   NULL if S is 0
+ *                                  (uep_stage_replica_weights moves both: N*D/2 and 2*N of its
+ *                                  16-bit elements an expert)
+ *   out [rows][N or N/2] bf16 bits  out   not overlapping an input (UEP_EINVAL)
+ *   err                       out  optional; UEP_ERR_OFFSET: a table that falls or leaves
+ *                                  [0, rows]
+ * q, weights and out 16-byte aligned.  D % 16 == 0, D <= 65536, N % 8 == 0 (SwiGLU: 16),
+ * N*D < 2^31, S <= 8, rows < 2^31; otherwise UEP_EGEOM.
+ * ------------------------------------------------------------------------- */
+enum { UEP_PRODUCT_PLAIN = 0, UEP_PRODUCT_SWIGLU = 1 };
+uep_status uep_expert_product(const int8_t* q, const float* q_scale, int64_t rows,
+                              const int32_t* inst_offset, int32_t R, int32_t E, int32_t S,
+                              const int8_t* main_w, const float* main_scale,
+                              const int8_t* slot_w, const float* slot_scale, int32_t N,
+                              int32_t D, int32_t act, uint16_t* out, int32_t* err,
+                              void* stream);
 
 #ifdef __cplusplus
 }

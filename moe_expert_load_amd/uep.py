@@ -25,10 +25,11 @@ LIB_PATH = os.path.join(_HERE, "libuep.so")
 OK, EINVAL, EGEOM, EWORKSPACE, EHIP = 0, 1, 2, 3, 4
 ERR_ID_RANGE, ERR_DUP_ID, ERR_QUOTA_SUM, ERR_INST_DUP = 1, 2, 4, 8
 ERR_BAD_QUOTA, ERR_COVER, ERR_LP, ERR_ROW_RANGE = 16, 32, 64, 128
-ERR_LOGIT, ERR_GRAD, ERR_PLAN = 256, 512, 1024
+ERR_LOGIT, ERR_GRAD, ERR_PLAN, ERR_OFFSET, ERR_VALUE = 256, 512, 1024, 2048, 4096
 STAGE_WEIGHTS, STAGE_GRAD_REDUCE = 0, 1
 F32, BF16 = 0, 1
 GATE_SOFTMAX, GATE_SIGMOID = 0, 1
+PRODUCT_PLAIN, PRODUCT_SWIGLU = 0, 1
 ADAMW_BLOCK = 256       # elements of one tensor that share an entry of `tops` (8-bit states)
 
 _P = ctypes.c_void_p
@@ -76,6 +77,13 @@ SIGNATURES = {
     "uep_adamw_prepare": (_I, [_P, _I, _I, _I, _I, _P, _SZ, _P, _P]),
     "uep_adamw": (_I, [_P, _I64, _I, _I, _I, _P, _P, _D, _D, _D, _U32, _P, _P]),
     "uep_adamw_decode": (_I, [_P, _P, _P, _I64, _I, _P, _P, _P]),
+    "uep_balance_loss_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "uep_balance_loss": (_I, [_P, _I, _P, _P, _I, _I, _I, _I, _I, _I] + [_P] * 6 + [_SZ, _P]),
+    "uep_balance_loss_grad": (_I, [_P, _P, _I, _P, _P, _P, _P] + [_I] * 6 + [_P] * 4),
+    "uep_quant_rows": (_I, [_P, _I64, _I, _P, _P, _P, _P, _P]),
+    "uep_permute_quant": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I64, _P, _P]),
+    "uep_expert_product": (_I, [_P, _P, _I64, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P,
+                                _P]),
 }
 
 
@@ -601,6 +609,141 @@ def adamw_decode(m_codes, v_codes, tops, m=None, v=None, dtype=torch.float32, st
     _check(LIB.uep_adamw_decode(_p(m_codes), _p(v_codes), _p(tops), n, dt, _p(m), _p(v),
                                 _s(stream)), "uep_adamw_decode")
     return m, v
+
+
+def balance_loss_workspace_size(R, T, E, n_seq=1) -> int:
+    return int(LIB.uep_balance_loss_workspace_size(R, T, E, n_seq))
+
+
+def _sequences(topk_ids, logits, seq_offset, n_seq):
+    """Shapes of a balance call: (R, T, E, K, dtype of the logits)."""
+    if logits.dim() != 3 or topk_ids.dim() != 3:
+        raise TypeError("logits must be [R][T][E] and topk_ids [R][T][K]")
+    _i32(topk_ids, "topk_ids")
+    if topk_ids.shape[:2] != logits.shape[:2]:
+        raise TypeError("logits and topk_ids must have the same [R][T]")
+    if seq_offset is not None:
+        _buf(seq_offset, n_seq + 1, "seq_offset")
+    R, T, E = logits.shape
+    return R, T, E, topk_ids.shape[2], _dtype(logits, "logits")
+
+
+def balance_loss(logits, topk_ids, n_seq=1, seq_offset=None, score=GATE_SOFTMAX, loss=None,
+                 counts=None, prob=None, tokens=None, err=None, ws=None, stream=None):
+    """The router's balance loss: logits [R][T][E] float32 or bfloat16 and topk_ids [R][T][K] ->
+    (loss [n_seq] float32, counts [n_seq][E] int32, prob [n_seq][E] float32, tokens [n_seq]
+    int32).  n_seq equal sequences over the tokens, or those that seq_offset [n_seq + 1] bounds."""
+    R, T, E, K, dt = _sequences(topk_ids, logits, seq_offset, n_seq)
+    f32 = torch.float32
+    loss = _new((n_seq,), logits, stream, f32) if loss is None else _buf(loss, n_seq, "loss", f32)
+    counts = _new((n_seq, E), logits, stream) if counts is None \
+        else _buf(counts, n_seq * E, "counts")
+    prob = _new((n_seq, E), logits, stream, f32) if prob is None \
+        else _buf(prob, n_seq * E, "prob", f32)
+    tokens = _new((n_seq,), logits, stream) if tokens is None else _buf(tokens, n_seq, "tokens")
+    _buf(err, 1, "err")
+    if ws is None:
+        need = balance_loss_workspace_size(R, T, E, n_seq)
+        ws = _new((max(need, 16),), logits, stream, torch.uint8)
+    _check(LIB.uep_balance_loss(_p(logits), dt, _p(topk_ids), _p(seq_offset), n_seq, R, T, E, K,
+                                score, _p(loss), _p(counts), _p(prob), _p(tokens), _p(err), _p(ws),
+                                ws.numel() * ws.element_size(), _s(stream)), "uep_balance_loss")
+    return loss, counts, prob, tokens
+
+
+def balance_loss_grad(dloss, logits, topk_ids, counts, tokens, seq_offset=None,
+                      score=GATE_SOFTMAX, add=None, dlogits=None, err=None, stream=None):
+    """Gradient of balance_loss: dloss [n_seq] float32 -> dlogits [R][T][E] of the logits' dtype,
+    given what balance_loss took and wrote.  With `add` (the gate's gradient, say; may be dlogits
+    itself) the result is added to it."""
+    n_seq = dloss.numel()
+    R, T, E, K, dt = _sequences(topk_ids, logits, seq_offset, n_seq)
+    _buf(dloss, n_seq, "dloss", torch.float32)
+    _buf(counts, n_seq * E, "counts")
+    _buf(tokens, n_seq, "tokens")
+    _buf(add, R * T * E, "add", logits.dtype)
+    _buf(err, 1, "err")
+    dlogits = _new((R, T, E), logits, stream, logits.dtype) if dlogits is None \
+        else _buf(dlogits, R * T * E, "dlogits", logits.dtype)
+    _check(LIB.uep_balance_loss_grad(_p(dloss), _p(logits), dt, _p(topk_ids), _p(counts),
+                                     _p(tokens), _p(seq_offset), n_seq, R, T, E, K, score,
+                                     _p(add), _p(dlogits), _p(err), _s(stream)),
+           "uep_balance_loss_grad")
+    return dlogits
+
+
+def _int8_rows(q, scale, rows, H, like, stream):
+    if q is None:
+        q = _new((rows, H), like, stream, torch.int8)
+    elif q.dtype != torch.int8 or tuple(q.shape) != (rows, H):
+        raise TypeError(f"q must be int8 [{rows}][{H}]")
+    scale = _new((rows,), like, stream, torch.float32) if scale is None \
+        else _buf(scale, rows, "scale", torch.float32)
+    return q, scale
+
+
+def quant_rows(x, q=None, scale=None, live_rows=None, err=None, stream=None):
+    """bf16 rows x [n][H] -> q [n][H] int8 and scale [n] float32, x = q * scale to half a step.
+    live_rows: int32 [1] on the device, rows at or past it are left alone."""
+    if x.dim() != 2:
+        raise TypeError("x must be [n][H]")
+    n, H = x.shape
+    _bf16_rows(x, (n, H), "x")
+    q, scale = _int8_rows(q, scale, n, H, x, stream)
+    _buf(live_rows, 1, "live_rows")
+    _buf(err, 1, "err")
+    _check(LIB.uep_quant_rows(_p(x), n, H, _p(live_rows), _p(q), _p(scale), _p(err), _s(stream)),
+           "uep_quant_rows")
+    return q, scale
+
+
+def permute_quant(x, dest_row, q, scale, r_begin=0, r_end=None, err=None, stream=None):
+    """The dispatch in 8 bits: x [R][T][H] bf16 -> q [P][H] int8 and scale [P] float32, each
+    token's row in all of its dispatch rows (permute and quant_rows in one pass)."""
+    _i32(dest_row, "dest_row")
+    if x.dim() != 3 or q.dim() != 2:
+        raise TypeError("x must be [R][T][H] and q [P][H]")
+    R, T, H = x.shape
+    _bf16_rows(x, (R, T, H), "x")
+    if dest_row.dim() != 3 or tuple(dest_row.shape[:2]) != (R, T):
+        raise TypeError("dest_row must be [R][T][K] for x [R][T][H]")
+    P = q.shape[0]
+    q, scale = _int8_rows(q, scale, P, H, x, stream)
+    r_end = R if r_end is None else r_end
+    _buf(err, 1, "err")
+    _check(LIB.uep_permute_quant(_p(x), _p(dest_row), R, T, dest_row.shape[2], H, r_begin, r_end,
+                                 _p(q), _p(scale), P, _p(err), _s(stream)), "uep_permute_quant")
+    return q, scale
+
+
+def expert_product(q, q_scale, w, w_scale, inst_offset=None, R=1, S=0, slot_w=None,
+                   slot_scale=None, act=PRODUCT_PLAIN, out=None, err=None, stream=None):
+    """The experts' products in 8 bits: rows q [P][D] int8 with q_scale [P], each instance's block
+    [inst_offset[i], inst_offset[i + 1]) by its own weights, mains w [E][N][D] int8 with w_scale
+    [E][N], replicas slot_w [R][S][N][D] with slot_scale [R][S][N] -> out [P][N] bf16, or [P][N / 2]
+    with PRODUCT_SWIGLU (the first N / 2 channels are the gates).  One expert without inst_offset
+    takes all rows."""
+    if q.dim() != 2 or w.dim() != 3 or q.dtype != torch.int8 or w.dtype != torch.int8 or \
+            q.shape[1] != w.shape[2]:
+        raise TypeError("q must be int8 [P][D] and w int8 [E][N][D]")
+    P, D = q.shape
+    E, N, _ = w.shape
+    n_inst = R * (E // max(R, 1) + S)
+    n_out = N // 2 if act == PRODUCT_SWIGLU else N
+    f32 = torch.float32
+    _buf(q_scale, P, "q_scale", f32)
+    _buf(w_scale, E * N, "w_scale", f32)
+    _buf(slot_w, R * S * N * D, "slot_w", torch.int8)
+    _buf(slot_scale, R * S * N, "slot_scale", f32)
+    _buf(inst_offset, n_inst + 1, "inst_offset")
+    _buf(err, 1, "err")
+    if out is None:
+        out = _new((P, n_out), q, stream, torch.bfloat16)
+    _bf16_rows(out, (P, n_out), "out")
+    _check(LIB.uep_expert_product(_p(q), _p(q_scale), P, _p(inst_offset), R, E, S, _p(w),
+                                  _p(w_scale), _p(slot_w), _p(slot_scale), N, D, act, _p(out),
+                                  _p(err), _s(stream)), "uep_expert_product")
+    return out
 
 
 def device_copy(src, dst, stream=None):

@@ -24,7 +24,8 @@ the path itself fixes fp32).  Sources:
     - "背景知识与设计原则", "共享专家融合作为启用机制" (dispatch and combine) -> combine
 
 The training operators around the path (router gate, gradients of dispatch and combine,
-AdamW) are in gate, row_grad and adamw; the pages name these steps without writing them out.
+AdamW, the balance loss) are in gate, row_grad, adamw and balance, the experts' products in 8 bits
+in int8; the pages name these steps without writing them out.
 
 Parity status of each function (what pins it) is listed in the module headers.
 """
@@ -40,6 +41,8 @@ from .waterfill import waterfill, extend_topk
 from .lplb import lplb_structure, lplb_lp, simplex, hamilton_quotas, lplb, lplb_sample
 from .gate import gate, gate_grad, gate_keys
 from .row_grad import permute_grad, combine_grad
+from .balance import balance_loss, balance_loss_grad, balance_shares
+from .int8 import quant_rows, expert_product
 from . import adamw
 
 __all__ = [
@@ -48,4 +51,5 @@ __all__ = [
     "bf16_bits_to_f32", "stage_forward", "grad_reduce", "philox4x64_10", "philox4x64_10_np",
     "waterfill", "extend_topk", "lplb_structure", "lplb_lp", "simplex", "hamilton_quotas", "lplb",
     "lplb_sample", "gate", "gate_grad", "gate_keys", "permute_grad", "combine_grad", "adamw",
+    "balance_loss", "balance_loss_grad", "balance_shares", "quant_rows", "expert_product",
 ]

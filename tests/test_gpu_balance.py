@@ -1,0 +1,313 @@
+"""GPU parity of uep_balance_loss and its gradient against the oracle in 64 bits.
+
+Tolerances, in eps = 2^-24.  A softmax score's exponential takes an argument that is rounded
+twice (2 |d| eps, d the distance to the largest logit) and exp2 adds two more; the sum of a row
+goes through at most 64 + 6 additions, its reciprocal and the product add three: a score is
+within (2 |d| + 2 + 70 + 2 max|d| + 2 + 3) eps.  A sigmoid's exponential is off by (|x| + 2), the rest
+by 3.  Sums over tokens are sums of positive numbers through at most 64 + 6 + 4 additions.  So
+(4 spread + 160) eps relative covers scores, means and losses, with spread the largest |d| or |x|.
+The gradient is h p_e ((c_e - c_0) - dot): the difference of counts is exact, dot is within
+(rel + 75 eps) sum_j p_j |c_j - c_0|; the store rounds by half a step."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import oracle as O                                       # noqa: E402
+from moe_expert_load_amd import uep as U                 # noqa: E402
+from tests.gpu_helpers import DEV, to_dev, host, say, err_word   # noqa: E402
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+# seed, R, T, E, K, sequences (number, or "ragged"), dtype, score
+CASES = [
+    (0, 4, 512, 8, 2, 4, "f32", 0),            # the tiny layer
+    (1, 2, 1500, 128, 8, 1, "f32", 0),         # one loss over several blocks
+    (2, 2, 1500, 128, 8, "ragged", "f32", 1),
+    (3, 4, 700, 256, 8, 4, "bf16", 1),
+    (4, 1, 3001, 256, 8, "ragged", "bf16", 0),
+    (5, 1, 1, 128, 8, 1, "f32", 0),            # one token
+    (6, 1, 1, 64, 6, 1, "bf16", 1),
+    (7, 3, 333, 61, 4, "ragged", "bf16", 0),   # odd rows: vectors at any alignment
+    (8, 3, 333, 99, 4, 3, "f32", 1),
+    (9, 1, 257, 3, 1, 1, "f32", 0),            # rows shorter than a vector
+    (10, 2, 100, 7, 2, "ragged", "bf16", 1),
+    (11, 2, 100, 1, 1, 2, "f32", 0),           # one expert
+    (12, 1, 300, 4, 4, 1, "f32", 1),           # every expert chosen
+    (13, 1, 70, 1000, 16, "ragged", "f32", 0),
+    (14, 1, 60, 4096, 64, 1, "f32", 1),
+    (15, 1, 60, 4096, 10, 2, "bf16", 0),
+    (16, 1, 55, 2500, 8, "ragged", "bf16", 1),
+    (17, 2, 64, 33, 5, 128, "f32", 0),         # a sequence per token
+    (18, 8, 5000, 16, 2, 8, "bf16", 0),
+    (19, 1, 20000, 512, 8, "ragged", "bf16", 1),
+]
+
+
+def make(seed, R, T, E, K, seqs, dtype, score, empty=0.1):
+    rng = np.random.default_rng(seed)
+    n = R * T
+    x = to_dev(rng.normal(size=(R, T, E)) * 2 + rng.normal(size=E), DT[dtype])
+    logits = x.double().cpu().numpy()
+    ids = np.argsort(-logits, axis=-1, kind="stable")[..., :K].astype(np.int32)
+    ids[rng.random((R, T)) < empty] = -1                          # absent tokens
+    ids[rng.random(ids.shape) < 0.05] = -1                        # and single slots
+    if seqs != "ragged":
+        return rng, x, logits, ids, seqs, None
+    G = min(n, 7) + 3
+    cut = np.sort(rng.integers(0, n + 1, G + 1))
+    cut[2] = cut[1]                                               # an empty sequence
+    return rng, x, logits, ids, G, cut.astype(np.int32)
+
+
+def spread(logits, score):
+    f = np.where(np.isfinite(logits), logits, np.nan)
+    f = f.reshape(-1, f.shape[-1])[np.isfinite(logits).any(-1).reshape(-1)]
+    return float(np.nanmax(np.abs(f)) if score else np.nanmax(np.nanmax(f, -1) - np.nanmin(f, -1)))
+
+
+def forward(x, ids_d, G, off, score, err=None):
+    return U.balance_loss(x, ids_d, n_seq=G, seq_offset=off, score=score, err=err)
+
+
+def check_forward(got, logits, ids, G, off, score):
+    loss, counts, prob, tokens = (host(t) for t in got)
+    want = O.balance_loss(logits, ids, G, off, score)
+    rel = (4 * spread(logits, score) + 160) * EPS
+    assert np.array_equal(counts, want[1]) and np.array_equal(tokens, want[3])
+    # scores below 2^-126 may be missing: they are no larger than that
+    assert (np.abs(prob - want[2]) <= rel * want[2] + 2.0 ** -126).all()
+    assert (np.abs(loss - want[0]) <= (rel + 4 * EPS) * want[0]).all()
+    return want
+
+
+def grad_bound(dloss, logits, ids, want, G, off, score):
+    """The oracle's gradient and how far a call may be from it before it is stored."""
+    E, K = logits.shape[-1], ids.shape[-1]
+    ref = O.balance_loss_grad(dloss, logits, ids, want[1], want[3], G, off, score)
+    p, _ = O.balance_shares(logits, score)
+    rel = (4 * spread(logits, score) + 160) * EPS
+    flat = ids.reshape(-1, K)
+    room = np.zeros_like(p)
+    for g, (a, b) in enumerate(O.balance.spans(len(p), G, off)):
+        n = float(want[3][g])
+        if n == 0 or a == b:
+            continue
+        c = want[1][g].astype(float)
+        c0 = np.where(flat[a:b, 0] >= 0, c[np.maximum(flat[a:b, 0], 0)], 0.0)[:, None]
+        mean = (p[a:b] * np.abs(c - c0)).sum(-1, keepdims=True)
+        h = abs(float(dloss[g])) * E / (K * n * n)
+        room[a:b] = h * p[a:b] * ((rel + 8 * EPS) * (np.abs(c - c0) + mean) + (rel + 75 * EPS) * mean)
+    return ref, room.reshape(ref.shape)
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_loss_and_gradient(case):
+    say("case: balance", *case)
+    *_, dtype, score = case
+    rng, x, logits, ids, G, off = make(*case)
+    ids_d, off_d, err = to_dev(ids), None if off is None else to_dev(off), err_word()
+    got = forward(x, ids_d, G, off_d, score, err)
+    want = check_forward(got, logits, ids, G, off, score)
+    again = forward(x, ids_d, G, off_d, score)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))     # the same bits
+
+    dloss = rng.normal(size=G).astype(np.float32)
+    base = to_dev(rng.normal(size=logits.shape) * 1e-3, DT[dtype])
+    dl_d = to_dev(dloss, torch.float32)
+    ref, room = grad_bound(dloss, logits, ids, want, G, off, score)
+    half = torch.finfo(DT[dtype]).eps / 2
+    args = dict(seq_offset=off_d, score=score, err=err)
+    d = U.balance_loss_grad(dl_d, x, ids_d, got[1], got[3], **args)
+    diff = np.abs(d.double().cpu().numpy() - ref)
+    assert (diff <= room + half * (np.abs(ref) + room) + 2.0 ** -133).all()
+    both = U.balance_loss_grad(dl_d, x, ids_d, got[1], got[3], add=base, **args)
+    total = ref + base.double().cpu().numpy()
+    diff = np.abs(both.double().cpu().numpy() - total)
+    assert (diff <= room + (half + EPS) * (np.abs(total) + room) + EPS * np.abs(ref)
+            + 2.0 ** -133).all()
+    place = base.clone()
+    U.balance_loss_grad(dl_d, x, ids_d, got[1], got[3], add=place, dlogits=place, **args)
+    assert torch.equal(place, both)
+    assert int(host(err)[0]) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E", [5, 24, 61, 128])
+def test_masked_and_bad_logits(E, score, dtype):
+    """-infinity and the type's lowest value mask without a word, a row of masks has no scores;
+    NaN and +infinity mask and are flagged; an id out of range is flagged and taken as empty."""
+    say("case: masks", E, score, dtype)
+    low = torch.finfo(DT[dtype]).min
+    rng = np.random.default_rng(E)
+    x = to_dev(rng.normal(size=(1, 40, E)), DT[dtype])
+    x[0, 3] = -float("inf")
+    x[0, 5, ::2] = -float("inf")
+    x[0, 6, 1:] = low
+    x[0, 7, 0] = low
+    logits = x.double().cpu().numpy()
+    ids = rng.integers(0, E, (1, 40, 2)).astype(np.int32)
+    ids[0, 9] = -1
+    err = err_word()
+    got = forward(x, to_dev(ids), 1, None, score, err)
+    # the lowest value is no number to take tolerances from: its scores are 0 on both sides
+    tame = np.where(logits < -1e30, -np.inf, logits)
+    want = check_forward(got, tame, ids, 1, None, score)
+    assert int(host(err)[0]) == 0
+    dl = torch.ones(1, device=DEV)
+    d = U.balance_loss_grad(dl, x, to_dev(ids), got[1], got[3], score=score, err=err)
+    ref, room = grad_bound(np.ones(1), tame, ids, want, 1, None, score)
+    half = torch.finfo(DT[dtype]).eps / 2
+    dn = d.double().cpu().numpy()
+    assert (np.abs(dn - ref) <= room + half * (np.abs(ref) + room) + 2.0 ** -133).all()
+    assert (dn[0, 3] == 0).all() and (dn[0, 9] == 0).all() and int(host(err)[0]) == 0
+
+    x2 = x.clone()
+    x2[0, 11, 1], x2[0, 12, 0] = float("nan"), float("inf")
+    masked = x.clone()
+    masked[0, 11, 1] = masked[0, 12, 0] = -float("inf")
+    ids2, clean = ids.copy(), ids.copy()
+    ids2[0, 15, 0], ids2[0, 16, 1] = E, -7
+    clean[0, 15, 0] = clean[0, 16, 1] = -1
+    got = forward(x2, to_dev(ids2), 1, None, score, err)
+    assert int(host(err)[0]) == U.ERR_LOGIT | U.ERR_ID_RANGE
+    ref = forward(masked, to_dev(clean), 1, None, score)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    err.zero_()
+    d = U.balance_loss_grad(dl, x2, to_dev(ids2), got[1], got[3], score=score, err=err)
+    assert int(host(err)[0]) == U.ERR_LOGIT | U.ERR_ID_RANGE
+    e = U.balance_loss_grad(dl, masked, to_dev(clean), got[1], got[3], score=score)
+    assert torch.equal(d, e)
+
+
+def test_no_tokens():
+    x = torch.empty(2, 0, 16, device=DEV)
+    ids = torch.empty(2, 0, 2, dtype=torch.int32, device=DEV)
+    outs = [torch.full(s, 7, dtype=t, device=DEV) for s, t in
+            (((2,), torch.float32), ((2, 16), torch.int32), ((2, 16), torch.float32),
+             ((2,), torch.int32))]
+    U.balance_loss(x, ids, 2, loss=outs[0], counts=outs[1], prob=outs[2], tokens=outs[3])
+    assert all(int(torch.count_nonzero(o)) == 0 for o in outs)
+    off = torch.zeros(3, dtype=torch.int32, device=DEV)
+    outs = U.balance_loss(x, ids, 2, seq_offset=off)
+    assert all(int(torch.count_nonzero(o)) == 0 for o in outs)
+    # tokens, but none present; the gradient is zero everywhere
+    x = torch.randn(2, 50, 16, device=DEV)
+    ids = torch.full((2, 50, 2), -1, dtype=torch.int32, device=DEV)
+    outs = U.balance_loss(x, ids, 2)
+    assert all(int(torch.count_nonzero(o)) == 0 for o in outs)
+    d = U.balance_loss_grad(torch.ones(2, device=DEV), x, ids, outs[1], outs[3])
+    assert int(torch.count_nonzero(d)) == 0
+
+
+@pytest.mark.parametrize("off", [[0, 50, 20, 100], [-5, 10, 20, 100], [0, 10, 20, 300],
+                                 [90, 60, 30, 0], [2 ** 31 - 1] * 4, [-2 ** 31] * 4])
+def test_bad_offsets_are_flagged(off):
+    """Tables that fall or leave the tokens: flagged by both calls, which read and write nothing
+    outside of their arrays."""
+    say("case: bad offsets", off)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(1, 100, 32, generator=g, device=DEV)
+    ids = torch.randint(0, 32, (1, 100, 2), generator=g, device=DEV, dtype=torch.int32)
+    off_d, err = torch.tensor(off, dtype=torch.int32, device=DEV), err_word()
+    _, counts, _, tokens = U.balance_loss(x, ids, 3, seq_offset=off_d, err=err)
+    assert int(host(err)[0]) & U.ERR_OFFSET
+    err.zero_()
+    guard = torch.full((3, 100, 32), 5.0, device=DEV)
+    U.balance_loss_grad(torch.ones(3, device=DEV), x, ids, counts, tokens, seq_offset=off_d,
+                        dlogits=guard[1:2], err=err)
+    assert int(host(err)[0]) & U.ERR_OFFSET
+    assert (host(guard[0]) == 5).all() and (host(guard[2]) == 5).all()
+
+
+def test_a_sure_expert_keeps_its_gradient():
+    """Where one expert takes nearly all of p the gradient of its logit is a small difference: it
+    keeps its digits, against 64 bits."""
+    x = torch.zeros(1, 64, 16, device=DEV)
+    x[..., 0] = 18.0
+    ids = torch.tensor([0, 1], dtype=torch.int32, device=DEV).expand(1, 64, 2).contiguous()
+    _, counts, _, tokens = U.balance_loss(x, ids)
+    d = U.balance_loss_grad(torch.ones(1, device=DEV), x, ids, counts, tokens)
+    ref = O.balance_loss_grad([1.0], host(x), host(ids), host(counts), host(tokens))
+    assert (np.abs(host(d) - ref) <= 400 * EPS * np.abs(ref)).all() and (ref[..., 0] != 0).all()
+
+
+def test_unaligned_rows_and_streams():
+    """Tensors that start anywhere, on a stream of their own, without a caller's workspace."""
+    flat = torch.randn(1 + 300 * 40, device=DEV)
+    x = flat[1:].view(1, 300, 40)
+    ids = torch.randint(0, 40, (1, 300, 4), device=DEV, dtype=torch.int32)
+    want = U.balance_loss(x.clone(), ids, 3)
+    dl = torch.ones(3, device=DEV)
+    d0 = U.balance_loss_grad(dl, x.clone(), ids, want[1], want[3])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = U.balance_loss(x, ids, 3, stream=s)
+    store = torch.empty(1 + 300 * 40, device=DEV)
+    s.wait_stream(torch.cuda.current_stream())
+    d1 = U.balance_loss_grad(dl, x, ids, got[1], got[3], dlogits=store[1:].view(1, 300, 40),
+                             stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(d0, d1)
+
+
+def test_captured_and_replayed():
+    """Both calls in a graph, replayed on new logits between eager work; a second captured graph
+    shares the workspace and runs after the first."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(2, 2000, 64, generator=g, device=DEV)
+    ids = torch.topk(x, 4, dim=-1).indices.to(torch.int32)
+    off = torch.tensor([0, 100, 2500, 4000], dtype=torch.int32, device=DEV)
+    dl = torch.rand(3, generator=g, device=DEV)
+    ws = torch.empty(U.balance_loss_workspace_size(2, 2000, 64, 3), dtype=torch.uint8, device=DEV)
+    outs = list(U.balance_loss(x, ids, 3, seq_offset=off, ws=ws))
+    d = U.balance_loss_grad(dl, x, ids, outs[1], outs[3], seq_offset=off)
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            U.balance_loss(x, ids, 3, seq_offset=off, ws=ws, loss=outs[0], counts=outs[1],
+                           prob=outs[2], tokens=outs[3])
+            U.balance_loss_grad(dl, x, ids, outs[1], outs[3], seq_offset=off, dlogits=d)
+        graphs.append(graph)
+    for i in range(4):
+        x.copy_(torch.randn(2, 2000, 64, generator=g, device=DEV))
+        ids.copy_(torch.topk(x, 4, dim=-1).indices.to(torch.int32))
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        want = U.balance_loss(x, ids, 3, seq_offset=off)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert torch.equal(d, U.balance_loss_grad(dl, x, ids, want[1], want[3], seq_offset=off))
+
+
+def test_binding_refusals():
+    x, ids = torch.randn(1, 6, 8, device=DEV), torch.zeros(1, 6, 2, dtype=torch.int32, device=DEV)
+    loss, counts, prob, tokens = U.balance_loss(x, ids, 2)
+    dl = torch.ones(2, device=DEV)
+    for call in (
+            lambda: U.balance_loss(x.half(), ids),
+            lambda: U.balance_loss(x, ids.long()),
+            lambda: U.balance_loss(x, ids[:, :5].contiguous()),
+            lambda: U.balance_loss(x[0], ids),
+            lambda: U.balance_loss(x, ids, 2, seq_offset=torch.zeros(2, dtype=torch.int32, device=DEV)),
+            lambda: U.balance_loss(x, ids, 2, loss=torch.empty(1, device=DEV)),
+            lambda: U.balance_loss(x, ids, 2, counts=torch.empty(2, 8, device=DEV)),
+            lambda: U.balance_loss(x.cpu(), ids),
+            lambda: U.balance_loss(x.expand(2, 6, 8), ids.repeat(2, 1, 1)),
+            lambda: U.balance_loss_grad(dl.double(), x, ids, counts, tokens),
+            lambda: U.balance_loss_grad(dl, x, ids, counts[:1], tokens),
+            lambda: U.balance_loss_grad(dl, x, ids, counts, tokens, add=x.to(torch.bfloat16)),
+            lambda: U.balance_loss_grad(dl, x, ids, counts, tokens, dlogits=x[:, :3])):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: U.balance_loss(x, ids, 4),
+                 lambda: U.balance_loss(x, ids, 2, ws=torch.empty(16, dtype=torch.uint8, device=DEV)),
+                 lambda: U.balance_loss_grad(dl, x, ids, counts, tokens, dlogits=x)):
+        with pytest.raises(U.UEPError):
+            call()
