@@ -110,12 +110,13 @@ __device__ __forceinline__ float pr_swiglu(float gate, float up) {
 // 64 kU, and add their sums in LDS.
 constexpr int kPrWaves = 4;
 template <int kRB, int kCB, int kU, bool kGlu>
-__global__ __launch_bounds__(kPrWaves* kWave) void pr_stream_kernel(PrArgs a, int n_tiles) {
+__global__ __launch_bounds__(kPrWaves* kWave) void pr_stream_kernel(PrArgs a, int t0,
+                                                                   int n_tiles) {
   constexpr int kOut = kGlu ? kCB / 2 : kCB;     // blocks of 16 outputs
   __shared__ i32x4 sums[kPrWaves][kRB * kCB][kWave];
   if (blockIdx.x == 0) pr_check_offsets(a);
   const int64_t id = xcd_block(blockIdx.x, gridDim.x);
-  const PrTile tile = pr_tile<16 * kRB>(a, (int)(id % n_tiles));
+  const PrTile tile = pr_tile<16 * kRB>(a, t0 + (int)(id % n_tiles));
   if (tile.n_rows <= 0) return;
   const int c0 = (int)(id / n_tiles) * 16 * kOut;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -189,20 +190,230 @@ __global__ __launch_bounds__(kPrWaves* kWave) void pr_stream_kernel(PrArgs a, in
   }
 }
 
+// ---------------------------------------------------------------------------------------
+// Many rows: tiles of 256 channels (SwiGLU: 128 gates and their ups) and 256 rows by eight
+// waves, two beside each other on every SIMD, each 128 channels and 64 rows (128 registers of
+// sums).  The depth goes by steps of 128 through two pairs of LDS buffers that the memory fills by
+// itself (buffer loads into LDS); a step's loads have a whole step's time.  Half steps of 64 are
+// read from LDS into registers one half ahead of the matrix instructions, so that one barrier a
+// step is enough: behind it every wave has the step in registers, its buffers are free for the
+// step after next, and the next step has landed.
+//
+// LDS rows are 128 bytes in eight slots of 16; slot s of row r holds bytes 16 (s ^ r % 8), so that the
+// 16 rows that a wave reads together spread over all banks.
+constexpr int kPtSide = 256, kPtDepth = 128, kPtThreads = 512;
+constexpr int kPtBuf = kPtSide * kPtDepth;          // one buffer of one operand
+
+__device__ __forceinline__ i32x4 pt_span(const int8_t* p, int64_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)u),
+               __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32) & 0xFFFF),
+               __builtin_amdgcn_readfirstlane((int)bytes), kRsrcWord3};
+}
+
+// 64 lanes' 16 bytes from span offset `off` + `more` into the 1 KiB of LDS from `lds` on.  Written
+// by hand because the compiler has every later read of LDS wait for all of them.
+__device__ __forceinline__ void pt_fetch(i32x4 span, uint32_t lds, int off, int more) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(off), "s"(span), "s"(more)
+      : "memory", "m0");
+}
+
+template <bool kGlu>
+__global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int t0, int n_tiles,
+                                                                int cols) {
+  constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;   // outputs of a tile
+  __shared__ __attribute__((aligned(1024))) char lds[4 * kPtBuf];
+  if (blockIdx.x == 0) pr_check_offsets(a);
+  // eight row tiles by all columns at a time: what an XCD's 32 workgroups share stays in its L2
+  const int id = (int)xcd_block(blockIdx.x, gridDim.x);
+  const int band = id / (8 * cols), in_band = id % (8 * cols);
+  const int high = min(8, n_tiles - band * 8);
+  const PrTile tile = pr_tile<kPtSide>(a, t0 + band * 8 + in_band % high);
+  if (tile.n_rows <= 0) return;
+  const int c0 = in_band / high * kWide;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  bool slot;
+  const int64_t at = pr_weight(a, tile.inst, slot);
+  const int64_t size = (int64_t)a.N * a.D;
+  const i32x4 ws = pt_span((slot ? a.slot_w : a.main_w) + at * size, size);
+  const i32x4 qs = pt_span(a.q + tile.row0 * a.D, (int64_t)tile.n_rows * a.D);
+  const uint32_t base = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
+
+  // a wave fills 32 rows of both operands' buffers, 8 by 8
+  const int fetch = (lane / 8) * a.D + ((lane ^ (lane / 8)) % 8) * 16;
+  int w_row[4], q_row[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = wave * 32 + i * 8, f = r % 128 / 16;
+    const int ch = kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
+    w_row[i] = (c0 + ch) * a.D;
+    q_row[i] = r * a.D;
+  }
+  auto fetch_piece = [&](int step, int i) {             // i: 0..3 weights, 4..7 rows
+    const uint32_t to = base + (step % 2) * kPtBuf + wave * 4096 + (i % 4) * 1024;
+    if (i < 4) pt_fetch(ws, to, fetch, w_row[i % 4] + step * kPtDepth);
+    else pt_fetch(qs, to + 2 * kPtBuf, fetch, q_row[i % 4] + step * kPtDepth);
+  };
+
+  const int w_wave = wave % 2 * 128, q_wave = wave / 2 * 64;
+  const int part = (lane / 16 ^ lane % 8) * 16;          // of the first half; the second ^ 64
+  const char* w_lds = lds + (w_wave + lane % 16) * kPtDepth;
+  const char* q_lds = lds + 2 * kPtBuf + (q_wave + lane % 16) * kPtDepth;
+  i32x4 acc[8][4] = {};
+  i32x4 w[2][8], x[2][4];
+  auto read_w = [&](int step, int h, int f) {
+    w[h][f] = *reinterpret_cast<const i32x4*>(w_lds + (part ^ h * 64) + step % 2 * kPtBuf +
+                                              f * 16 * kPtDepth);
+  };
+  auto read_x = [&](int step, int h, int f) {
+    x[h][f] = *reinterpret_cast<const i32x4*>(q_lds + (part ^ h * 64) + step % 2 * kPtBuf +
+                                              f * 16 * kPtDepth);
+  };
+  auto multiply = [&](int h, int f) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][f], x[h][j], acc[f][j], 0, 0, 0);
+  };
+
+  const int steps = (a.D + kPtDepth - 1) / kPtDepth;
+  for (int i = 0; i < 8; ++i) fetch_piece(0, i);
+  if (steps > 1) {
+    for (int i = 0; i < 8; ++i) fetch_piece(1, i);
+    asm volatile("s_waitcnt vmcnt(8)" ::: "memory");     // the first step's
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int f = 0; f < 8; ++f) {
+    if (f < 4) read_x(0, 0, f);
+    read_w(0, 0, f);
+  }
+  auto first_half = [&](int k) {
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      if (f < 4) read_x(k, 1, f);
+      read_w(k, 1, f);
+      multiply(0, f);
+      __builtin_amdgcn_sched_barrier(0);                 // keeps the reads between the products
+    }
+  };
+  auto second_half = [&](int k, bool more) {
+    // own reads of this step are in registers, own loads of the next have landed
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      if (more) fetch_piece(k + 2, f);
+      if (f < 4) read_x(k + 1, 0, f);
+      read_w(k + 1, 0, f);
+      multiply(1, f);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int k = 0;
+  for (; k < steps - 2; ++k) {
+    first_half(k);
+    second_half(k, true);
+  }
+  if (k < steps - 1) {
+    first_half(k);
+    second_half(k, false);
+    ++k;
+  }
+  // The last step: bytes past the end of the depth are another row's, and count as zeros.
+  const int rest = a.D - k * kPtDepth;
+  auto cut = [&](int h) {
+    const bool in = h * 64 + lane / 16 * 16 < rest;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[h][j][i] = in ? x[h][j][i] : 0;
+  };
+  cut(0);
+  first_half(k);
+  cut(1);
+#pragma unroll
+  for (int f = 0; f < 8; ++f) multiply(1, f);
+
+  const float* w_scale = (slot ? a.slot_scale : a.main_scale) + at * a.N;
+  float q_scale[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = q_wave + 16 * j + lane % 16;
+    q_scale[j] = row < tile.n_rows ? a.q_scale[tile.row0 + row] : 0.0f;
+  }
+  constexpr int kStep = kGlu ? 2 : 1;
+#pragma unroll
+  for (int f = 0; f < 8; f += kStep) {
+    const int ch = c0 + (kGlu ? wave % 2 * 64 + f / 2 * 16 : w_wave + f * 16) + lane / 16 * 4;
+    if (ch >= a.n_out) continue;
+    float s[4], s_up[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = w_scale[ch + i];
+      if constexpr (kGlu) s_up[i] = w_scale[a.n_out + ch + i];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = q_wave + 16 * j + lane % 16;
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = pr_scaled(acc[f][j][i], s[i], q_scale[j]);
+        if constexpr (kGlu) y[i] = pr_swiglu(y[i], pr_scaled(acc[f + 1][j][i], s_up[i], q_scale[j]));
+      }
+      const uint2 v = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+      if (row < tile.n_rows)
+        *reinterpret_cast<uint2*>(a.out + (tile.row0 + row) * a.n_out + ch) = v;
+    }
+  }
+}
+
+// Launches of fewer than 2^32 threads each, over ranges of tiles.
+template <typename F>
+static uep_status pr_launches(const PrArgs& a, int side, int cols, int threads, F launch) {
+  const int64_t tiles = std::min(a.rows, a.rows / side + a.n_inst);
+  const int64_t most = ((1ll << 32) - 1) / threads / cols;
+  for (int64_t t = 0; t < tiles; t += most) {
+    launch((int)t, (int)std::min(tiles - t, most));
+    UEP_CHECK_LAUNCH();
+  }
+  return UEP_OK;
+}
+
 template <int kRB, int kCB, int kU, bool kGlu>
 static uep_status pr_stream(const PrArgs& a, hipStream_t s) {
-  constexpr int kOut = kGlu ? kCB / 2 : kCB;
-  const int64_t tiles = std::min(a.rows, a.rows / (16 * kRB) + a.n_inst);
-  const int64_t cols = (a.n_out + 16 * kOut - 1) / (16 * kOut);
-  if (tiles * cols * kPrWaves * kWave >= (1ll << 32)) return UEP_EGEOM;
-  hipLaunchKernelGGL((pr_stream_kernel<kRB, kCB, kU, kGlu>), dim3((unsigned)(tiles * cols)),
-                     dim3(kPrWaves * kWave), 0, s, a, (int)tiles);
-  UEP_CHECK_LAUNCH();
-  return UEP_OK;
+  constexpr int kWide = 16 * (kGlu ? kCB / 2 : kCB);
+  const int cols = (a.n_out + kWide - 1) / kWide;
+  return pr_launches(a, 16 * kRB, cols, kPrWaves * kWave, [&](int t, int n) {
+    hipLaunchKernelGGL((pr_stream_kernel<kRB, kCB, kU, kGlu>), dim3((unsigned)n * cols),
+                       dim3(kPrWaves * kWave), 0, s, a, t, n);
+  });
+}
+
+template <bool kGlu>
+static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
+  constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;
+  const int cols = (a.n_out + kWide - 1) / kWide;
+  return pr_launches(a, kPtSide, cols, kPtThreads, [&](int t, int n) {
+    hipLaunchKernelGGL((pr_tile_kernel<kGlu>), dim3((unsigned)n * cols), dim3(kPtThreads), 0, s, a,
+                       t, n, cols);
+  });
 }
 
 template <bool kGlu>
 static uep_status pr_run(const PrArgs& a, hipStream_t s) {
+  if (a.rows >= 64ll * a.n_inst) return pr_tiles_of<kGlu>(a, s);
   return pr_stream<4, 4, 2, kGlu>(a, s);
 }
 
