@@ -41,46 +41,57 @@ __device__ __forceinline__ int pr_tiles(int begin, int end, int rows) {
   return n / rows + (n % rows != 0);
 }
 
-// The t-th tile of at most kRows rows of one instance, the instances in order and without the
-// empty ones.  Every lane of the wave calls it; lanes take consecutive instances each.
+// Tiles of at most kRows rows of one instance each, the instances in order and without the empty
+// ones.  Every lane of the wave takes consecutive instances and keeps the tiles up to its last.
+// All lanes of the wave make the calls; what is found is the same for all.
 template <int kRows>
-__device__ __forceinline__ PrTile pr_tile(const PrArgs& a, int t) {
-  if (!a.offset) {
-    const int64_t row0 = (int64_t)t * kRows;
-    return {0, row0, (int)max((int64_t)0, min((int64_t)kRows, a.rows - row0))};
+struct PrMap {
+  int upto;
+
+  static __device__ __forceinline__ int row(const PrArgs& a, int i) {
+    return min(max(a.offset[i], 0), (int)a.rows);
   }
-  const int lane = threadIdx.x % kWave, per = (a.n_inst + kWave - 1) / kWave;
-  const int i0 = min(lane * per, a.n_inst), i1 = min(i0 + per, a.n_inst), most = (int)a.rows;
-  int tiles = 0;
-  {
-    int begin = min(max(a.offset[i0], 0), most);
-    for (int i = i0; i < i1; ++i) {
-      const int end = min(max(a.offset[i + 1], 0), most);
-      tiles += pr_tiles(begin, end, kRows);
-      begin = end;
-    }
+  static __device__ __forceinline__ int per_lane(const PrArgs& a) {
+    return (a.n_inst + kWave - 1) / kWave;
   }
-  const int upto = wave_incl_scan(tiles);
-  const int owner = first_lane(upto > t);
-  if (owner < 0) return {0, 0, 0};
-  int left = t - (upto - tiles), inst = 0, row0 = 0, n = 0;
-  if (lane == owner) {
-    int begin = min(max(a.offset[i0], 0), most);
-    for (int i = i0; i < i1; ++i) {
-      const int end = min(max(a.offset[i + 1], 0), most);
-      const int here = pr_tiles(begin, end, kRows);
-      if (left < here) {
-        inst = i;
-        row0 = begin + left * kRows;
-        n = min(kRows, end - row0);
-        break;
+  __device__ __forceinline__ explicit PrMap(const PrArgs& a) {
+    const int lane = threadIdx.x % kWave;
+    int tiles = 0;
+    if (!a.offset) {
+      tiles = lane == 0 ? pr_tiles(0, (int)a.rows, kRows) : 0;
+    } else {
+      const int per = per_lane(a), first = min(lane * per, a.n_inst);
+      const int last = min(first + per, a.n_inst);
+      for (int i = first, at = row(a, first); i < last; ++i) {
+        const int to = row(a, i + 1);
+        tiles += pr_tiles(at, to, kRows);
+        at = to;
       }
-      left -= here;
-      begin = end;
     }
+    upto = wave_incl_scan(tiles);
   }
-  return {readlane(inst, owner), readlane(row0, owner), readlane(n, owner)};
-}
+  __device__ __forceinline__ int total() const { return readlane(upto, kWave - 1); }
+  // t >= 0 and the same in every lane
+  __device__ __forceinline__ PrTile find(const PrArgs& a, int t) const {
+    const int owner = first_lane(upto > t);
+    if (owner < 0) return {0, 0, 0};
+    int left = owner > 0 ? t - readlane(upto, owner - 1) : t;
+    int inst = 0, at = 0, to = (int)a.rows;
+    if (a.offset) {
+      inst = __builtin_amdgcn_readfirstlane(owner * per_lane(a));
+      at = row(a, inst);
+      to = row(a, inst + 1);
+      while (left >= pr_tiles(at, to, kRows)) {
+        left -= pr_tiles(at, to, kRows);
+        ++inst;
+        at = to;
+        to = row(a, inst + 1);
+      }
+    }
+    const int64_t row0 = at + (int64_t)left * kRows;
+    return {inst, row0, (int)min((int64_t)kRows, to - row0)};
+  }
+};
 
 __device__ __forceinline__ int64_t pr_weight(const PrArgs& a, int inst, bool& slot) {
   const int r = inst / a.inst_per_rank, j = inst % a.inst_per_rank;
@@ -116,7 +127,7 @@ __global__ __launch_bounds__(kPrWaves* kWave) void pr_stream_kernel(PrArgs a, in
   __shared__ i32x4 sums[kPrWaves][kRB * kCB][kWave];
   if (blockIdx.x == 0) pr_check_offsets(a);
   const int64_t id = xcd_block(blockIdx.x, gridDim.x);
-  const PrTile tile = pr_tile<16 * kRB>(a, t0 + (int)(id % n_tiles));
+  const PrTile tile = PrMap<16 * kRB>(a).find(a, t0 + (int)(id % n_tiles));
   if (tile.n_rows <= 0) return;
   const int c0 = (int)(id / n_tiles) * 16 * kOut;
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -197,22 +208,28 @@ __global__ __launch_bounds__(kPrWaves* kWave) void pr_stream_kernel(PrArgs a, in
 // itself (buffer loads into LDS); a step's loads have a whole step's time.  Half steps of 64 are
 // read from LDS into registers one half ahead of the matrix instructions, so that one barrier a
 // step is enough: behind it every wave has the step in registers, its buffers are free for the
-// step after next, and the next step has landed.
+// step after next, and the next step has landed.  A workgroup stays on its CU and takes tile after
+// tile: the next one's first two steps are under way while this one's results go out.
 //
-// LDS rows are 128 bytes in eight slots of 16; slot s of row r holds bytes 16 (s ^ r % 8), so that the
-// 16 rows that a wave reads together spread over all banks.
+// LDS: rows of 128 bytes in eight slots of 16; slot s of row r holds bytes 16 (s ^ r % 8), so that
+// the 16 rows that a wave reads together spread over all banks.  Beside the buffers each wave has
+// 4 KiB of its own: 2 to turn results into whole lines, and the scales of this tile and the next.
 constexpr int kPtSide = 256, kPtDepth = 128, kPtThreads = 512;
 constexpr int kPtBuf = kPtSide * kPtDepth;          // one buffer of one operand
+constexpr int kPtTurn = 4 * kPtBuf;                 // the waves' own parts
+constexpr int kPtScales = 2048, kPtScaleBytes = 768;
+constexpr int kPtBand = 8;
+constexpr int kPtMostOut = 1 << 21;                 // a tile's outputs are one span
 
-__device__ __forceinline__ i32x4 pt_span(const int8_t* p, int64_t bytes) {
+__device__ __forceinline__ i32x4 pt_span(const void* p, int64_t bytes) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
   return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)u),
                __builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32) & 0xFFFF),
                __builtin_amdgcn_readfirstlane((int)bytes), kRsrcWord3};
 }
 
-// 64 lanes' 16 bytes from span offset `off` + `more` into the 1 KiB of LDS from `lds` on.  Written
-// by hand because the compiler has every later read of LDS wait for all of them.
+// 64 lanes' 16 (4) bytes from span offset `off` + `more` into the 1 KiB (256 bytes) of LDS from
+// `lds` on.  Written by hand because the compiler has every later read of LDS wait for them.
 __device__ __forceinline__ void pt_fetch(i32x4 span, uint32_t lds, int off, int more) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -222,52 +239,83 @@ __device__ __forceinline__ void pt_fetch(i32x4 span, uint32_t lds, int off, int 
       : "s"(lds), "v"(off), "s"(span), "s"(more)
       : "memory", "m0");
 }
+__device__ __forceinline__ void pt_fetch4(i32x4 span, uint32_t lds, int off, int more) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(off), "s"(span), "s"(more)
+      : "memory", "m0");
+}
+
+// What a workgroup knows of a tile.
+struct PtTile {
+  i32x4 ws, qs;                        // spans of its weights and rows
+  const float* w_scale;
+  int64_t row0;
+  int n_rows, c0;
+};
 
 template <bool kGlu>
-__global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int t0, int n_tiles,
-                                                                int cols) {
-  constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;   // outputs of a tile
-  __shared__ __attribute__((aligned(1024))) char lds[4 * kPtBuf];
+__device__ __forceinline__ PtTile pt_tile(const PrArgs& a, const PrMap<kPtSide>& map, int id,
+                                          int cols) {
+  // bands of eight row tiles by all columns: what an XCD's workgroups share stays in its L2
+  const int band = id / (kPtBand * cols), in_band = id % (kPtBand * cols);
+  const int high = min(kPtBand, map.total() - band * kPtBand);
+  const PrTile t = map.find(a, band * kPtBand + in_band % high);
+  bool slot;
+  const int64_t at = pr_weight(a, t.inst, slot), size = (int64_t)a.N * a.D;
+  return {pt_span((slot ? a.slot_w : a.main_w) + at * size, size),
+          pt_span(a.q + t.row0 * a.D, (int64_t)t.n_rows * a.D),
+          (slot ? a.slot_scale : a.main_scale) + at * a.N,
+          t.row0,
+          t.n_rows,
+          in_band / high * (kGlu ? kPtSide / 2 : kPtSide)};
+}
+
+template <bool kGlu>
+__global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int cols) {
+  __shared__ __attribute__((aligned(1024))) char lds[kPtTurn + 8 * 4096];
   if (blockIdx.x == 0) pr_check_offsets(a);
-  // eight row tiles by all columns at a time: what an XCD's 32 workgroups share stays in its L2
-  const int id = (int)xcd_block(blockIdx.x, gridDim.x);
-  const int band = id / (8 * cols), in_band = id % (8 * cols);
-  const int high = min(8, n_tiles - band * 8);
-  const PrTile tile = pr_tile<kPtSide>(a, t0 + band * 8 + in_band % high);
-  if (tile.n_rows <= 0) return;
-  const int c0 = in_band / high * kWide;
+  const PrMap<kPtSide> map(a);
+  const int total = map.total() * cols;
+  // of every gridDim.x tiles an XCD takes consecutive ones
+  int id = (int)xcd_block(blockIdx.x, gridDim.x);
+  if (id >= total) return;
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  bool slot;
-  const int64_t at = pr_weight(a, tile.inst, slot);
-  const int64_t size = (int64_t)a.N * a.D;
-  const i32x4 ws = pt_span((slot ? a.slot_w : a.main_w) + at * size, size);
-  const i32x4 qs = pt_span(a.q + tile.row0 * a.D, (int64_t)tile.n_rows * a.D);
   const uint32_t base = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
 
   // a wave fills 32 rows of both operands' buffers, 8 by 8
   const int fetch = (lane / 8) * a.D + ((lane ^ (lane / 8)) % 8) * 16;
-  int w_row[4], q_row[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = wave * 32 + i * 8, f = r % 128 / 16;
-    const int ch = kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
-    w_row[i] = (c0 + ch) * a.D;
-    q_row[i] = r * a.D;
-  }
-  auto fetch_piece = [&](int step, int i) {             // i: 0..3 weights, 4..7 rows
+  auto fetch_piece = [&](const PtTile& t, int step, int i) {   // i: 0..3 weights, 4..7 rows
     const uint32_t to = base + (step % 2) * kPtBuf + wave * 4096 + (i % 4) * 1024;
-    if (i < 4) pt_fetch(ws, to, fetch, w_row[i % 4] + step * kPtDepth);
-    else pt_fetch(qs, to + 2 * kPtBuf, fetch, q_row[i % 4] + step * kPtDepth);
+    const int r = wave * 32 + i % 4 * 8, f = r % 128 / 16;
+    const int ch = kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
+    if (i < 4) pt_fetch(t.ws, to, fetch, (t.c0 + ch) * a.D + step * kPtDepth);
+    else pt_fetch(t.qs, to + 2 * kPtBuf, fetch, r * a.D + step * kPtDepth);
+  };
+  const int w_wave = wave % 2 * 128, q_wave = wave / 2 * 64;
+  const int steps = (a.D + kPtDepth - 1) / kPtDepth;
+  // scales of the wave's channels (SwiGLU: gates, then ups) and rows, then the first two steps
+  auto begin = [&](const PtTile& t, int odd) {
+    const uint32_t to = base + kPtTurn + wave * 4096 + kPtScales + odd * kPtScaleBytes;
+    const int ch = t.c0 + (kGlu ? wave % 2 * 64 : w_wave);
+    const i32x4 w_scale = pt_span(t.w_scale, a.N * 4ll);
+    pt_fetch4(w_scale, to, lane * 4, ch * 4);
+    pt_fetch4(w_scale, to + 256, lane * 4, (ch + (kGlu ? a.n_out : 64)) * 4);
+    pt_fetch4(pt_span(a.q_scale + t.row0, t.n_rows * 4ll), to + 512, lane * 4, q_wave * 4);
+    for (int i = 0; i < 8; ++i) fetch_piece(t, 0, i);
+    if (steps > 1)
+      for (int i = 0; i < 8; ++i) fetch_piece(t, 1, i);
   };
 
-  const int w_wave = wave % 2 * 128, q_wave = wave / 2 * 64;
   const int part = (lane / 16 ^ lane % 8) * 16;          // of the first half; the second ^ 64
   const char* w_lds = lds + (w_wave + lane % 16) * kPtDepth;
   const char* q_lds = lds + 2 * kPtBuf + (q_wave + lane % 16) * kPtDepth;
-  i32x4 acc[8][4] = {};
-  i32x4 w[2][8], x[2][4];
+  i32x4 acc[8][4], w[2][8], x[2][4];
   auto read_w = [&](int step, int h, int f) {
     w[h][f] = *reinterpret_cast<const i32x4*>(w_lds + (part ^ h * 64) + step % 2 * kPtBuf +
                                               f * 16 * kPtDepth);
@@ -281,22 +329,6 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int t0
     for (int j = 0; j < 4; ++j)
       acc[f][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][f], x[h][j], acc[f][j], 0, 0, 0);
   };
-
-  const int steps = (a.D + kPtDepth - 1) / kPtDepth;
-  for (int i = 0; i < 8; ++i) fetch_piece(0, i);
-  if (steps > 1) {
-    for (int i = 0; i < 8; ++i) fetch_piece(1, i);
-    asm volatile("s_waitcnt vmcnt(8)" ::: "memory");     // the first step's
-  } else {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  }
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-#pragma unroll
-  for (int f = 0; f < 8; ++f) {
-    if (f < 4) read_x(0, 0, f);
-    read_w(0, 0, f);
-  }
   auto first_half = [&](int k) {
 #pragma unroll
     for (int f = 0; f < 8; ++f) {
@@ -306,76 +338,118 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int t0
       __builtin_amdgcn_sched_barrier(0);                 // keeps the reads between the products
     }
   };
-  auto second_half = [&](int k, bool more) {
+  auto meet = [&]() {
     // own reads of this step are in registers, own loads of the next have landed
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+  };
+  auto second_half = [&](const PtTile& t, int k, bool more) {
+    meet();
 #pragma unroll
     for (int f = 0; f < 8; ++f) {
-      if (more) fetch_piece(k + 2, f);
+      if (more) fetch_piece(t, k + 2, f);
       if (f < 4) read_x(k + 1, 0, f);
       read_w(k + 1, 0, f);
       multiply(1, f);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int k = 0;
-  for (; k < steps - 2; ++k) {
-    first_half(k);
-    second_half(k, true);
-  }
-  if (k < steps - 1) {
-    first_half(k);
-    second_half(k, false);
-    ++k;
-  }
-  // The last step: bytes past the end of the depth are another row's, and count as zeros.
-  const int rest = a.D - k * kPtDepth;
-  auto cut = [&](int h) {
-    const bool in = h * 64 + lane / 16 * 16 < rest;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[h][j][i] = in ? x[h][j][i] : 0;
-  };
-  cut(0);
-  first_half(k);
-  cut(1);
-#pragma unroll
-  for (int f = 0; f < 8; ++f) multiply(1, f);
 
-  const float* w_scale = (slot ? a.slot_scale : a.main_scale) + at * a.N;
-  float q_scale[4];
+  PtTile t = pt_tile<kGlu>(a, map, id, cols);
+  begin(t, 0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  for (int odd = 0;; odd ^= 1) {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int row = q_wave + 16 * j + lane % 16;
-    q_scale[j] = row < tile.n_rows ? a.q_scale[tile.row0 + row] : 0.0f;
-  }
-  constexpr int kStep = kGlu ? 2 : 1;
+    for (int f = 0; f < 8; ++f)
 #pragma unroll
-  for (int f = 0; f < 8; f += kStep) {
-    const int ch = c0 + (kGlu ? wave % 2 * 64 + f / 2 * 16 : w_wave + f * 16) + lane / 16 * 4;
-    if (ch >= a.n_out) continue;
-    float s[4], s_up[4];
+      for (int j = 0; j < 4; ++j) acc[f][j] = i32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] = w_scale[ch + i];
-      if constexpr (kGlu) s_up[i] = w_scale[a.n_out + ch + i];
+    for (int f = 0; f < 8; ++f) {
+      if (f < 4) read_x(0, 0, f);
+      read_w(0, 0, f);
     }
+    int k = 0;
+    for (; k < steps - 2; ++k) {
+      first_half(k);
+      second_half(t, k, true);
+    }
+    if (k < steps - 1) {
+      first_half(k);
+      second_half(t, k, false);
+      ++k;
+    }
+    // The last step: bytes past the end of the depth are another row's, and count as zeros.
+    const int rest = a.D - k * kPtDepth;
+    auto cut = [&](int h) {
+      const bool in = h * 64 + lane / 16 * 16 < rest;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[h][j][i] = in ? x[h][j][i] : 0;
+    };
+    cut(0);
+    first_half(k);
+    cut(1);
+    const PtTile done = t;
+    id += gridDim.x;
+    const bool again = id < total;
+    if (again) {
+      t = pt_tile<kGlu>(a, map, id, cols);
+      meet();                                            // the buffers are free
+      begin(t, odd ^ 1);
+    }
+#pragma unroll
+    for (int f = 0; f < 8; ++f) multiply(1, f);
+
+    // Results: 16 rows by 64 channels at a time through the wave's own LDS into whole lines.
+    // Rows and channels outside go past the span's end, so that the number of stores is fixed.
+    int l = lane;                                        // what is made of it, is made here
+    asm volatile("" : "+v"(l));
+    char* own = lds + kPtTurn + wave * 4096;
+    const float* scales = reinterpret_cast<const float*>(own + kPtScales + odd * kPtScaleBytes);
+    const span_t os = span_of(a.out + done.row0 * a.n_out, (int64_t)done.n_rows * a.n_out * 2);
+    constexpr int kPasses = kGlu ? 1 : 2;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = q_wave + 16 * j + lane % 16;
-      float y[4];
+      const float q_scale = scales[128 + 16 * j + l % 16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[i] = pr_scaled(acc[f][j][i], s[i], q_scale[j]);
-        if constexpr (kGlu) y[i] = pr_swiglu(y[i], pr_scaled(acc[f + 1][j][i], s_up[i], q_scale[j]));
+      for (int p = 0; p < kPasses; ++p) {
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {                    // 16 outputs
+          const int f = kGlu ? 2 * o : 4 * p + o, at = (4 * p + o) * 16 + l / 16 * 4;
+          const f32x4 s = *reinterpret_cast<const f32x4*>(scales + at);
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = pr_scaled(acc[f][j][i], s[i], q_scale);
+          if constexpr (kGlu) {
+            const f32x4 s_up = *reinterpret_cast<const f32x4*>(scales + 64 + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              y[i] = pr_swiglu(y[i], pr_scaled(acc[f + 1][j][i], s_up[i], q_scale));
+          }
+          const int piece = (2 * o + l / 32) ^ l % 8;
+          *reinterpret_cast<uint2*>(own + l % 16 * 128 + piece * 16 + l / 16 % 2 * 8) =
+              uint2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 8 * h + l / 8, row = q_wave + 16 * j + r;
+          const int ch = done.c0 + (kGlu ? wave % 2 * 64 : w_wave + 64 * p) + l % 8 * 8;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * 128 + (l % 8 ^ r % 8) * 16);
+          const bool in = row < done.n_rows && ch < a.n_out;
+          __builtin_amdgcn_raw_buffer_store_b128(v, os, in ? (row * a.n_out + ch) * 2 : kPrFar, 0, 0);
+        }
+        __builtin_amdgcn_wave_barrier();
       }
-      const uint2 v = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-      if (row < tile.n_rows)
-        *reinterpret_cast<uint2*>(a.out + (tile.row0 + row) * a.n_out + ch) = v;
     }
+    if (!again) break;
+    // the loads before those stores, in order
+    if constexpr (kGlu) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
   }
 }
 
@@ -401,19 +475,25 @@ static uep_status pr_stream(const PrArgs& a, hipStream_t s) {
   });
 }
 
+// One workgroup for every CU; the tiles' number is known on the device only.
+constexpr int kPtGroups = 256;
 template <bool kGlu>
 static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;
   const int cols = (a.n_out + kWide - 1) / kWide;
-  return pr_launches(a, kPtSide, cols, kPtThreads, [&](int t, int n) {
-    hipLaunchKernelGGL((pr_tile_kernel<kGlu>), dim3((unsigned)n * cols), dim3(kPtThreads), 0, s, a,
-                       t, n, cols);
-  });
+  const int64_t tiles = std::min(a.rows, a.rows / kPtSide + a.n_inst) * cols;
+  hipLaunchKernelGGL((pr_tile_kernel<kGlu>), dim3((unsigned)std::min<int64_t>(tiles, kPtGroups)),
+                     dim3(kPtThreads), 0, s, a, cols);
+  UEP_CHECK_LAUNCH();
+  return UEP_OK;
 }
 
 template <bool kGlu>
 static uep_status pr_run(const PrArgs& a, hipStream_t s) {
-  if (a.rows >= 64ll * a.n_inst) return pr_tiles_of<kGlu>(a, s);
+  // ids of tiles and offsets in a tile's outputs are 32-bit
+  const int64_t ids = (a.rows / kPtSide + a.n_inst) * (a.n_out / (kPtSide / 2) + 1ll);
+  const bool fits = a.n_out <= kPtMostOut && ids < (1ll << 31) - kPtGroups;
+  if (fits && a.rows >= 64ll * a.n_inst) return pr_tiles_of<kGlu>(a, s);
   return pr_stream<4, 4, 2, kGlu>(a, s);
 }
 
