@@ -116,110 +116,11 @@ __device__ __forceinline__ float pr_swiglu(float gate, float up) {
 }
 
 // ---------------------------------------------------------------------------------------
-// Few rows: weights stream from HBM straight into operands.  A block takes 16 kRB rows and 16 kCB
-// channels (SwiGLU: half of them gates, half their ups); its waves share the depth, in pieces of
-// 64 kU, and add their sums in LDS.
-constexpr int kPrWaves = 4;
-template <int kRB, int kCB, int kU, bool kGlu>
-__global__ __launch_bounds__(kPrWaves* kWave) void pr_stream_kernel(PrArgs a, int t0,
-                                                                   int n_tiles) {
-  constexpr int kOut = kGlu ? kCB / 2 : kCB;     // blocks of 16 outputs
-  __shared__ i32x4 sums[kPrWaves][kRB * kCB][kWave];
-  if (blockIdx.x == 0) pr_check_offsets(a);
-  const int64_t id = xcd_block(blockIdx.x, gridDim.x);
-  const PrTile tile = PrMap<16 * kRB>(a).find(a, t0 + (int)(id % n_tiles));
-  if (tile.n_rows <= 0) return;
-  const int c0 = (int)(id / n_tiles) * 16 * kOut;
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  bool slot;
-  const int64_t at = pr_weight(a, tile.inst, slot);
-  const int64_t size = (int64_t)a.N * a.D;
-  const span_t ws = span_of((slot ? a.slot_w : a.main_w) + at * size, size);
-  const span_t qs = span_of(a.q + tile.row0 * a.D, (int64_t)tile.n_rows * a.D);
-
-  int w_row[kCB], q_row[kRB];
-#pragma unroll
-  for (int c = 0; c < kCB; ++c) {
-    const int ch = c0 + 16 * (c % kOut) + lane % 16;
-    w_row[c] = ch < a.n_out ? (ch + c / kOut * a.n_out) * a.D : kPrFar;
-  }
-#pragma unroll
-  for (int r = 0; r < kRB; ++r) q_row[r] = (16 * r + lane % 16) * a.D;
-  i32x4 acc[kRB][kCB] = {};
-  for (int k0 = wave * 64 * kU; k0 < a.D; k0 += kPrWaves * 64 * kU) {
-    i32x4 w[kU][kCB], x[kU][kRB];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int k = k0 + 64 * u + 16 * (lane / 16);
-      const bool in = k < a.D;
-#pragma unroll
-      for (int c = 0; c < kCB; ++c)
-        w[u][c] = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                       ws, in && w_row[c] >= 0 ? w_row[c] + k : kPrFar, 0, 0));
-#pragma unroll
-      for (int r = 0; r < kRB; ++r)
-        x[u][r] = __builtin_bit_cast(
-            i32x4, __builtin_amdgcn_raw_buffer_load_b128(qs, in ? q_row[r] + k : kPrFar, 0, 0));
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int r = 0; r < kRB; ++r)
-#pragma unroll
-        for (int c = 0; c < kCB; ++c)
-          acc[r][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][c], x[u][r], acc[r][c], 0, 0, 0);
-  }
-#pragma unroll
-  for (int r = 0; r < kRB; ++r)
-#pragma unroll
-    for (int c = 0; c < kCB; ++c) sums[wave][r * kCB + c][lane] = acc[r][c];
-  __syncthreads();
-
-  const float* w_scale = (slot ? a.slot_scale : a.main_scale) + at * a.N;
-  for (int o = threadIdx.x; o < kRB * kOut * kWave; o += kPrWaves * kWave) {
-    const int l = o % kWave, f = o / kWave, r = f / kOut, c = f % kOut;
-    const int row = 16 * r + l % 16, ch = c0 + 16 * c + 4 * (l / 16);
-    if (row >= tile.n_rows || ch >= a.n_out) continue;
-    i32x4 z = sums[0][r * kCB + c][l], up = {0, 0, 0, 0};
-    if constexpr (kGlu) up = sums[0][r * kCB + kOut + c][l];
-#pragma unroll
-    for (int w = 1; w < kPrWaves; ++w) {
-      z += sums[w][r * kCB + c][l];
-      if constexpr (kGlu) up += sums[w][r * kCB + kOut + c][l];
-    }
-    const float qs1 = a.q_scale[tile.row0 + row];
-    float y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[j] = pr_scaled(z[j], w_scale[ch + j], qs1);
-      if constexpr (kGlu)
-        y[j] = pr_swiglu(y[j], pr_scaled(up[j], w_scale[a.n_out + ch + j], qs1));
-    }
-    uint2 v = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
-    *reinterpret_cast<uint2*>(a.out + (tile.row0 + row) * a.n_out + ch) = v;
-  }
-}
-
-// ---------------------------------------------------------------------------------------
-// Many rows: tiles of 256 channels (SwiGLU: 128 gates and their ups) and 256 rows by eight
-// waves, two beside each other on every SIMD, each 128 channels and 64 rows (128 registers of
-// sums).  The depth goes by steps of 128 through two pairs of LDS buffers that the memory fills by
-// itself (buffer loads into LDS); a step's loads have a whole step's time.  Half steps of 64 are
-// read from LDS into registers one half ahead of the matrix instructions, so that one barrier a
-// step is enough: behind it every wave has the step in registers, its buffers are free for the
-// step after next, and the next step has landed.  A workgroup stays on its CU and takes tile after
-// tile: the next one's first two steps are under way while this one's results go out.
-//
-// LDS: rows of 128 bytes in eight slots of 16; slot s of row r holds bytes 16 (s ^ r % 8), so that
-// the 16 rows that a wave reads together spread over all banks.  Beside the buffers each wave has
-// 4 KiB of its own: 2 to turn results into whole lines, and the scales of this tile and the next.
-constexpr int kPtSide = 256, kPtDepth = 128, kPtThreads = 512;
-constexpr int kPtBuf = kPtSide * kPtDepth;          // one buffer of one operand
-constexpr int kPtTurn = 4 * kPtBuf;                 // the waves' own parts
-constexpr int kPtScales = 2048, kPtScaleBytes = 768;
-constexpr int kPtBand = 8;
-constexpr int kPtMostOut = 1 << 21;                 // a tile's outputs are one span
+// What the two kernels below share.  The depth goes by steps of 128, and the memory itself fills
+// the LDS with them (buffer loads into LDS).  A step's rows are 128 bytes in eight slots of 16;
+// slot s of row r holds bytes 16 (s ^ r % 8), so that the 16 rows that a wave reads together spread
+// over all banks.
+constexpr int kPtDepth = 128;
 
 __device__ __forceinline__ i32x4 pt_span(const void* p, int64_t bytes) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
@@ -248,6 +149,181 @@ __device__ __forceinline__ void pt_fetch4(i32x4 span, uint32_t lds, int off, int
       : "s"(lds), "v"(off), "s"(span), "s"(more)
       : "memory", "m0");
 }
+
+// Lane's part of 8 rows that one load brings, and of 16 rows that one read takes (first half of the
+// step; the second is at ^ 64).
+__device__ __forceinline__ int pt_fetch_lane(int lane, int D) {
+  return (lane / 8) * D + ((lane ^ (lane / 8)) % 8) * 16;
+}
+__device__ __forceinline__ int pt_read_lane(int lane) {
+  return lane % 16 * kPtDepth + (lane / 16 ^ lane % 8) * 16;
+}
+
+// ---------------------------------------------------------------------------------------
+// Few rows, or too few tiles of the large kernel to fill the chip: tiles of kCh channels (SwiGLU:
+// blocks of 16 gates and their ups in turn) and kRows rows.  kWC by kWR waves share a tile, and
+// kGroups such groups share the depth, a step each in turn, and add their sums at the end: a long
+// depth is the only axis that a small tile has left to split.  A ring of kStages times kGroups
+// steps in LDS is what HBM is asked ahead; one barrier for every kGroups steps, half steps read one
+// half ahead of the matrix instructions, as in the large kernel below.
+template <int kCh, int kRows, int kWC, int kWR, int kGroups, int kStages, bool kGlu>
+__global__ __launch_bounds__(kWC* kWR* kGroups* kWave) void pr_ring_kernel(PrArgs a, int t0,
+                                                                           int n_tiles) {
+  constexpr int kWide = kGlu ? kCh / 2 : kCh;
+  constexpr int kTeam = kWC * kWR;
+  constexpr int kLoads = (kCh + kRows) / 8 / kTeam;      // of a wave for one step
+  constexpr int kStage = (kCh + kRows) * kPtDepth;
+  constexpr int kCB = kCh / 16 / kWC, kRB = kRows / 16 / kWR;   // blocks of 16 of a wave
+  static_assert((kCh / 8) % kTeam == 0 && (kRows / 8) % kTeam == 0 && (!kGlu || kCB % 2 == 0), "");
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kGroups * kStage];
+  static_assert(sizeof(lds) >= (kGroups - 1) * kCh * kRows * 4, "sums of the groups");
+  if (blockIdx.x == 0) pr_check_offsets(a);
+  const int64_t id = xcd_block(blockIdx.x, gridDim.x);
+  const PrTile tile = PrMap<kRows>(a).find(a, t0 + (int)(id % n_tiles));
+  if (tile.n_rows <= 0) return;
+  const int c0 = (int)(id / n_tiles) * kWide;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kTeam;
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) / kTeam;
+  bool slot;
+  const int64_t at = pr_weight(a, tile.inst, slot), size = (int64_t)a.N * a.D;
+  const i32x4 ws = pt_span((slot ? a.slot_w : a.main_w) + at * size, size);
+  const i32x4 qs = pt_span(a.q + tile.row0 * a.D, (int64_t)tile.n_rows * a.D);
+  const uint32_t base = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
+  const int rounds = (a.D + kPtDepth * kGroups - 1) / (kPtDepth * kGroups);
+  const int fetch_lane = pt_fetch_lane(lane, a.D);
+  // loads past the depth go past the span's end: the same number is on the way at every step
+  auto fetch = [&](int round) {
+    const int step = round * kGroups + group;
+    const int off = step * kPtDepth < a.D ? fetch_lane : kPrFar;
+    const uint32_t to = base + (round % kStages * kGroups + group) * kStage;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int piece = wave + kTeam * i;
+      if (kTeam * i < kCh / 8) {
+        const int r = piece * 8, f = r / 16;
+        const int ch = kGlu ? f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
+        pt_fetch(ws, to + piece * 1024, off, (c0 + ch) * a.D + step * kPtDepth);
+      } else {
+        pt_fetch(qs, to + piece * 1024, off, (piece * 8 - kCh) * a.D + step * kPtDepth);
+      }
+    }
+  };
+  const int w_wave = wave % kWC * (kCh / kWC), q_wave = wave / kWC * (kRows / kWR);
+  const int read_lane = pt_read_lane(lane);
+  i32x4 acc[kCB][kRB] = {}, w[2][kCB], x[2][kRB];
+  auto read = [&](int round, int h) {
+    const char* stage = lds + (round % kStages * kGroups + group) * kStage;
+#pragma unroll
+    for (int r = 0; r < kRB; ++r)
+      x[h][r] = *reinterpret_cast<const i32x4*>(stage + (kCh + q_wave + 16 * r) * kPtDepth +
+                                                (read_lane ^ h * 64));
+#pragma unroll
+    for (int c = 0; c < kCB; ++c)
+      w[h][c] = *reinterpret_cast<const i32x4*>(stage + (w_wave + 16 * c) * kPtDepth +
+                                                (read_lane ^ h * 64));
+  };
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int c = 0; c < kCB; ++c)
+#pragma unroll
+      for (int r = 0; r < kRB; ++r)
+        acc[c][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][c], x[h][r], acc[c][r], 0, 0, 0);
+  };
+  // own reads of the last step are done and own loads of the next have landed; then everyone's
+  auto meet = [&]() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((kStages - 2) * kLoads) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) fetch(k);
+  meet();
+  fetch(kStages - 1);
+  read(0, 0);
+  int k = 0;
+  for (; k < rounds - 1; ++k) {
+    read(k, 1);
+    multiply(0);
+    __builtin_amdgcn_sched_barrier(0);                   // keeps the reads ahead of the products
+    meet();
+    fetch(k + kStages);
+    read(k + 1, 0);
+    multiply(1);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // The last round: bytes past the end of the depth are another row's, and count as zeros.
+  read(k, 1);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const bool in = (k * kGroups + group) * kPtDepth + h * 64 + lane / 16 * 16 < a.D;
+#pragma unroll
+    for (int r = 0; r < kRB; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[h][r][i] = in ? x[h][r][i] : 0;
+    multiply(h);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // no load into LDS outlives its stage
+  if constexpr (kGroups > 1) {
+    __syncthreads();
+    i32x4(*sums)[kTeam][kCB * kRB][kWave] =
+        reinterpret_cast<i32x4(*)[kTeam][kCB * kRB][kWave]>(lds);
+    if (group > 0) {
+#pragma unroll
+      for (int c = 0; c < kCB; ++c)
+#pragma unroll
+        for (int r = 0; r < kRB; ++r) sums[group - 1][wave][c * kRB + r][lane] = acc[c][r];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g)
+#pragma unroll
+      for (int c = 0; c < kCB; ++c)
+#pragma unroll
+        for (int r = 0; r < kRB; ++r) acc[c][r] += sums[g - 1][wave][c * kRB + r][lane];
+  }
+
+  const float* w_scale = (slot ? a.slot_scale : a.main_scale) + at * a.N;
+#pragma unroll
+  for (int r = 0; r < kRB; ++r) {
+    const int row = q_wave + 16 * r + lane % 16;
+    if (row >= tile.n_rows) continue;
+    const float q_scale = a.q_scale[tile.row0 + row];
+#pragma unroll
+    for (int c = 0; c < kCB; c += kGlu ? 2 : 1) {
+      const int ch = c0 + (w_wave + 16 * c) / (kGlu ? 2 : 1) + lane / 16 * 4;
+      if (ch >= a.n_out) continue;
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = pr_scaled(acc[c][r][i], w_scale[ch + i], q_scale);
+        if constexpr (kGlu)
+          y[i] = pr_swiglu(y[i], pr_scaled(acc[c + 1][r][i], w_scale[a.n_out + ch + i], q_scale));
+      }
+      *reinterpret_cast<uint2*>(a.out + (tile.row0 + row) * a.n_out + ch) =
+          uint2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Many rows: tiles of 256 channels (SwiGLU: 128 gates and their ups) and 256 rows by eight
+// waves, two beside each other on every SIMD, each 128 channels and 64 rows (128 registers of
+// sums).  Steps go through two pairs of LDS buffers; a step's loads have a whole step's time.  Half
+// steps of 64 are read from LDS into registers one half ahead of the matrix instructions, so that
+// one barrier a step is enough: behind it every wave has the step in registers, its buffers are
+// free for the step after next, and the next step has landed.  A workgroup stays on its CU and
+// takes tile after tile: the next one's first two steps are under way while this one's results go
+// out.  Beside the buffers each wave has 4 KiB of LDS of its own: 2 to turn results into whole
+// lines, and the scales of this tile and the next.
+constexpr int kPtSide = 256, kPtThreads = 512;
+constexpr int kPtBuf = kPtSide * kPtDepth;          // one buffer of one operand
+constexpr int kPtTurn = 4 * kPtBuf;                 // the waves' own parts
+constexpr int kPtScales = 2048, kPtScaleBytes = 768;
+constexpr int kPtBand = 8;
+constexpr int kPtMostOut = 1 << 21;                 // a tile's outputs are one span
 
 // What a workgroup knows of a tile.
 struct PtTile {
@@ -289,7 +365,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
 
   // a wave fills 32 rows of both operands' buffers, 8 by 8
-  const int fetch = (lane / 8) * a.D + ((lane ^ (lane / 8)) % 8) * 16;
+  const int fetch = pt_fetch_lane(lane, a.D);
   auto fetch_piece = [&](const PtTile& t, int step, int i) {   // i: 0..3 weights, 4..7 rows
     const uint32_t to = base + (step % 2) * kPtBuf + wave * 4096 + (i % 4) * 1024;
     const int r = wave * 32 + i % 4 * 8, f = r % 128 / 16;
@@ -312,9 +388,9 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
       for (int i = 0; i < 8; ++i) fetch_piece(t, 1, i);
   };
 
-  const int part = (lane / 16 ^ lane % 8) * 16;          // of the first half; the second ^ 64
-  const char* w_lds = lds + (w_wave + lane % 16) * kPtDepth;
-  const char* q_lds = lds + 2 * kPtBuf + (q_wave + lane % 16) * kPtDepth;
+  const int part = pt_read_lane(lane);
+  const char* w_lds = lds + w_wave * kPtDepth;
+  const char* q_lds = lds + 2 * kPtBuf + q_wave * kPtDepth;
   i32x4 acc[8][4], w[2][8], x[2][4];
   auto read_w = [&](int step, int h, int f) {
     w[h][f] = *reinterpret_cast<const i32x4*>(w_lds + (part ^ h * 64) + step % 2 * kPtBuf +
@@ -362,37 +438,47 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
   for (int odd = 0;; odd ^= 1) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
+    // a wave whose rows are past the tile's only fetches: its neighbour has the SIMD to itself
+    const bool busy = q_wave < t.n_rows;
+    if (busy) {
 #pragma unroll
-    for (int f = 0; f < 8; ++f)
+      for (int f = 0; f < 8; ++f)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[f][j] = i32x4{0, 0, 0, 0};
+        for (int j = 0; j < 4; ++j) acc[f][j] = i32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int f = 0; f < 8; ++f) {
-      if (f < 4) read_x(0, 0, f);
-      read_w(0, 0, f);
-    }
-    int k = 0;
-    for (; k < steps - 2; ++k) {
+      for (int f = 0; f < 8; ++f) {
+        if (f < 4) read_x(0, 0, f);
+        read_w(0, 0, f);
+      }
+      int k = 0;
+      for (; k < steps - 2; ++k) {
+        first_half(k);
+        second_half(t, k, true);
+      }
+      if (k < steps - 1) {
+        first_half(k);
+        second_half(t, k, false);
+        ++k;
+      }
+      // The last step: bytes past the end of the depth are another row's, and count as zeros.
+      const int rest = a.D - k * kPtDepth;
+      auto cut = [&](int h) {
+        const bool in = h * 64 + lane / 16 * 16 < rest;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[h][j][i] = in ? x[h][j][i] : 0;
+      };
+      cut(0);
       first_half(k);
-      second_half(t, k, true);
+      cut(1);
+    } else {
+      for (int k = 0; k < steps - 1; ++k) {
+        meet();
+        if (k + 2 < steps)
+          for (int i = 0; i < 8; ++i) fetch_piece(t, k + 2, i);
+      }
     }
-    if (k < steps - 1) {
-      first_half(k);
-      second_half(t, k, false);
-      ++k;
-    }
-    // The last step: bytes past the end of the depth are another row's, and count as zeros.
-    const int rest = a.D - k * kPtDepth;
-    auto cut = [&](int h) {
-      const bool in = h * 64 + lane / 16 * 16 < rest;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[h][j][i] = in ? x[h][j][i] : 0;
-    };
-    cut(0);
-    first_half(k);
-    cut(1);
     const PtTile done = t;
     id += gridDim.x;
     const bool again = id < total;
@@ -400,6 +486,11 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
       t = pt_tile<kGlu>(a, map, id, cols);
       meet();                                            // the buffers are free
       begin(t, odd ^ 1);
+    }
+    if (!busy) {
+      if (!again) break;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      continue;
     }
 #pragma unroll
     for (int f = 0; f < 8; ++f) multiply(1, f);
@@ -454,25 +545,19 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
 }
 
 // Launches of fewer than 2^32 threads each, over ranges of tiles.
-template <typename F>
-static uep_status pr_launches(const PrArgs& a, int side, int cols, int threads, F launch) {
-  const int64_t tiles = std::min(a.rows, a.rows / side + a.n_inst);
-  const int64_t most = ((1ll << 32) - 1) / threads / cols;
+template <int kCh, int kRows, int kWC, int kWR, int kGroups, int kStages, bool kGlu>
+static uep_status pr_ring(const PrArgs& a, hipStream_t s) {
+  constexpr int kWide = kGlu ? kCh / 2 : kCh, kThreads = kWC * kWR * kGroups * kWave;
+  const int cols = (a.n_out + kWide - 1) / kWide;
+  const int64_t tiles = std::min(a.rows, a.rows / kRows + a.n_inst);
+  const int64_t most = ((1ll << 32) - 1) / kThreads / cols;
   for (int64_t t = 0; t < tiles; t += most) {
-    launch((int)t, (int)std::min(tiles - t, most));
+    const int n = (int)std::min(tiles - t, most);
+    hipLaunchKernelGGL((pr_ring_kernel<kCh, kRows, kWC, kWR, kGroups, kStages, kGlu>),
+                       dim3((unsigned)n * cols), dim3(kThreads), 0, s, a, (int)t, n);
     UEP_CHECK_LAUNCH();
   }
   return UEP_OK;
-}
-
-template <int kRB, int kCB, int kU, bool kGlu>
-static uep_status pr_stream(const PrArgs& a, hipStream_t s) {
-  constexpr int kWide = 16 * (kGlu ? kCB / 2 : kCB);
-  const int cols = (a.n_out + kWide - 1) / kWide;
-  return pr_launches(a, 16 * kRB, cols, kPrWaves * kWave, [&](int t, int n) {
-    hipLaunchKernelGGL((pr_stream_kernel<kRB, kCB, kU, kGlu>), dim3((unsigned)n * cols),
-                       dim3(kPrWaves * kWave), 0, s, a, t, n);
-  });
 }
 
 // One workgroup for every CU; the tiles' number is known on the device only.
@@ -488,13 +573,40 @@ static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   return UEP_OK;
 }
 
+// The largest tile of which there are enough to fill 256 CUs, since a larger one reads less for each
+// product, but none far above an instance's mean rows, of which the rest would be wasted.  Chosen
+// against next, us (one instance, depth 7168, 4096 channels, unless noted):
+//   256 x 256 tiles        4096 rows x 8 of 32 instances, depth 4096: 100 / 175
+//   128 x 128, two a CU    2048 rows: 63 / 77 (one a CU with twice the steps) / 81 (256 x 256)
+//   128 x 128, one a CU    1024 rows: 39 / 57 (two) / 50 (128 x 64)
+//   128 x 64               2048 rows of 32 instances, depth 4096: 132 / 147 (64 x 32)
+//   64 x 128, depth in 2   512 rows: 28 / 36 (128 x 64) / 38 (64 x 64)
+//   64 x 64, depth in 2    256 rows: 21 / 28 (64 x 128) / 30 (64 x 32)
+//   64 x 32                8 rows of 8 instances, SwiGLU: 42 / 44 (depth in 2)
+//   64 x 32, depth in 2    128 rows: 17 / 20 (not split) / 21 (64 x 64)
+//   32 x 32                64 rows: 13 / 16 (64 x 32)
+//   32 x 32, depth in 2    1 row: 9.6 / 10.8 (not split) / 13 (64 x 32)
 template <bool kGlu>
 static uep_status pr_run(const PrArgs& a, hipStream_t s) {
-  // ids of tiles and offsets in a tile's outputs are 32-bit
+  // ids of tiles and offsets in a tile's outputs are 32-bit in the largest
   const int64_t ids = (a.rows / kPtSide + a.n_inst) * (a.n_out / (kPtSide / 2) + 1ll);
   const bool fits = a.n_out <= kPtMostOut && ids < (1ll << 31) - kPtGroups;
-  if (fits && a.rows >= 64ll * a.n_inst) return pr_tiles_of<kGlu>(a, s);
-  return pr_stream<4, 4, 2, kGlu>(a, s);
+  const int64_t used = std::min<int64_t>(a.n_inst, a.rows), mean = a.rows / used;
+  // about how many workgroups: half a tile is left over in every instance
+  auto groups = [&](int ch, int rows) {
+    const int wide = kGlu ? ch / 2 : ch;
+    return (a.n_out + wide - 1) / wide * std::max(used, (a.rows + rows - 1) / rows + used / 2);
+  };
+  if (fits && mean >= 128 && groups(256, 256) >= 200) return pr_tiles_of<kGlu>(a, s);
+  if (mean >= 96 && groups(128, 128) >= 280) return pr_ring<128, 128, 4, 2, 1, 2, kGlu>(a, s);
+  if (mean >= 96 && groups(128, 128) >= 200) return pr_ring<128, 128, 4, 2, 1, 4, kGlu>(a, s);
+  if (mean >= 32 && groups(128, 64) >= 512) return pr_ring<128, 64, 2, 2, 1, 3, kGlu>(a, s);
+  if (mean >= 96 && groups(64, 128) >= 200) return pr_ring<64, 128, 2, 2, 2, 3, kGlu>(a, s);
+  if (mean >= 48 && groups(64, 64) >= 200) return pr_ring<64, 64, 2, 2, 2, 4, kGlu>(a, s);
+  if (groups(64, 32) >= 400) return pr_ring<64, 32, 2, 2, 1, 4, kGlu>(a, s);
+  if (groups(64, 32) >= 200) return pr_ring<64, 32, 2, 2, 2, 5, kGlu>(a, s);
+  if (groups(32, 32) >= 200) return pr_ring<32, 32, 1, 2, 1, 8, kGlu>(a, s);
+  return pr_ring<32, 32, 1, 2, 2, 8, kGlu>(a, s);
 }
 
 }  // namespace uep
