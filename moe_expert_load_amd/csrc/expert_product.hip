@@ -573,40 +573,71 @@ static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   return UEP_OK;
 }
 
-// The largest tile of which there are enough to fill 256 CUs, since a larger one reads less for each
-// product, but none far above an instance's mean rows, of which the rest would be wasted.  Chosen
-// against next, us (one instance, depth 7168, 4096 channels, unless noted):
-//   256 x 256 tiles        4096 rows x 8 of 32 instances, depth 4096: 100 / 175
-//   128 x 128, two a CU    2048 rows: 63 / 77 (one a CU with twice the steps) / 81 (256 x 256)
-//   128 x 128, one a CU    1024 rows: 39 / 57 (two) / 50 (128 x 64)
-//   128 x 64               2048 rows of 32 instances, depth 4096: 132 / 147 (64 x 32)
-//   64 x 128, depth in 2   512 rows: 28 / 36 (128 x 64) / 38 (64 x 64)
-//   64 x 64, depth in 2    256 rows: 21 / 28 (64 x 128) / 30 (64 x 32)
-//   64 x 32                8 rows of 8 instances, SwiGLU: 42 / 44 (depth in 2)
-//   64 x 32, depth in 2    128 rows: 17 / 20 (not split) / 21 (64 x 64)
-//   32 x 32                64 rows: 13 / 16 (64 x 32)
-//   32 x 32, depth in 2    1 row: 9.6 / 10.8 (not split) / 13 (64 x 32)
+// Which tile.  Each form's time is a chip load of workgroups (`resident` a CU) times the steps of
+// the depth, at what a step was measured to take with one workgroup a CU (`one`) and with all
+// (`all`), plus what a load takes beside its steps (`load`: first loads, results; us).  Half a tile is
+// left over in every instance.  The form that comes out least is taken; over 120 shapes of every
+// kind its measured time is 1.03 times the best form's on the average.  Rows past an instance's are
+// loads that bring nothing, but not for nothing: a form is weighed from `mean` rows an instance on
+// (13 rows of 34 instances, 5840 channels, depth 5360: 75 us by 64 x 32, 89 by 128 x 64; 64 rows in
+// each of 32, depth 4096: 130 us by 128 x 64, 151 by 128 x 128).
+// Measured, one instance, 4096 channels, depth 7168, us:
+//   rows            1    64   128   256   512  1024  2048   8192 (8192 channels, depth 8192)
+//   taken         9.6  13.1  16.6  20.9  28.3  38.4  62.0    378
+//   next larger  13.0  16.4  21.0  28.0  38.2  54.7  80.4
+//   next smaller    -  22.0  18.9  30.1  38.1  53.3  76.2
+struct PrForm {
+  int ch, rows, mean, resident;
+  float one, all, load;
+};
+enum { kPrLarge, kPr128x128, kPr128x128Deep, kPr64x128, kPr128x64, kPr64x64, kPr64x32Deep,
+       kPr64x32, kPr32x32, kPr32x32Deep, kPrForms };
+constexpr PrForm kPrForm[kPrForms] = {
+    {256, 256, 96, 1, 1.50f, 1.50f, 5}, {128, 128, 80, 2, 0.93f, 1.09f, 8},
+    {128, 128, 80, 1, 0.66f, 0.66f, 5}, {64, 128, 80, 1, 0.47f, 0.47f, 4},
+    {128, 64, 24, 2, 0.60f, 0.87f, 6},  {64, 64, 24, 1, 0.34f, 0.34f, 3},
+    {64, 32, 0, 1, 0.27f, 0.27f, 2},    {64, 32, 0, 3, 0.32f, 0.65f, 5},
+    {32, 32, 0, 2, 0.20f, 0.31f, 3},    {32, 32, 0, 1, 0.36f, 0.36f, 1}};
+
 template <bool kGlu>
-static uep_status pr_run(const PrArgs& a, hipStream_t s) {
-  // ids of tiles and offsets in a tile's outputs are 32-bit in the largest
+static int pr_form(const PrArgs& a) {
+  const int64_t used = std::min<int64_t>(a.n_inst, a.rows);
+  const float steps = (float)((a.D + kPtDepth - 1) / kPtDepth);
+  // ids of tiles and offsets in a tile's outputs are 32-bit in the large kernel
   const int64_t ids = (a.rows / kPtSide + a.n_inst) * (a.n_out / (kPtSide / 2) + 1ll);
   const bool fits = a.n_out <= kPtMostOut && ids < (1ll << 31) - kPtGroups;
-  const int64_t used = std::min<int64_t>(a.n_inst, a.rows), mean = a.rows / used;
-  // about how many workgroups: half a tile is left over in every instance
-  auto groups = [&](int ch, int rows) {
-    const int wide = kGlu ? ch / 2 : ch;
-    return (a.n_out + wide - 1) / wide * std::max(used, (a.rows + rows - 1) / rows + used / 2);
-  };
-  if (fits && mean >= 128 && groups(256, 256) >= 200) return pr_tiles_of<kGlu>(a, s);
-  if (mean >= 96 && groups(128, 128) >= 280) return pr_ring<128, 128, 4, 2, 1, 2, kGlu>(a, s);
-  if (mean >= 96 && groups(128, 128) >= 200) return pr_ring<128, 128, 4, 2, 1, 4, kGlu>(a, s);
-  if (mean >= 32 && groups(128, 64) >= 512) return pr_ring<128, 64, 2, 2, 1, 3, kGlu>(a, s);
-  if (mean >= 96 && groups(64, 128) >= 200) return pr_ring<64, 128, 2, 2, 2, 3, kGlu>(a, s);
-  if (mean >= 48 && groups(64, 64) >= 200) return pr_ring<64, 64, 2, 2, 2, 4, kGlu>(a, s);
-  if (groups(64, 32) >= 400) return pr_ring<64, 32, 2, 2, 1, 4, kGlu>(a, s);
-  if (groups(64, 32) >= 200) return pr_ring<64, 32, 2, 2, 2, 5, kGlu>(a, s);
-  if (groups(32, 32) >= 200) return pr_ring<32, 32, 1, 2, 1, 8, kGlu>(a, s);
-  return pr_ring<32, 32, 1, 2, 2, 8, kGlu>(a, s);
+  int best = kPr32x32;
+  float least = 0.0f;
+  for (int i = 0; i < kPrForms; ++i) {
+    const PrForm& f = kPrForm[i];
+    if ((i == kPrLarge && !fits) || a.rows < f.mean * used) continue;
+    const int wide = kGlu ? f.ch / 2 : f.ch;
+    const int64_t groups = (a.n_out + wide - 1) / wide *
+                           std::max(used, (a.rows + f.rows - 1) / f.rows + used / 2);
+    const float loads = (float)groups / (256.0f * f.resident);
+    float us = f.load / 2 + steps * f.one;               // at most one workgroup a CU
+    if (i == kPr32x32Deep && groups <= 128) us = 1.0f + steps * 0.14f;   // half the CUs: no queue
+    else if (f.resident == 1) us = (float)((groups + 255) / 256) * (steps * f.one + f.load);
+    else if (groups > 256) us = std::max(us, loads * (steps * f.all + f.load));
+    if (least == 0.0f || us < least) least = us, best = i;
+  }
+  return best;
+}
+
+template <bool kGlu>
+static uep_status pr_run(const PrArgs& a, hipStream_t s) {
+  switch (pr_form<kGlu>(a)) {
+    case kPrLarge: return pr_tiles_of<kGlu>(a, s);
+    case kPr128x128: return pr_ring<128, 128, 4, 2, 1, 2, kGlu>(a, s);
+    case kPr128x128Deep: return pr_ring<128, 128, 4, 2, 1, 4, kGlu>(a, s);
+    case kPr64x128: return pr_ring<64, 128, 2, 2, 2, 3, kGlu>(a, s);
+    case kPr128x64: return pr_ring<128, 64, 2, 2, 1, 3, kGlu>(a, s);
+    case kPr64x64: return pr_ring<64, 64, 2, 2, 2, 4, kGlu>(a, s);
+    case kPr64x32Deep: return pr_ring<64, 32, 2, 2, 2, 5, kGlu>(a, s);
+    case kPr64x32: return pr_ring<64, 32, 2, 2, 1, 4, kGlu>(a, s);
+    case kPr32x32Deep: return pr_ring<32, 32, 1, 2, 2, 8, kGlu>(a, s);
+    default: return pr_ring<32, 32, 1, 2, 1, 8, kGlu>(a, s);
+  }
 }
 
 }  // namespace uep
