@@ -1,11 +1,13 @@
 // Balance loss of the router and its gradient (uep.h: uep_balance_loss, uep_balance_loss_grad).
 //
-// Loss.  Every logit is read once: a token's kL lanes make its scores, and each lane adds the
-// scores of its own experts over the tokens that it sees, so the sums over tokens stay in
-// registers until a block ends.  A block takes one chunk of one sequence; the chunks' sums are
-// joined in a second launch in a fixed order (no float atomics: a call repeats its bits).
+// Loss.  A block takes one chunk of one sequence.  The chunk's ids, read in one piece, give its
+// counts and which tokens are present; then every logit is read once: a token's kL lanes make its
+// scores, and each lane adds those of its own experts over the tokens that it sees, so that sums
+// over tokens stay in registers until the block ends.  The chunks' sums are joined in a second
+// launch in a fixed order, without float atomics: a call repeats its bits.
 // Gradient.  One pass: the scores again from the logits, one dot product a token with the
-// sequence's counts, which a block keeps in registers.  Both are bound by HBM.
+// sequence's counts, which a lane keeps in registers.
+// Both are bound by HBM, with sigmoid scores by the exponentials and reciprocals beside it.
 #include <algorithm>
 #include <type_traits>
 
@@ -15,10 +17,13 @@
 
 namespace uep {
 
-constexpr int kBlThreads = 256;
-constexpr int kBlWaves = kBlThreads / kWave;
 constexpr int kBlMaxE = 4096;
-constexpr int kBlMaxSeq = 65535;      // a grid's second dimension
+constexpr int kBlMaxSeq = 65535;      // blocks of the second launch
+constexpr int kBlMaxChunk = 2048;     // tokens of a chunk
+
+constexpr int kBlThreads = 256;
+constexpr int kBlSliced = 128;        // chunks of a sequence from which its experts are sliced
+constexpr int kBlSliceWide = 4;
 
 // How the tokens fall into chunks of at most `size` tokens of one sequence each.  Equal
 // sequences have `per` chunks each.  Otherwise chunk numbers go by offset[g] / size + g, which
@@ -50,23 +55,33 @@ __device__ __forceinline__ void bl_check_edges(const BlChunks& c, int g, int32_t
   if (a < 0 || z < a || z > c.n_tok) set_err(err, UEP_ERR_OFFSET);
 }
 
-// Every lane of the wave calls it.  The last edge with number <= b is found 64 at a time.
+// Every thread of the block calls it.  Where each has an edge of its own at most, one load finds
+// the last edge with number <= b; otherwise every wave searches 64 at a time.
 __device__ __forceinline__ BlChunk bl_chunk(const BlChunks& c, int b) {
   if (!c.offset) {
     const int g = b / c.per, j = b % c.per, end = (g + 1) * c.len;
     const int begin = g * c.len + j * c.size;
     return {g, begin, min(begin + c.size, end), j};
   }
-  const int lane = threadIdx.x % kWave;
-  int lo = 0, hi = c.n_seq + (c.outer ? 2 : 0);
-  while (hi - lo > 1) {
-    const int step = (hi - lo + kWave - 1) / kWave, at = lo + lane * step;
-    const bool below = at < hi && (at == lo || bl_edge(c, at) / c.size + at <= b);
-    const int n = __popcll(ballot(below));
-    lo = min(lo + (n - 1) * step, hi - 1);
-    hi = min(lo + step, hi);
+  int lo = 0, hi = c.n_seq + (c.outer ? 2 : 0), begin, end;
+  if (hi < (int)blockDim.x) {
+    __shared__ int edge[2];
+    const int i = threadIdx.x, at = bl_edge(c, min(i, hi));
+    lo = max(__syncthreads_count(i < hi && (i == 0 || at / c.size + i <= b)) - 1, 0);
+    if (i == lo || i == lo + 1) edge[i - lo] = at;
+    __syncthreads();
+    begin = edge[0], end = edge[1];
+  } else {
+    const int lane = threadIdx.x % kWave;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + kWave - 1) / kWave, at = lo + lane * step;
+      const bool below = at < hi && (at == lo || bl_edge(c, at) / c.size + at <= b);
+      const int n = __popcll(ballot(below));
+      lo = min(lo + (n - 1) * step, hi - 1);
+      hi = min(lo + step, hi);
+    }
+    begin = bl_edge(c, lo), end = bl_edge(c, lo + 1);
   }
-  const int begin = bl_edge(c, lo), end = bl_edge(c, lo + 1);
   const int j = b - (begin / c.size + lo);
   BlChunk k;
   k.seq = c.outer ? lo - 1 : lo;
@@ -74,6 +89,29 @@ __device__ __forceinline__ BlChunk bl_chunk(const BlChunks& c, int b) {
   k.begin = j < 0 || end <= begin || j > (end - begin) / c.size ? end : begin + j * c.size;
   k.end = min(k.begin + c.size, end);
   return k;
+}
+
+// Calls f(token of the chunk, slot, id) for every id of the chunk in [0, E); true if one is
+// neither that nor -1.  k_magic = ceil(2^32 / K), exact for the at most 2^17 ids of a chunk.
+template <typename F>
+__device__ __forceinline__ bool bl_ids(const int32_t* ids, const BlChunk& c, int E, int K,
+                                       uint32_t k_magic, F f) {
+  const int n = (c.end - c.begin) * K, step = blockDim.x;
+  const int32_t* p = ids + (int64_t)c.begin * K;
+  bool bad = false;
+  for (int i0 = threadIdx.x; i0 < n; i0 += 4 * step) {
+    int e[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) e[u] = i0 + u * step < n ? p[i0 + u * step] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * step, t = K == 1 ? i : (int)__umulhi(i, k_magic);
+      const bool in = e[u] >= 0 && e[u] < E;
+      bad |= !in && e[u] != -1;
+      if (in) f(t, i - t * K, e[u]);
+    }
+  }
+  return bad;
 }
 
 // over the kL lanes of a token
@@ -166,174 +204,184 @@ struct BlRow {
 };
 
 // Scores of one token into s, and the factor that makes them sum to one (0 if none is left).
-// Only finite logits have a score; NaN and +infinity are reported in `bad`.  The sigmoid's
-// 1 - s = e^-l s goes into `rest` where the gradient asks for it.  Scores below 2^-126 are 0.
+// Only finite logits have a score; NaN and +infinity are reported in `bad`: a NaN makes the sum
+// one, and so does +infinity through the softmax's maximum; a sigmoid is asked for its maximum.
+// The sigmoid's 1 - s = e^-l s goes into `rest` where the gradient asks for it (anything finite
+// where s is 0).  Scores below 2^-126 are 0.
 template <bool kSig, bool kRest, int kL, typename Row>
 __device__ __forceinline__ float bl_scores(const Row& row, float (&s)[Row::kPer],
                                            float (&rest)[Row::kPer], bool& bad) {
   float x[Row::kPer];
-  bool odd = false;
 #pragma unroll
-  for (int i = 0; i < Row::kPer; ++i) {
-    x[i] = row.at(i);
-    odd |= __builtin_amdgcn_classf(x[i], 0x203);      // NaN, +infinity
-  }
+  for (int i = 0; i < Row::kPer; ++i) x[i] = row.at(i);
+  float top, total;
+  auto score = [&]() {
+    top = x[0];
+#pragma unroll
+    for (int i = 1; i < Row::kPer; ++i) top = fmaxf(top, x[i]);
+    total = 0.0f;
+    if constexpr (kSig) {
+#pragma unroll
+      for (int i = 0; i < Row::kPer; ++i) {
+        const float t = __builtin_amdgcn_exp2f(-1.44269504f * x[i]);
+        s[i] = __builtin_amdgcn_rcpf(1.0f + t);
+        if constexpr (kRest) rest[i] = fminf(t, 0x1p126f) * s[i];
+        total += s[i];
+      }
+    } else {
+      top = bl_lanes_max<kL>(top);
+      const float from = top > -__builtin_inff() ? top : 0.0f;      // every expert masked
+#pragma unroll
+      for (int i = 0; i < Row::kPer; ++i) {
+        s[i] = gt_exp(x[i] - from);
+        total += s[i];
+      }
+    }
+  };
+  score();
+  const bool odd = !gt_finite(total) || (kSig && top == __builtin_inff());
   if (ballot(odd)) {
     bad |= odd;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i)
       if (!gt_finite(x[i])) x[i] = -__builtin_inff();
-  }
-  float total = 0.0f;
-  if constexpr (kSig) {
-#pragma unroll
-    for (int i = 0; i < Row::kPer; ++i) {
-      const float t = __builtin_amdgcn_exp2f(-1.44269504f * x[i]);
-      s[i] = __builtin_amdgcn_rcpf(1.0f + t);
-      if constexpr (kRest) rest[i] = t < 0x1p100f ? t * s[i] : 1.0f;
-      total += s[i];
-    }
-  } else {
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < Row::kPer; ++i) top = fmaxf(top, x[i]);
-    top = bl_lanes_max<kL>(top);
-    top = gt_finite(top) ? top : 0.0f;                // every expert masked
-#pragma unroll
-    for (int i = 0; i < Row::kPer; ++i) {
-      s[i] = gt_exp(x[i] - top);
-      total += s[i];
-    }
+    score();
   }
   total = bl_lanes_sum<kL>(total);
   return total > 0.0f ? 1.0f / total : 0.0f;
 }
 
-// Partial sums of the chunks, and what joins them.
+// Partial sums of the chunks: rows of `pitch` (E rounded up to whole vectors).
 struct BlPartial {
-  float* prob;      // [chunks][E]
-  int32_t* count;   // [chunks][E]
+  float* prob;      // [chunks][pitch]
+  int32_t* count;   // [chunks][pitch]
   int32_t* tokens;  // [chunks]
   double* loss;     // [n_seq][slices]
-  int32_t* ticket;  // [n_seq]
 };
 
-__device__ __forceinline__ float bl_factor(double E, double K, double n) {
-  return n > 0.0 ? (float)(E / (K * n * n)) : 0.0f;
+// What a sequence's sums are worth: E / (K n) * sum_e counts_e sum_e / n.
+__device__ __forceinline__ float bl_loss(double dot, int E, int K, int n) {
+  return n > 0 ? (float)(dot * E / ((double)K * n * n)) : 0.0f;
+}
+
+__device__ __forceinline__ double bl_wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  return v;
 }
 
 // kWhole: every sequence is one chunk, and the block writes the call's outputs.
 template <typename T, bool kSig, int kL, int kNV, bool kVec, bool kWhole>
 __global__ __launch_bounds__(kBlThreads) void bl_sum_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ ids, BlChunks chunks, int E, int K,
-    BlPartial part, float* __restrict__ loss, int32_t* __restrict__ counts,
-    float* __restrict__ prob, int32_t* __restrict__ tokens, int32_t* err) {
+    uint32_t k_magic, int pitch, BlPartial part, float* __restrict__ loss,
+    int32_t* __restrict__ counts, float* __restrict__ prob, int32_t* __restrict__ tokens,
+    int32_t* err) {
   typedef BlRow<T, kL, kNV, kVec> Row;
-  constexpr int kGroups = kBlThreads / kL;
-  __shared__ float sum[kBlMaxE < kL * Row::kPer ? kBlMaxE : kL * Row::kPer];
-  __shared__ int32_t hist[kBlMaxE < kL * Row::kPer ? kBlMaxE : kL * Row::kPer];
-  __shared__ int32_t present;
-  __shared__ double loss_wave[kBlWaves];
+  constexpr int kWaves = kBlThreads / kWave, kCols = kL * Row::kPer;
+  __shared__ float sum[kWaves][kCols];
+  __shared__ int32_t hist[kCols], present;
+  __shared__ uint8_t live[kBlMaxChunk];
+  __shared__ double loss_wave[kWaves];
   const int b = blockIdx.x, lane = threadIdx.x % kL, group = threadIdx.x / kL;
+  const int groups = blockDim.x / kL, wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
   const BlChunk c = bl_chunk(chunks, b);
-  if constexpr (!kWhole)
-    if (b == 0)
-      for (int g = threadIdx.x; g < chunks.n_seq; g += kBlThreads) part.ticket[g] = 0;
-  if (!kWhole && c.begin >= c.end) return;
-  for (int e = threadIdx.x; e < E; e += kBlThreads) hist[e] = 0, sum[e] = 0.0f;
+  const int n_tok = c.end - c.begin;
+  if (!kWhole && n_tok <= 0) return;
+  // the first row is on its way while the ids are counted
+  constexpr bool kAhead = Row::kPer <= 16;
+  Row next;
+  const T* first = logits + (int64_t)c.begin * E;
+  auto fetch = [&](int t) {
+    next.load(first + (int64_t)(t < n_tok ? t : 0) * E, lane, t < n_tok ? E : 0);
+  };
+  if (kAhead) fetch(group);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
+  for (int t = threadIdx.x; t < n_tok; t += blockDim.x) live[t] = 0;
   if (threadIdx.x == 0) present = 0;
   __syncthreads();
+  const bool bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int, int e) {
+    live[t] = 1;
+    atomicAdd(&hist[e], 1);
+  });
+  __syncthreads();
+  int mine = 0;
+  for (int t = threadIdx.x; t < n_tok; t += blockDim.x) mine += live[t];
+  mine = wave_sum(mine);
+  if (threadIdx.x % kWave == 0) atomicAdd(&present, mine);
 
   float acc[Row::kPer] = {};
-  bool bad_logit = false, bad_id = false;
-  Row next;
-  next.load(logits + (int64_t)min(c.begin + group, chunks.n_tok - 1) * E, lane,
-            c.begin + group < c.end ? E : 0);
-  for (int t0 = c.begin; t0 < c.end; t0 += kGroups) {
-    const int t = t0 + group, t1 = t + kGroups;
+  bool bad_logit = false;
+  for (int t0 = 0; t0 < n_tok; t0 += groups) {
+    const int t = t0 + group;
+    if (!kAhead) fetch(t);
     const Row row = next;
-    next.load(logits + (int64_t)min(t1, chunks.n_tok - 1) * E, lane, t1 < c.end ? E : 0);
-    float on = 0.0f;
-    if (t < c.end)
-      for (int k = lane; k < K; k += kL) {
-        const int e = ids[(int64_t)t * K + k];
-        const bool in = e >= 0 && e < E;
-        bad_id |= !in && e != -1;
-        if (in) {
-          on = 1.0f;
-          atomicAdd(&hist[e], 1);
-        }
-      }
-    on = bl_lanes_max<kL>(on);
-    if (on > 0.0f && lane == 0) atomicAdd(&present, 1);
+    if (kAhead) fetch(t + groups);
     float s[Row::kPer], rest[Row::kPer];
-    bool bad = false;
-    const float share = on * bl_scores<kSig, false, kL>(row, s, rest, bad);
-    bad_logit |= bad && t < c.end;
+    const float share = bl_scores<kSig, false, kL>(row, s, rest, bad_logit);
+    const float on = t < n_tok && live[t] ? share : 0.0f;
 #pragma unroll
-    for (int i = 0; i < Row::kPer; ++i) acc[i] = fmaf(s[i], share, acc[i]);
+    for (int i = 0; i < Row::kPer; ++i) acc[i] = fmaf(s[i], on, acc[i]);
   }
   if (ballot(bad_logit) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_LOGIT);
   if (ballot(bad_id) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_ID_RANGE);
 
-  // the wave's tokens by butterflies, the waves one after the other
+  // a wave's tokens by butterflies, the waves in order
 #pragma unroll
   for (int o = kL; o < kWave; o *= 2)
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) acc[i] += __shfl_xor(acc[i], o, kWave);
-  for (int w = 0; w < kBlWaves; ++w) {
-    if (threadIdx.x / kWave == w && threadIdx.x % kWave < kL)
+  if (threadIdx.x % kWave < kL)
 #pragma unroll
-      for (int i = 0; i < Row::kPer; ++i) {
-        const int e = Row::expert(lane, i);
-        if (e < E) sum[e] += acc[i];
-      }
-    __syncthreads();
-  }
-  if constexpr (!kWhole) {
-    for (int e = threadIdx.x; e < E; e += kBlThreads) {
-      part.prob[(int64_t)b * E + e] = sum[e];
-      part.count[(int64_t)b * E + e] = hist[e];
-    }
-    if (threadIdx.x == 0) part.tokens[b] = present;
-    return;
-  }
+    for (int i = 0; i < Row::kPer; ++i) sum[wave][Row::expert(lane, i)] = acc[i];
+  __syncthreads();
   const int n = present;
   double dot = 0.0;
-  for (int e = threadIdx.x; e < E; e += kBlThreads) {
-    counts[(int64_t)c.seq * E + e] = hist[e];
-    prob[(int64_t)c.seq * E + e] = n > 0 ? sum[e] / (float)n : 0.0f;
-    dot += (double)hist[e] * (double)sum[e];
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float p = sum[0][e];
+    for (int w = 1; w < waves; ++w) p += sum[w][e];
+    if constexpr (kWhole) {
+      counts[(int64_t)c.seq * E + e] = hist[e];
+      prob[(int64_t)c.seq * E + e] = n > 0 ? p / (float)n : 0.0f;
+      dot += (double)hist[e] * (double)p;
+    } else {
+      part.prob[(int64_t)b * pitch + e] = p;
+      part.count[(int64_t)b * pitch + e] = hist[e];
+    }
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
-  if (threadIdx.x % kWave == 0) loss_wave[threadIdx.x / kWave] = dot;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kBlWaves; ++w) dot += loss_wave[w];
-    tokens[c.seq] = n;
-    loss[c.seq] = n > 0 ? (float)(dot * E / ((double)K * n * n)) : 0.0f;
+  if constexpr (kWhole) {
+    dot = bl_wave_sum(dot);
+    if (threadIdx.x % kWave == 0) loss_wave[wave] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < waves; ++w) dot += loss_wave[w];
+      tokens[c.seq] = n;
+      loss[c.seq] = bl_loss(dot, E, K, n);
+    }
+  } else {
+    if (threadIdx.x == 0) part.tokens[b] = n;
   }
 }
 
-// Joins the chunks of one sequence for kBlSlice experts in 64 bits: blockDim.x / kBlSlice
-// threads an expert share them out.  The last slice of a sequence adds its loss.
-constexpr int kBlSlice = 16;
-constexpr int kBlJoinThreads = 1024;
-constexpr int kBlJoinRows = kBlJoinThreads / kBlSlice;
-__global__ __launch_bounds__(kBlJoinThreads) void bl_join_kernel(
-    BlChunks chunks, int E, int K, BlPartial part, float* __restrict__ loss,
+// Joins the chunks of one sequence in 64 bits: `wide` threads have four experts each, the other
+// factor of the block shares the chunks out; rows of sums are added as a tree.  A sequence of many
+// chunks is joined by several blocks, for 4 `wide` experts each; their parts of the loss are added
+// by a launch of its own.
+constexpr int kBlJoin = 1024;
+__global__ __launch_bounds__(kBlJoin) void bl_join_kernel(
+    BlChunks chunks, int E, int K, int pitch, int wide, BlPartial part, float* __restrict__ loss,
     int32_t* __restrict__ counts, float* __restrict__ prob, int32_t* __restrict__ tokens,
     int32_t* err) {
-  __shared__ double p_lds[kBlJoinRows][kBlSlice];
-  __shared__ int32_t c_lds[kBlJoinRows][kBlSlice], n_lds[kBlJoinRows];
-  __shared__ bool last;
-  const int g = blockIdx.y, slices = gridDim.x, col = threadIdx.x % kBlSlice;
-  const int r = threadIdx.x / kBlSlice, e = blockIdx.x * kBlSlice + col;
-  const int rows = blockDim.x / kBlSlice;
-  int first, n_ch;
+  __shared__ double p_lds[4][kBlJoin];
+  __shared__ int32_t c_lds[4][kBlJoin];
+  __shared__ double loss_wave[kBlJoin / kWave];
+  __shared__ int32_t present;
+  const int g = blockIdx.x, col = threadIdx.x % wide, r = threadIdx.x / wide;
+  const int rows = blockDim.x / wide, slices = gridDim.y;
+  int64_t first;
+  int n_ch;
   if (!chunks.offset) {
-    first = g * chunks.per;
+    first = (int64_t)g * chunks.per;
     n_ch = chunks.per;
   } else {
     if (threadIdx.x == 0) bl_check_edges(chunks, g, err);
@@ -341,54 +389,71 @@ __global__ __launch_bounds__(kBlJoinThreads) void bl_join_kernel(
     first = lo / chunks.size + g;
     n_ch = hi > lo ? (hi - lo + chunks.size - 1) / chunks.size : 0;
   }
-  double p = 0.0;
-  int32_t cnt = 0, n = 0;
-#pragma unroll 4
-  for (int j = r; j < n_ch; j += rows) {
-    const int64_t at = first + j;
-    n += part.tokens[at];
-    if (e < E) {
-      p += part.prob[at * E + e];
-      cnt += part.count[at * E + e];
-    }
-  }
-  p_lds[r][col] = p;
-  c_lds[r][col] = cnt;
-  if (col == 0) n_lds[r] = n;
+  if (threadIdx.x == 0) present = 0;
   __syncthreads();
-  for (int h = rows / 2; h > 0; h /= 2) {
-    if (r < h) {
-      p_lds[r][col] += p_lds[r + h][col];
-      c_lds[r][col] += c_lds[r + h][col];
-      if (col == 0) n_lds[r] += n_lds[r + h];
+  int mine = 0;
+  for (int j = threadIdx.x; j < n_ch; j += blockDim.x) mine += part.tokens[first + j];
+  mine = wave_sum(mine);
+  if (threadIdx.x % kWave == 0 && mine) atomicAdd(&present, mine);
+  double dot = 0.0;
+  for (int q0 = blockIdx.y * wide; 4 * q0 < E; q0 += slices * wide) {
+    const int e0 = 4 * (q0 + col);
+    double p[4] = {};
+    int32_t k[4] = {};
+    if (e0 < E) {
+#pragma unroll 8
+      for (int j = r; j < n_ch; j += rows) {
+        const int64_t at = (first + j) * pitch + e0;
+        const f32x4 a = *reinterpret_cast<const f32x4*>(part.prob + at);
+        const u32x4 c = *reinterpret_cast<const u32x4*>(part.count + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] += a[i], k[i] += (int32_t)c[i];
+      }
+    }
+    __syncthreads();                              // the last round's reads
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p_lds[i][threadIdx.x] = p[i], c_lds[i][threadIdx.x] = k[i];
+    for (int h = rows / 2; h > 0; h /= 2) {
+      __syncthreads();
+      if (r < h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p_lds[i][threadIdx.x] += p_lds[i][threadIdx.x + h * wide];
+          c_lds[i][threadIdx.x] += c_lds[i][threadIdx.x + h * wide];
+        }
     }
     __syncthreads();
-  }
-  n = n_lds[0];
-  if (r == 0 && e < E) {
-    counts[(int64_t)g * E + e] = c_lds[0][col];
-    prob[(int64_t)g * E + e] = n > 0 ? (float)(p_lds[0][col] / n) : 0.0f;
-  }
-  if (threadIdx.x == 0) {
-    double dot = 0.0;
-    for (int i = 0; i < kBlSlice; ++i) dot += p_lds[0][i] * c_lds[0][i];
-    __hip_atomic_store(&part.loss[(int64_t)g * slices + blockIdx.x], dot, __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(&part.ticket[g], 1, __ATOMIC_ACQ_REL,
-                                  __HIP_MEMORY_SCOPE_AGENT) == slices - 1;
-  }
-  __syncthreads();
-  if (!last || threadIdx.x >= kWave) return;
-  double dot = 0.0;
-  for (int i = threadIdx.x; i < slices; i += kWave)
-    dot += __hip_atomic_load(&part.loss[(int64_t)g * slices + i], __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+    const int n = present;
+    if (r == 0)
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
-  if (threadIdx.x == 0) {
-    tokens[g] = n;
-    loss[g] = n > 0 ? (float)(dot * E / ((double)K * n * n)) : 0.0f;
+      for (int i = 0; i < 4; ++i)
+        if (e0 + i < E) {
+          const double s = p_lds[i][col];
+          const int32_t c = c_lds[i][col];
+          counts[(int64_t)g * E + e0 + i] = c;
+          prob[(int64_t)g * E + e0 + i] = n > 0 ? (float)(s / n) : 0.0f;
+          dot += s * c;
+        }
   }
+  dot = bl_wave_sum(dot);
+  if (threadIdx.x % kWave == 0) loss_wave[threadIdx.x / kWave] = dot;
+  __syncthreads();
+  if (threadIdx.x > 0) return;
+  for (int w = 1; w < (int)blockDim.x / kWave; ++w) dot += loss_wave[w];
+  if (blockIdx.y == 0) tokens[g] = present;
+  if (slices == 1) loss[g] = bl_loss(dot, E, K, present);
+  else part.loss[(int64_t)g * slices + blockIdx.y] = dot;
+}
+
+// A wave for each sequence adds its slices' parts, in an order that their number fixes.
+__global__ __launch_bounds__(kWave) void bl_loss_kernel(BlPartial part, int slices, int E, int K,
+                                                        const int32_t* __restrict__ tokens,
+                                                        float* __restrict__ loss) {
+  const int g = blockIdx.x;
+  double dot = 0.0;
+  for (int i = threadIdx.x; i < slices; i += kWave) dot += part.loss[(int64_t)g * slices + i];
+  dot = bl_wave_sum(dot);
+  if (threadIdx.x == 0) loss[g] = bl_loss(dot, E, K, tokens[g]);
 }
 
 // dl_e = f p_e ((c_e - c_0) - sum_j p_j (c_j - c_0)) [(1 - s_e)].  c_0 is the count of the
@@ -398,67 +463,78 @@ template <typename T, bool kSig, bool kAdd, int kL, int kNV, bool kVec>
 __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const float* __restrict__ dloss, const T* __restrict__ logits,
     const int32_t* __restrict__ ids, const int32_t* __restrict__ counts,
-    const int32_t* __restrict__ tokens, BlChunks chunks, int E, int K, const T* add, T* dlogits,
-    int32_t* err) {
+    const int32_t* __restrict__ tokens, BlChunks chunks, int E, int K, uint32_t k_magic,
+    const T* add, T* dlogits, int32_t* err) {
   typedef BlRow<T, kL, kNV, kVec> Row;
-  constexpr int kGroups = kBlThreads / kL;
-  __shared__ float c_lds[kBlMaxE < kL * Row::kPer ? kBlMaxE : kL * Row::kPer];
-  const int lane = threadIdx.x % kL, group = threadIdx.x / kL;
+  __shared__ float c_lds[kL * Row::kPer];
+  __shared__ int16_t head[kBlMaxChunk];           // a token's first id, -1 if that slot is empty
+  __shared__ uint8_t live[kBlMaxChunk];
+  const int lane = threadIdx.x % kL, group = threadIdx.x / kL, groups = blockDim.x / kL;
   if (chunks.offset && blockIdx.x == 0)
-    for (int g = threadIdx.x; g < chunks.n_seq; g += kBlThreads) bl_check_edges(chunks, g, err);
+    for (int g = threadIdx.x; g < chunks.n_seq; g += blockDim.x) bl_check_edges(chunks, g, err);
   const BlChunk c = bl_chunk(chunks, blockIdx.x);
-  if (c.begin >= c.end) return;
+  const int n_tok = c.end - c.begin;
+  if (n_tok <= 0) return;
   const bool inside = c.seq >= 0 && c.seq < chunks.n_seq;
+  const int e_read = inside ? E : 0;
+  const int64_t first = (int64_t)c.begin * E;
+  Row next, next_base;
+  auto fetch = [&](int t) {
+    const int64_t at = first + (int64_t)(t < n_tok ? t : 0) * E;
+    next.load(logits + at, lane, t < n_tok ? e_read : 0);
+    if constexpr (kAdd) next_base.load(add + at, lane, t < n_tok ? E : 0);
+  };
+  constexpr bool kAhead = Row::kPer <= 16;
+  if (kAhead) fetch(group);
+  for (int t = threadIdx.x; t < n_tok; t += blockDim.x) live[t] = 0, head[t] = -1;
+  if (inside)
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+      c_lds[e] = (float)counts[(int64_t)c.seq * E + e];
+  __syncthreads();
+  bool bad_id = false;
   float f = 0.0f;
   if (inside) {
-    f = dloss[c.seq] * bl_factor(E, K, tokens[c.seq]);
-    for (int e = threadIdx.x; e < E; e += kBlThreads)
-      c_lds[e] = (float)counts[(int64_t)c.seq * E + e];
-    __syncthreads();
+    const double n = tokens[c.seq];
+    f = n > 0.0 ? dloss[c.seq] * (float)(E / (K * n * n)) : 0.0f;
+    bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int slot, int e) {
+      live[t] = 1;
+      if (slot == 0) head[t] = (int16_t)e;
+    });
   }
+  __syncthreads();
   float cnt[Row::kPer];
 #pragma unroll
   for (int i = 0; i < Row::kPer; ++i) {
     const int e = Row::expert(lane, i);
     cnt[i] = inside && e < E ? c_lds[e] : 0.0f;
   }
-  bool bad_logit = false, bad_id = false;
-  for (int t0 = c.begin; t0 < c.end; t0 += kGroups) {
+  bool bad_logit = false;
+  for (int t0 = 0; t0 < n_tok; t0 += groups) {
     const int t = t0 + group;
-    const bool live = t < c.end;
-    const int64_t at = (int64_t)(live ? t : c.begin) * E;
-    Row row, base;
-    row.load(logits + at, lane, live && inside ? E : 0);
-    if constexpr (kAdd) base.load(add + at, lane, live ? E : 0);
-    float on = 0.0f, c0 = 0.0f;
-    if (live && inside) {
-      for (int k = lane; k < K; k += kL) {
-        const int e = ids[(int64_t)t * K + k];
-        const bool in = e >= 0 && e < E;
-        bad_id |= !in && e != -1;
-        if (in) on = 1.0f;
-      }
-      const int first = ids[(int64_t)t * K];
-      if (first >= 0 && first < E) c0 = c_lds[first];
-    }
-    on = bl_lanes_max<kL>(on);
+    if (!kAhead) fetch(t);
+    const Row row = next, base = next_base;
+    if (kAhead) fetch(t + groups);
+    const int h0 = t < n_tok ? head[t] : -1;
+    const bool on = t < n_tok && live[t];
+    const float c0 = h0 >= 0 ? c_lds[h0] : 0.0f;
     float s[Row::kPer], rest[Row::kPer], out[Row::kPer];
-    bool bad = false;
-    const float share = bl_scores<kSig, kSig, kL>(row, s, rest, bad);
-    bad_logit |= bad;
+    const float share = bl_scores<kSig, kSig, kL>(row, s, rest, bad_logit);
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < Row::kPer; ++i) dot = fmaf(s[i], cnt[i] - c0, dot);
+    for (int i = 0; i < Row::kPer; ++i) {
+      out[i] = cnt[i] - c0;
+      dot = fmaf(s[i], out[i], dot);
+    }
     dot = bl_lanes_sum<kL>(dot) * share;
-    const float h = on > 0.0f && share > 0.0f ? f * share : 0.0f;
+    const float h = on && share > 0.0f ? f * share : 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {
-      float d = h * s[i] * ((cnt[i] - c0) - dot);
+      float d = h * s[i] * (out[i] - dot);
       if constexpr (kSig) d *= rest[i];
       if constexpr (kAdd) d += base.at(i);
       out[i] = d;
     }
-    if (live) Row::store(dlogits + at, lane, E, out);
+    if (t < n_tok) Row::store(dlogits + first + (int64_t)t * E, lane, E, out);
   }
   if (ballot(bad_logit) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_LOGIT);
   if (ballot(bad_id) && threadIdx.x % kWave == 0) set_err(err, UEP_ERR_ID_RANGE);
@@ -481,20 +557,22 @@ struct BlCall {
   hipStream_t stream;
 };
 
-// Lanes of a token: as few as hold the experts in kNV = 4 vectors each.
+// Lanes of a token: as few as hold the experts with 16 each (above 1024 experts 64 each).  With 32
+// a lane the sigmoid's gradient takes 226 registers and two waves a SIMD (262144 tokens of 256
+// bf16 logits, added to others: 100 us against BF32).
 static int bl_lanes_of(int E, int size) {
   if (E * size < 16) return 8;
   int l = 2;
-  while (l < 64 && l * 64 < E * size) l *= 2;
+  while (l < 64 && l * 16 < E) l *= 2;
   return l;
 }
 
-// Tokens of a chunk: a block's passes over its kGroups tokens amortise its start and its
-// partial sums; about 1024 chunks are enough to fill the chip.
-static int bl_chunk_size(int64_t n_tok, int E, int size) {
+// Tokens of a chunk: a token for every group of lanes until there are about four blocks for every
+// CU, then more.
+static int bl_chunk_tokens(int64_t n_tok, int E, int size) {
   const int groups = kBlThreads / bl_lanes_of(E, size);
-  int passes = 4;
-  while (passes < 64 && n_tok > (int64_t)groups * passes * 1024) passes *= 2;
+  int passes = 1;
+  while (groups * passes * 2 <= kBlMaxChunk && n_tok > (int64_t)groups * passes * 1024) passes *= 2;
   return groups * passes;
 }
 
@@ -503,52 +581,76 @@ static int64_t bl_n_chunks(const BlChunks& c) {
   return (int64_t)c.n_tok / c.size + c.n_seq + (c.outer ? 2 : 0);
 }
 
-static BlChunks bl_chunks(const int32_t* offset, int n_tok, int n_seq, int E, int size, bool outer) {
+static BlChunks bl_chunks(const int32_t* offset, int n_tok, int n_seq, int size, bool outer) {
   BlChunks c;
   c.offset = offset;
   c.n_tok = n_tok;
   c.n_seq = n_seq;
   c.len = offset ? 0 : n_tok / n_seq;
-  c.size = bl_chunk_size(n_tok, E, size);
+  c.size = size;
   c.per = offset ? 0 : std::max(1, (c.len + c.size - 1) / c.size);
   c.outer = offset && outer;
   return c;
 }
 
+static uint32_t bl_magic(int K) { return K == 1 ? 0u : (uint32_t)(((1ull << 32) + K - 1) / K); }
+static int bl_pitch(int E) { return (E + 3) / 4 * 4; }
+
+template <typename T, bool kSig, int kL, int kNV, bool kVec, bool kWhole>
+static void bl_sum(const BlCall& c, const BlChunks& ch) {
+  hipLaunchKernelGGL((bl_sum_kernel<T, kSig, kL, kNV, kVec, kWhole>),
+                     dim3((unsigned)bl_n_chunks(ch)), dim3(kBlThreads), 0, c.stream,
+                     static_cast<const T*>(c.logits), c.ids, ch, c.E, c.K, bl_magic(c.K),
+                     bl_pitch(c.E), c.part, c.loss, c.counts, c.prob, c.tokens, c.err);
+}
+
 template <typename T, bool kSig, int kL, int kNV, bool kVec>
 static uep_status bl_forward(const BlCall& c) {
-  const BlChunks ch = bl_chunks(c.offset, c.n_tok, c.n_seq, c.E, sizeof(T), false);
-  const unsigned blocks = (unsigned)bl_n_chunks(ch);
-  const T* logits = static_cast<const T*>(c.logits);
-  if (!c.offset && ch.per == 1) {
-    hipLaunchKernelGGL((bl_sum_kernel<T, kSig, kL, kNV, kVec, true>), dim3(blocks),
-                       dim3(kBlThreads), 0, c.stream, logits, c.ids, ch, c.E, c.K, c.part, c.loss,
-                       c.counts, c.prob, c.tokens, c.err);
+  const int size = bl_chunk_tokens(c.n_tok, c.E, sizeof(T));
+  const int len = c.n_tok / c.n_seq, most = std::min(4 * kBlThreads / kL, kBlMaxChunk);
+  // short sequences: a block each, up to four passes, and no second launch
+  if (!c.offset && len <= std::max(size, most)) {
+    bl_sum<T, kSig, kL, kNV, kVec, true>(
+        c, bl_chunks(nullptr, c.n_tok, c.n_seq, std::max(len, 1), false));
     UEP_CHECK_LAUNCH();
     return UEP_OK;
   }
-  hipLaunchKernelGGL((bl_sum_kernel<T, kSig, kL, kNV, kVec, false>), dim3(blocks),
-                     dim3(kBlThreads), 0, c.stream, logits, c.ids, ch, c.E, c.K, c.part, c.loss,
-                     c.counts, c.prob, c.tokens, c.err);
+  const BlChunks ch = bl_chunks(c.offset, c.n_tok, c.n_seq, size, false);
+  bl_sum<T, kSig, kL, kNV, kVec, false>(c, ch);
   UEP_CHECK_LAUNCH();
-  const unsigned slices = (unsigned)((c.E + kBlSlice - 1) / kBlSlice);
-  int rows = 4;                       // as many as a sequence has chunks on the average
-  while (rows < kBlJoinRows && rows * c.n_seq < (int)blocks) rows *= 2;
-  hipLaunchKernelGGL(bl_join_kernel, dim3(slices, (unsigned)c.n_seq), dim3(rows * kBlSlice), 0,
-                     c.stream, ch, c.E, c.K, c.part, c.loss, c.counts, c.prob, c.tokens, c.err);
+  // as many rows of threads as a sequence has chunks on the average; from 128 on the experts go to
+  // several blocks (1024 chunks of one sequence, 128 experts: JOIN us)
+  const int64_t mean = bl_n_chunks(ch) / c.n_seq;
+  int wide = 16, slices = 1;
+  while (wide < 256 && 4 * wide < c.E) wide *= 2;
+  if (mean >= kBlSliced) {
+    wide = kBlSliceWide;
+    slices = (c.E + 4 * wide - 1) / (4 * wide);
+  }
+  int threads = std::max(wide, kWave);
+  while (threads < kBlJoin && threads / wide < mean) threads *= 2;
+  hipLaunchKernelGGL(bl_join_kernel, dim3((unsigned)c.n_seq, slices), dim3(threads), 0, c.stream,
+                     ch, c.E, c.K, bl_pitch(c.E), wide, c.part, c.loss, c.counts, c.prob,
+                     c.tokens, c.err);
+  if (slices > 1) {
+    UEP_CHECK_LAUNCH();
+    hipLaunchKernelGGL(bl_loss_kernel, dim3((unsigned)c.n_seq), dim3(kWave), 0, c.stream, c.part,
+                       slices, c.E, c.K, c.tokens, c.loss);
+  }
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }
 
 template <typename T, bool kSig, int kL, int kNV, bool kVec>
 static uep_status bl_backward(const BlCall& c) {
-  const BlChunks ch = bl_chunks(c.offset, c.n_tok, c.n_seq, c.E, sizeof(T), true);
-  const unsigned blocks = (unsigned)bl_n_chunks(ch);
+  const BlChunks ch = bl_chunks(c.offset, c.n_tok, c.n_seq,
+                                bl_chunk_tokens(c.n_tok, c.E, sizeof(T)), true);
 #define UEP_BL_GRAD(ADD)                                                                        \
-  hipLaunchKernelGGL((bl_grad_kernel<T, kSig, ADD, kL, kNV, kVec>), dim3(blocks),               \
-                     dim3(kBlThreads), 0, c.stream, c.dloss, static_cast<const T*>(c.logits),   \
-                     c.ids, c.counts, c.tokens, ch, c.E, c.K, static_cast<const T*>(c.add),     \
-                     static_cast<T*>(c.dlogits), c.err)
+  hipLaunchKernelGGL((bl_grad_kernel<T, kSig, ADD, kL, kNV, kVec>),                             \
+                     dim3((unsigned)bl_n_chunks(ch)), dim3(kBlThreads), 0, c.stream, c.dloss,    \
+                     static_cast<const T*>(c.logits), c.ids, c.counts, c.tokens, ch, c.E, c.K,  \
+                     bl_magic(c.K), static_cast<const T*>(c.add), static_cast<T*>(c.dlogits),   \
+                     c.err)
   if (c.add) UEP_BL_GRAD(true);
   else UEP_BL_GRAD(false);
 #undef UEP_BL_GRAD
@@ -567,15 +669,15 @@ static uep_status bl_by_experts(const BlCall& c) {
   constexpr int kSize = sizeof(T);
   if (c.E * kSize < 16) return bl_either<T, kSig, 8, 1, false>(c);
   switch (bl_lanes_of(c.E, kSize)) {
-    case 2: return bl_either<T, kSig, 2, 4, true>(c);
-    case 4: return bl_either<T, kSig, 4, 4, true>(c);
-    case 8: return bl_either<T, kSig, 8, 4, true>(c);
-    case 16: return bl_either<T, kSig, 16, 4, true>(c);
-    case 32: return bl_either<T, kSig, 32, 4, true>(c);
+    case 2: return bl_either<T, kSig, 2, kSize, true>(c);
+    case 4: return bl_either<T, kSig, 4, kSize, true>(c);
+    case 8: return bl_either<T, kSig, 8, kSize, true>(c);
+    case 16: return bl_either<T, kSig, 16, kSize, true>(c);
+    case 32: return bl_either<T, kSig, 32, kSize, true>(c);
     default: break;
   }
-  if (c.E * kSize <= 64 * 64) return bl_either<T, kSig, 64, 4, true>(c);
-  return bl_either<T, kSig, 64, kBlMaxE * kSize / 16 / 64, true>(c);
+  if (c.E <= 1024) return bl_either<T, kSig, 64, kSize, true>(c);
+  return bl_either<T, kSig, 64, 4 * kSize, true>(c);
 }
 
 static uep_status bl_run(const BlCall& c, int dtype, int score) {
@@ -601,21 +703,20 @@ static uep_status bl_check(const void* logits, int32_t dtype, const int32_t* top
 static size_t bl_align(size_t n) { return (n + 255) / 256 * 256; }
 
 // Layout of the workspace; chunks for the smaller of the two dtypes' sizes.
-static size_t bl_workspace(char* ws, int64_t n_tok, int64_t n_seq, int64_t E, BlPartial* p) {
-  const int64_t size =
-      std::min(bl_chunk_size(n_tok, (int)E, 4), bl_chunk_size(n_tok, (int)E, 2));
+static size_t bl_workspace(char* ws, int64_t n_tok, int64_t n_seq, int E, BlPartial* p) {
+  const int64_t size = std::min(bl_chunk_tokens(n_tok, E, 4), bl_chunk_tokens(n_tok, E, 2));
   const size_t chunks = (size_t)(n_tok / size + n_seq);
-  const size_t slices = (size_t)((E + kBlSlice - 1) / kBlSlice);
-  const size_t a = bl_align(n_seq * slices * sizeof(double)), t = bl_align(n_seq * 4);
-  const size_t row = bl_align(chunks * E * 4), tok = bl_align(chunks * 4);
+  const size_t row = bl_align(chunks * bl_pitch(E) * 4), tok = bl_align(chunks * 4);
+  // sliced only with kBlSliced chunks a sequence and more
+  const size_t slices = (E + 4 * kBlSliceWide - 1) / (4 * kBlSliceWide);
+  const size_t sliced = std::min<size_t>(n_seq, chunks / kBlSliced + 1) * slices * sizeof(double);
   if (p) {
-    p->loss = reinterpret_cast<double*>(ws);
-    p->ticket = reinterpret_cast<int32_t*>(ws + a);
-    p->prob = reinterpret_cast<float*>(ws + a + t);
-    p->count = reinterpret_cast<int32_t*>(ws + a + t + row);
-    p->tokens = reinterpret_cast<int32_t*>(ws + a + t + 2 * row);
+    p->loss = reinterpret_cast<double*>(ws + 2 * row + tok);
+    p->prob = reinterpret_cast<float*>(ws);
+    p->count = reinterpret_cast<int32_t*>(ws + row);
+    p->tokens = reinterpret_cast<int32_t*>(ws + 2 * row);
   }
-  return a + t + 2 * row + tok;
+  return 2 * row + tok + bl_align(sliced);
 }
 
 }  // namespace uep
