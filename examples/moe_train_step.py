@@ -1,17 +1,19 @@
 """One MoE layer trained through the library: every step of the layer that is not a plain
-matrix product runs in its kernels.
+matrix product runs in its kernels.  Once trained it also answers in 8 bits, products and all.
 
     router logits -> gate -> plan (replicas, quotas, rows) -> replica weights staged ->
-    permute -> experts -> combine -> loss
+    permute -> experts -> combine -> loss (and the router's balance loss, a sequence per rank)
     loss -> combine gradient -> experts' backward -> replica gradients reduced ->
-    permute gradient, gate gradient -> AdamW over the experts and the router
+    permute gradient, gate gradient, balance gradient -> AdamW over the experts and the router
+    8 bits: ... plan -> replica weights staged -> dispatch in 8 bits -> gate and up products ->
+    rows to 8 bits -> down products -> combine
 
 The layer's ranks are virtual, as everywhere in this library; an instance of an expert (its
 main, or a replica in a redundant slot) computes on the rows that the plan gave it.  The
 experts are SwiGLU blocks (gate, up and down matrices) held in bf16 beside fp32 master
-weights; their matrix products are torch's, in fp32.
+weights; in training their matrix products are torch's, in fp32.
 
-    python examples/moe_train_step.py --steps 30 --state-bits 8
+    python examples/moe_train_step.py --steps 30 --state-bits 8 --balance 0.01
 """
 
 import argparse
@@ -36,6 +38,7 @@ class Geometry:
     H: int = 128        # hidden size
     F: int = 64         # an expert's inner size
     q_min: int = 16     # smallest quota of a replica
+    balance: float = 0.0    # weight of the balance loss
 
 
 class Layer:
@@ -131,9 +134,58 @@ class Layer:
         dx = torch.empty_like(x)
         U.permute_grad(drows, drow, dx, err=self.err)
         dlogits = U.gate_grad(dgate_w, logits, ids, w, err=self.err)
+        if g.balance:
+            _, counts, _, tokens = self.balance_loss(logits, ids)
+            each = torch.full((g.R,), g.balance / g.R, device=x.device)
+            U.balance_loss_grad(each, logits, ids, counts, tokens, add=dlogits, dlogits=dlogits,
+                                err=self.err)
         flat = dlogits.view(-1, g.E)
         torch.matmul(x.view(-1, g.H).float().t(), flat, out=self.router_grad)
         return dx.float() + (flat @ self.router.t()).view_as(x)
+
+    def balance_loss(self, logits, ids):
+        """(loss, counts, mean scores, tokens) of every rank's tokens as a sequence."""
+        return U.balance_loss(logits, ids, n_seq=self.geo.R, err=self.err)
+
+    def quantise(self):
+        """The experts in 8 bits, a scale for each output channel: gates and ups [E][2F][H], downs
+        [E][H][F]."""
+        g = self.geo
+        gate, up, down = zip(*(self._matrices(w) for w in self.main_w))
+        pairs = ([torch.cat([a.t(), b.t()]) for a, b in zip(gate, up)], [d.t() for d in down])
+        self.int8 = []
+        for mats in pairs:
+            m = torch.stack(mats).to(torch.bfloat16).contiguous()
+            q, scale = U.quant_rows(m.view(-1, m.shape[-1]), err=self.err)
+            self.int8.append((q.view(m.shape), scale.view(m.shape[:2]),
+                              q.new_zeros(g.R, g.S, *m.shape[1:]),
+                              scale.new_zeros(g.R, g.S, m.shape[1])))
+
+    def forward_int8(self, x):
+        """y [R][T][H] bf16 for x [R][T][H] bf16 with the experts of the last quantise()."""
+        g = self.geo
+        logits = x.float() @ self.router + self.lean
+        ids, w = U.gate(logits, g.K, err=self.err)
+        plan = U.plan(ids, g.E, g.S, g.q_min, err=self.err)
+        drow, off = plan["dest_row"], plan["inst_offset"]
+        for main, scale, slot, slot_scale in self.int8:
+            for a, b in ((main, slot), (scale, slot_scale)):
+                a, b = a.view(torch.int16), b.view(torch.int16)
+                U.stage_replica_weights(U.STAGE_WEIGHTS, g.R, g.E, g.S, plan["slot_expert"],
+                                        a.numel() // g.E, main_w=a, slot_w=b)
+        P = g.R * g.T * g.K
+        q = torch.zeros(P, g.H, dtype=torch.int8, device=x.device)
+        scale = torch.zeros(P, device=x.device)
+        U.permute_quant(x, drow, q, scale, err=self.err)
+        for (main, main_scale, slot, slot_scale), act in zip(
+                self.int8, (U.PRODUCT_SWIGLU, U.PRODUCT_PLAIN)):
+            if act == U.PRODUCT_PLAIN:
+                q, scale = U.quant_rows(out, live_rows=off[-1:], err=self.err)
+            out = U.expert_product(q, scale, main, main_scale, off, g.R, g.S, slot, slot_scale,
+                                   act=act, err=self.err)
+        y = torch.empty_like(x)
+        U.combine(out, drow, w, y, err=self.err)
+        return y
 
     def update(self):
         self.step += 1
@@ -151,7 +203,11 @@ class Layer:
 
 def train(steps=30, seed=0, state_bits=32, geo=None):
     """Losses of `steps` steps on fixed random data."""
-    layer = Layer(geo or Geometry(), seed, state_bits)
+    return fit(Layer(geo or Geometry(), seed, state_bits), steps, seed)[0]
+
+
+def fit(layer, steps, seed):
+    """Losses of `steps` steps of a layer on fixed random data, and the data."""
     g = layer.geo
     gen = torch.Generator(device="cuda").manual_seed(seed + 1)
     x = torch.randn(g.R, g.T, g.H, generator=gen, device="cuda").to(torch.bfloat16)
@@ -160,7 +216,7 @@ def train(steps=30, seed=0, state_bits=32, geo=None):
     losses = [float(v) for v in losses]
     if int(layer.err.item()):
         raise RuntimeError(f"the library reported error bits {int(layer.err.item())}")
-    return losses
+    return losses, x
 
 
 def main():
@@ -168,11 +224,18 @@ def main():
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--state-bits", type=int, choices=(8, 32), default=32)
     ap.add_argument("--seed", type=int, default=0)
+    ap.add_argument("--balance", type=float, default=0.0, help="weight of the balance loss")
     a = ap.parse_args()
-    losses = train(a.steps, a.seed, a.state_bits)
+    layer = Layer(Geometry(balance=a.balance), a.seed, a.state_bits)
+    losses, x = fit(layer, a.steps, a.seed)
     for i in range(0, len(losses), max(1, len(losses) // 10)):
         print(f"step {i + 1:4d}  loss {losses[i]:.5f}")
     print(f"last       loss {losses[-1]:.5f}")
+    y, (_, logits, ids, *_) = layer.forward(x)
+    print(f"balance    loss {layer.balance_loss(logits, ids)[0].mean().item():.4f} (1 is even)")
+    layer.quantise()
+    off = (layer.forward_int8(x).float() - y.float()).norm() / y.float().norm()
+    print(f"8 bits     {off.item():.4f} from the bf16 layer's outputs")
 
 
 if __name__ == "__main__":

@@ -645,8 +645,8 @@ uep_status uep_adamw_decode(const uint8_t* m_codes, const uint8_t* v_codes,
  *   loss_g     E / (K n_g) * sum_e counts_ge prob_ge     (1 where both are even; 0 if n_g is 0)
  * A call without seq_offset has n_seq equal sequences of the R*T tokens in order (n_seq = R: a
  * loss for each rank's microbatch; 1: for the whole group).  -infinity masks an expert; NaN
- * and +infinity do too and are flagged; a token without a finite logit has p = 0.  A
- * sigmoid score below 2^-126 counts as 0.
+ * and +infinity do too and are flagged, except in an absent token, whose logits may be anything;
+ * a token without a finite logit has p = 0.  A sigmoid score below 2^-126 counts as 0.
  *
  *   logits     [R][T][E]    in   dtype UEP_F32 or UEP_BF16
  *   topk_ids   [R][T][K]    in   -1: empty slot

@@ -321,8 +321,11 @@ __global__ __launch_bounds__(kBlThreads) void bl_sum_kernel(
     const Row row = next;
     if (kAhead) fetch(t + groups);
     float s[Row::kPer], rest[Row::kPer];
-    const float share = bl_scores<kSig, false, kL>(row, s, rest, bad_logit);
-    const float on = t < n_tok && live[t] ? share : 0.0f;
+    bool bad = false;
+    const float share = bl_scores<kSig, false, kL>(row, s, rest, bad);
+    const bool here = t < n_tok && live[t];
+    bad_logit |= bad && here;                     // an absent token may hold anything
+    const float on = here ? share : 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) acc[i] = fmaf(s[i], on, acc[i]);
   }
@@ -521,7 +524,9 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const bool on = t < n_tok && live[t];
     const float c0 = h0 >= 0 ? c_lds[h0] : 0.0f;
     float s[Row::kPer], rest[Row::kPer], out[Row::kPer];
-    const float share = bl_scores<kSig, kSig, kL>(row, s, rest, bad_logit);
+    bool bad = false;
+    const float share = bl_scores<kSig, kSig, kL>(row, s, rest, bad);
+    bad_logit |= bad && on;                       // an absent token may hold anything
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {

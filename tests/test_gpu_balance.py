@@ -186,6 +186,56 @@ def test_masked_and_bad_logits(E, score, dtype):
     assert torch.equal(d, e)
 
 
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_absent_tokens_may_hold_anything(dtype, score):
+    """Padding: NaN, infinities and the type's largest numbers in the logits of tokens without ids,
+    or outside of every sequence, change nothing and are not reported."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.randn(1, 300, 40, generator=g, device=DEV).to(DT[dtype])
+    ids = torch.topk(x.float(), 3, dim=-1).indices.to(torch.int32)
+    ids[0, 100:130] = -1
+    off = torch.tensor([5, 90, 290], dtype=torch.int32, device=DEV)
+    junk = x.clone()
+    top = torch.finfo(DT[dtype]).max
+    for t, v in ((101, float("nan")), (110, float("inf")), (2, float("nan")), (295, float("inf")),
+                 (112, top), (113, -top), (114, -float("inf"))):
+        junk[0, t] = v
+    err, dl = err_word(), torch.ones(2, device=DEV)
+    want = U.balance_loss(x, ids, 2, seq_offset=off, score=score)
+    got = U.balance_loss(junk, ids, 2, seq_offset=off, score=score, err=err)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    a, b = (U.balance_loss_grad(dl, t, ids, got[1], got[3], seq_offset=off, score=score, err=err)
+            for t in (x, junk))
+    assert torch.equal(a, b) and int(host(err)[0]) == 0
+    assert int(torch.count_nonzero(b[0, :5])) == int(torch.count_nonzero(b[0, 290:])) == 0
+
+
+@pytest.mark.parametrize("G,n", [(254, 3000), (255, 3000), (256, 3000), (300, 100), (5000, 20000),
+                                 (65535, 70000)])
+def test_many_sequences(G, n):
+    """More sequences than threads of a block, most of a few tokens, some of none, one long."""
+    say("case: many sequences", G, n)
+    rng = np.random.default_rng(G)
+    off = np.sort(rng.integers(0, n + 1, G + 1)).astype(np.int32)
+    if G == 5000:
+        off[2000:] = np.maximum(off[2000:], 15000)
+        off[:2000] = np.minimum(off[:2000], 3000)
+    x = to_dev(rng.normal(size=(1, n, 16)) * 2, torch.float32)
+    logits = x.double().cpu().numpy()
+    ids = np.argsort(-logits, axis=-1, kind="stable")[..., :2].astype(np.int32)
+    ids[0, ::7] = -1
+    err = err_word()
+    got = forward(x, to_dev(ids), G, to_dev(off), 0, err)
+    want = check_forward(got, logits, ids, G, off, 0)
+    dloss = rng.normal(size=G).astype(np.float32)
+    d = U.balance_loss_grad(to_dev(dloss, torch.float32), x, to_dev(ids), got[1], got[3],
+                            seq_offset=to_dev(off), err=err)
+    ref, room = grad_bound(dloss, logits, ids, want, G, off, 0)
+    assert (np.abs(host(d) - ref) <= room + 2.0 ** -24 * np.abs(ref) + 2.0 ** -133).all()
+    assert int(host(err)[0]) == 0
+
+
 def test_no_tokens():
     x = torch.empty(2, 0, 16, device=DEV)
     ids = torch.empty(2, 0, 2, dtype=torch.int32, device=DEV)

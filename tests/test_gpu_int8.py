@@ -222,6 +222,14 @@ SHAPES = [
     (200, 4, 8, 2, 80, 272), (1000, 2, 6, 1, 144, 208), (900, 1, 3, 0, 528, 400),
     (2500, 1, 2, 0, 1024, 512), (3000, 2, 4, 1, 320, 1168), (1500, 1, 5, 0, 1008, 128),
     (33, 64, 256, 8, 16, 32),
+    # one of each of the call's forms at the least, with edges of tiles inside of everything
+    (5003, 1, 7, 0, 2576, 272),        # 256 x 256, several tiles a workgroup, half-empty ones
+    (9000, 1, 3, 0, 1040, 144),        # 256 x 256, two steps
+    (2100, 2, 4, 0, 2064, 400), (1000, 1, 1, 0, 4080, 4112),       # 128 x 128, two and one a CU
+    (1000, 1, 4, 0, 1040, 4112), (250, 1, 1, 0, 4080, 4112),       # 64 x 128, 64 x 64
+    (1100, 4, 16, 1, 2064, 528), (120, 1, 1, 0, 4080, 4112),       # 128 x 64, 64 x 32 (depth in 2)
+    (60, 4, 16, 1, 2064, 528), (60, 1, 1, 0, 4080, 4112),          # 64 x 32, 32 x 32
+    (3, 1, 1, 0, 1 << 20, 16),         # very wide
 ]
 
 
