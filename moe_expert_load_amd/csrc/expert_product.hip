@@ -356,9 +356,23 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
   if (blockIdx.x == 0) pr_check_offsets(a);
   const PrMap<kPtSide> map(a);
   const int total = map.total() * cols;
-  // of every gridDim.x tiles an XCD takes consecutive ones
-  int id = (int)xcd_block(blockIdx.x, gridDim.x);
-  if (id >= total) return;
+  // Of every round of gridDim.x tiles an XCD takes consecutive ones, and its share of a last one
+  // that is not full.  A last round of no more than half as many tiles as workgroups gives each
+  // to two, which take 128 of the 256 channels (`half`): 6000 rows, 4096 channels, depth 4096
+  // 100 -> 85 us.
+  int taken = 0, half = -1;
+  auto next = [&](PtTile& t) {
+    const int left = total - taken, grid = gridDim.x;
+    const bool halves = 2 * left <= grid;
+    const int round = min(halves ? 2 * left : left, grid);
+    if ((int)blockIdx.x >= round) return false;
+    int at = (int)xcd_block(blockIdx.x, round);
+    half = halves ? at % 2 : -1;
+    at = halves ? at / 2 : at;
+    t = pt_tile<kGlu>(a, map, taken + at, cols);
+    taken += gridDim.x;
+    return true;
+  };
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t base = __builtin_amdgcn_readfirstlane(
@@ -366,19 +380,22 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
 
   // a wave fills 32 rows of both operands' buffers, 8 by 8
   const int fetch = pt_fetch_lane(lane, a.D);
+  int w_fetch = fetch;                                   // of another's channels nothing
   auto fetch_piece = [&](const PtTile& t, int step, int i) {   // i: 0..3 weights, 4..7 rows
     const uint32_t to = base + (step % 2) * kPtBuf + wave * 4096 + (i % 4) * 1024;
     const int r = wave * 32 + i % 4 * 8, f = r % 128 / 16;
     const int ch = kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
-    if (i < 4) pt_fetch(t.ws, to, fetch, (t.c0 + ch) * a.D + step * kPtDepth);
+    if (i < 4) pt_fetch(t.ws, to, w_fetch, (t.c0 + ch) * a.D + step * kPtDepth);
     else pt_fetch(t.qs, to + 2 * kPtBuf, fetch, r * a.D + step * kPtDepth);
   };
-  const int w_wave = wave % 2 * 128, q_wave = wave / 2 * 64;
+  // The two waves of a SIMD (w and w + 4) differ in channels and in rows, so that half of a tile's
+  // rows, or half of its channels, is work for every SIMD.
+  const int w_half = wave / 4, w_wave = w_half * 128, q_wave = (wave + 2 * w_half) % 4 * 64;
   const int steps = (a.D + kPtDepth - 1) / kPtDepth;
   // scales of the wave's channels (SwiGLU: gates, then ups) and rows, then the first two steps
   auto begin = [&](const PtTile& t, int odd) {
     const uint32_t to = base + kPtTurn + wave * 4096 + kPtScales + odd * kPtScaleBytes;
-    const int ch = t.c0 + (kGlu ? wave % 2 * 64 : w_wave);
+    const int ch = t.c0 + (kGlu ? w_half * 64 : w_wave);
     const i32x4 w_scale = pt_span(t.w_scale, a.N * 4ll);
     pt_fetch4(w_scale, to, lane * 4, ch * 4);
     pt_fetch4(w_scale, to + 256, lane * 4, (ch + (kGlu ? a.n_out : 64)) * 4);
@@ -432,14 +449,17 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
     }
   };
 
-  PtTile t = pt_tile<kGlu>(a, map, id, cols);
+  PtTile t;
+  if (!next(t)) return;
+  w_fetch = half < 0 || half == w_half ? fetch : kPrFar;
   begin(t, 0);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   for (int odd = 0;; odd ^= 1) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    // a wave whose rows are past the tile's only fetches: its neighbour has the SIMD to itself
-    const bool busy = q_wave < t.n_rows;
+    // a wave whose rows are past the tile's, or whose channels another workgroup has, only fetches:
+    // its neighbour has the SIMD to itself
+    const bool busy = q_wave < t.n_rows && (half < 0 || half == w_half);
     if (busy) {
 #pragma unroll
       for (int f = 0; f < 8; ++f)
@@ -480,10 +500,9 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
       }
     }
     const PtTile done = t;
-    id += gridDim.x;
-    const bool again = id < total;
+    const bool again = next(t);
     if (again) {
-      t = pt_tile<kGlu>(a, map, id, cols);
+      w_fetch = half < 0 || half == w_half ? fetch : kPrFar;
       meet();                                            // the buffers are free
       begin(t, odd ^ 1);
     }
@@ -529,7 +548,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = 8 * h + l / 8, row = q_wave + 16 * j + r;
-          const int ch = done.c0 + (kGlu ? wave % 2 * 64 : w_wave + 64 * p) + l % 8 * 8;
+          const int ch = done.c0 + (kGlu ? w_half * 64 : w_wave + 64 * p) + l % 8 * 8;
           const u32x4 v = *reinterpret_cast<const u32x4*>(own + r * 128 + (l % 8 ^ r % 8) * 16);
           const bool in = row < done.n_rows && ch < a.n_out;
           __builtin_amdgcn_raw_buffer_store_b128(v, os, in ? (row * a.n_out + ch) * 2 : kPrFar, 0, 0);
@@ -566,7 +585,8 @@ template <bool kGlu>
 static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;
   const int cols = (a.n_out + kWide - 1) / kWide;
-  const int64_t tiles = std::min(a.rows, a.rows / kPtSide + a.n_inst) * cols;
+  // twice the tiles: a tile may be two workgroups' work
+  const int64_t tiles = 2 * std::min(a.rows, a.rows / kPtSide + a.n_inst) * cols;
   hipLaunchKernelGGL((pr_tile_kernel<kGlu>), dim3((unsigned)std::min<int64_t>(tiles, kPtGroups)),
                      dim3(kPtThreads), 0, s, a, cols);
   UEP_CHECK_LAUNCH();
@@ -616,9 +636,17 @@ static int pr_form(const PrArgs& a) {
                            std::max(used, (a.rows + f.rows - 1) / f.rows + used / 2);
     const float loads = (float)groups / (256.0f * f.resident);
     float us = f.load / 2 + steps * f.one;               // at most one workgroup a CU
-    if (i == kPr32x32Deep && groups <= 128) us = 1.0f + steps * 0.14f;   // half the CUs: no queue
-    else if (f.resident == 1) us = (float)((groups + 255) / 256) * (steps * f.one + f.load);
-    else if (groups > 256) us = std::max(us, loads * (steps * f.all + f.load));
+    if (i == kPr32x32Deep && groups <= 128) {
+      us = 1.0f + steps * 0.14f;                         // half the CUs: memory is not yet full
+    } else if (i == kPrLarge) {                          // a last round of halves
+      const int64_t last = groups % 256;
+      us = (float)(groups / 256) + (last > 128 ? 1.0f : last > 0 ? 0.6f : 0.0f);
+      us *= steps * f.one + f.load;
+    } else if (f.resident == 1) {
+      us = (float)((groups + 255) / 256) * (steps * f.one + f.load);
+    } else if (groups > 256) {
+      us = std::max(us, loads * (steps * f.all + f.load));
+    }
     if (least == 0.0f || us < least) least = us, best = i;
   }
   return best;
