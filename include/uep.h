@@ -658,7 +658,8 @@ uep_status uep_adamw_decode(const uint8_t* m_codes, const uint8_t* v_codes,
  *                                (n_g).  None may overlap another array
  *   err                     out  optional; UEP_ERR_LOGIT, UEP_ERR_ID_RANGE (such an id is taken
  *                                as -1), UEP_ERR_OFFSET
- *   ws, ws_bytes                 uep_balance_loss_workspace_size(), 16-byte aligned
+ *   ws, ws_bytes                 uep_balance_loss_workspace_size(), 16-byte aligned; calls that may
+ *                                overlap need one each
  * Sums over tokens are fp32 within a block of tokens and 64 bits across blocks, in an order that
  * depends on the geometry and seq_offset alone (the same call gives the same bits).
  * Returns UEP_EINVAL for null pointers, sizes < 1 (T may be 0: every output is 0), an unknown
@@ -749,7 +750,7 @@ uep_status uep_permute_quant(const uint16_t* x, const int32_t* dest_row, int32_t
  *   err                       out  optional; UEP_ERR_OFFSET: a table that falls or leaves
  *                                  [0, rows]
  * q, weights and out 16-byte aligned.  D % 16 == 0, D <= 65536, N % 8 == 0 (SwiGLU: 16),
- * N*D < 2^31, S <= 8, rows < 2^31; otherwise UEP_EGEOM.
+ * N*D < 2^31, S <= 8, rows <= 2^29; otherwise UEP_EGEOM.
  * ------------------------------------------------------------------------- */
 enum { UEP_PRODUCT_PLAIN = 0, UEP_PRODUCT_SWIGLU = 1 };
 uep_status uep_expert_product(const int8_t* q, const float* q_scale, int64_t rows,

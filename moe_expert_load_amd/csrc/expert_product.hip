@@ -15,6 +15,8 @@ namespace uep {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kPrMaxD = 65536;         // 2^16 products of at most 2^14 stay below 2^31
+constexpr int64_t kPrMaxRows = 1ll << 29;
+constexpr int kPrLaneTiles = (1 << 25) - 1;  // more than kPrMaxRows make; 64 of them fit an int
 constexpr int kPrFar = (int)0x80000000u;   // a span offset behind any end: reads zeros
 
 struct PrArgs {
@@ -67,6 +69,7 @@ struct PrMap {
         tiles += pr_tiles(at, to, kRows);
         at = to;
       }
+      tiles = min(tiles, kPrLaneTiles);                 // a table that falls may name more
     }
     upto = wave_incl_scan(tiles);
   }
@@ -131,6 +134,8 @@ __device__ __forceinline__ i32x4 pt_span(const void* p, int64_t bytes) {
 
 // 64 lanes' 16 (4) bytes from span offset `off` + `more` into the 1 KiB (256 bytes) of LDS from
 // `lds` on.  Written by hand because the compiler has every later read of LDS wait for them.
+// `off` is checked against what `more` leaves of the span, so that `more` has to lie inside:
+// rows that a tile does not have are fetched as its first ones, and count for nothing.
 __device__ __forceinline__ void pt_fetch(i32x4 span, uint32_t lds, int off, int more) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -196,17 +201,19 @@ __global__ __launch_bounds__(kWC* kWR* kGroups* kWave) void pr_ring_kernel(PrArg
   // loads past the depth go past the span's end: the same number is on the way at every step
   auto fetch = [&](int round) {
     const int step = round * kGroups + group;
-    const int off = step * kPtDepth < a.D ? fetch_lane : kPrFar;
+    const bool inside = step * kPtDepth < a.D;
+    const int off = inside ? fetch_lane : kPrFar, more = inside ? step * kPtDepth : 0;
     const uint32_t to = base + (round % kStages * kGroups + group) * kStage;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int piece = wave + kTeam * i;
       if (kTeam * i < kCh / 8) {
         const int r = piece * 8, f = r / 16;
-        const int ch = kGlu ? f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
-        pt_fetch(ws, to + piece * 1024, off, (c0 + ch) * a.D + step * kPtDepth);
+        const int ch = c0 + (kGlu ? f / 2 * 16 + r % 16 + f % 2 * a.n_out : r);
+        pt_fetch(ws, to + piece * 1024, off, (ch < a.N ? ch : 0) * a.D + more);
       } else {
-        pt_fetch(qs, to + piece * 1024, off, (piece * 8 - kCh) * a.D + step * kPtDepth);
+        const int r = piece * 8 - kCh;
+        pt_fetch(qs, to + piece * 1024, off, (r < tile.n_rows ? r : 0) * a.D + more);
       }
     }
   };
@@ -334,11 +341,11 @@ struct PtTile {
 };
 
 template <bool kGlu>
-__device__ __forceinline__ PtTile pt_tile(const PrArgs& a, const PrMap<kPtSide>& map, int id,
-                                          int cols) {
+__device__ __forceinline__ PtTile pt_tile(const PrArgs& a, const PrMap<kPtSide>& map, int tiles,
+                                          int id, int cols) {
   // bands of eight row tiles by all columns: what an XCD's workgroups share stays in its L2
   const int band = id / (kPtBand * cols), in_band = id % (kPtBand * cols);
-  const int high = min(kPtBand, map.total() - band * kPtBand);
+  const int high = min(kPtBand, tiles - band * kPtBand);
   const PrTile t = map.find(a, band * kPtBand + in_band % high);
   bool slot;
   const int64_t at = pr_weight(a, t.inst, slot), size = (int64_t)a.N * a.D;
@@ -351,11 +358,11 @@ __device__ __forceinline__ PtTile pt_tile(const PrArgs& a, const PrMap<kPtSide>&
 }
 
 template <bool kGlu>
-__global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int cols) {
+__global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int cols, int most) {
   __shared__ __attribute__((aligned(1024))) char lds[kPtTurn + 8 * 4096];
   if (blockIdx.x == 0) pr_check_offsets(a);
   const PrMap<kPtSide> map(a);
-  const int total = map.total() * cols;
+  const int tiles = min(map.total(), most), total = tiles * cols;
   // Of every round of gridDim.x tiles an XCD takes consecutive ones, and its share of a last one
   // that is not full.  A last round of no more than half as many tiles as workgroups gives each
   // to two, which take 128 of the 256 channels (`half`): 6000 rows, 4096 channels, depth 4096
@@ -369,7 +376,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
     int at = (int)xcd_block(blockIdx.x, round);
     half = halves ? at % 2 : -1;
     at = halves ? at / 2 : at;
-    t = pt_tile<kGlu>(a, map, taken + at, cols);
+    t = pt_tile<kGlu>(a, map, tiles, taken + at, cols);
     taken += gridDim.x;
     return true;
   };
@@ -384,9 +391,10 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
   auto fetch_piece = [&](const PtTile& t, int step, int i) {   // i: 0..3 weights, 4..7 rows
     const uint32_t to = base + (step % 2) * kPtBuf + wave * 4096 + (i % 4) * 1024;
     const int r = wave * 32 + i % 4 * 8, f = r % 128 / 16;
-    const int ch = kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r;
-    if (i < 4) pt_fetch(t.ws, to, w_fetch, (t.c0 + ch) * a.D + step * kPtDepth);
-    else pt_fetch(t.qs, to + 2 * kPtBuf, fetch, r * a.D + step * kPtDepth);
+    const int ch = t.c0 + (kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r);
+    const int more = step * kPtDepth;
+    if (i < 4) pt_fetch(t.ws, to, w_fetch, (ch < a.N ? ch : 0) * a.D + more);
+    else pt_fetch(t.qs, to + 2 * kPtBuf, fetch, (r < t.n_rows ? r : 0) * a.D + more);
   };
   // The two waves of a SIMD (w and w + 4) differ in channels and in rows, so that half of a tile's
   // rows, or half of its channels, is work for every SIMD.
@@ -395,11 +403,12 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
   // scales of the wave's channels (SwiGLU: gates, then ups) and rows, then the first two steps
   auto begin = [&](const PtTile& t, int odd) {
     const uint32_t to = base + kPtTurn + wave * 4096 + kPtScales + odd * kPtScaleBytes;
-    const int ch = t.c0 + (kGlu ? w_half * 64 : w_wave);
+    const int ch = t.c0 + (kGlu ? w_half * 64 : w_wave), ch2 = ch + (kGlu ? a.n_out : 64);
     const i32x4 w_scale = pt_span(t.w_scale, a.N * 4ll);
-    pt_fetch4(w_scale, to, lane * 4, ch * 4);
-    pt_fetch4(w_scale, to + 256, lane * 4, (ch + (kGlu ? a.n_out : 64)) * 4);
-    pt_fetch4(pt_span(a.q_scale + t.row0, t.n_rows * 4ll), to + 512, lane * 4, q_wave * 4);
+    pt_fetch4(w_scale, to, lane * 4, (ch < a.N ? ch : 0) * 4);
+    pt_fetch4(w_scale, to + 256, lane * 4, (ch2 < a.N ? ch2 : 0) * 4);
+    pt_fetch4(pt_span(a.q_scale + t.row0, t.n_rows * 4ll), to + 512, lane * 4,
+              (q_wave < t.n_rows ? q_wave : 0) * 4);
     for (int i = 0; i < 8; ++i) fetch_piece(t, 0, i);
     if (steps > 1)
       for (int i = 0; i < 8; ++i) fetch_piece(t, 1, i);
@@ -588,10 +597,11 @@ template <bool kGlu>
 static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;
   const int cols = (a.n_out + kWide - 1) / kWide;
+  const int64_t tiles = std::min(a.rows, a.rows / kPtSide + a.n_inst);
   // twice the tiles: a tile may be two workgroups' work
-  const int64_t tiles = 2 * std::min(a.rows, a.rows / kPtSide + a.n_inst) * cols;
-  hipLaunchKernelGGL((pr_tile_kernel<kGlu>), dim3((unsigned)std::min<int64_t>(tiles, kPtGroups)),
-                     dim3(kPtThreads), 0, s, a, cols);
+  hipLaunchKernelGGL((pr_tile_kernel<kGlu>),
+                     dim3((unsigned)std::min<int64_t>(2 * tiles * cols, kPtGroups)),
+                     dim3(kPtThreads), 0, s, a, cols, (int)tiles);
   UEP_CHECK_LAUNCH();
   return UEP_OK;
 }
@@ -685,7 +695,7 @@ extern "C" uep_status uep_expert_product(const int8_t* q, const float* q_scale, 
   if (act != UEP_PRODUCT_PLAIN && act != UEP_PRODUCT_SWIGLU) return UEP_EINVAL;
   const int n_out = act == UEP_PRODUCT_SWIGLU ? N / 2 : N;
   if (R > 64 || E > 4096 || S > 8 || E % R != 0 || D % 16 != 0 || D > kPrMaxD || N % 8 != 0 ||
-      n_out % 8 != 0 || (int64_t)N * D >= (1ll << 31) || rows >= (1ll << 31))
+      n_out % 8 != 0 || (int64_t)N * D >= (1ll << 31) || rows > kPrMaxRows)
     return UEP_EGEOM;
   const int e_loc = E / R, n_inst = R * (e_loc + S);
   if (!inst_offset && n_inst != 1) return UEP_EINVAL;

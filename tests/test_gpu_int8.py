@@ -301,6 +301,46 @@ def test_bad_offsets_are_flagged(off):
         assert (f64(guard[:100]) == 7).all() and (f64(guard[200:]) == 7).all()
 
 
+@pytest.mark.parametrize("rows", [400, 3000, 20000])
+def test_offsets_that_name_rows_many_times(rows):
+    """A table that goes up and down names far more tiles than its rows make: flagged, and no more
+    of them worked on than the rows could make."""
+    say("case: product, rising and falling offsets", rows)
+    o = operands(rows, 1, 200, 0, 2048, 32, 7)
+    off = np.tile(np.array([0, rows], np.int32), 101)[:201]
+    guard = torch.full((rows + 200, 2048), 7.0, dtype=torch.bfloat16, device=DEV)
+    err = err_word()
+    run_product(o, off, 1, 0, U.PRODUCT_PLAIN, guard[100:-100], err)
+    assert int(host(err)[0]) == U.ERR_OFFSET
+    assert (f64(guard[:100]) == 7).all() and (f64(guard[-100:]) == 7).all()
+
+
+@pytest.mark.parametrize("rows,N,D,act", [(1, 1000, 1040, 0), (5, 264, 336, 0), (33, 1008, 4112, 1),
+                                          (300, 4104, 144, 0), (700, 2064, 1040, 1),
+                                          (5000, 2056, 272, 0), (5000, 2064, 144, 1)])
+def test_operands_at_the_end_of_their_memory(rows, N, D, act):
+    """Rows, weights and scales behind which nothing that could be read is the same: the result
+    does not depend on what follows them in memory, in partial tiles of every kind."""
+    say("case: product, ends of memory", rows, N, D, act)
+    o = operands(rows, 1, 1, 0, N, D, 12)
+    n_out = N // 2 if act else N
+    outs = []
+    for fill in (0, 85):
+        tail = {}
+        for k in ("q", "q_scale", "w", "w_scale"):
+            t = o[k]
+            flat = torch.full((t.numel() * t.element_size() + 65536,), fill, dtype=torch.uint8,
+                              device=DEV)
+            flat[:t.numel() * t.element_size()] = t.reshape(-1).view(torch.uint8)
+            tail[k] = flat[:t.numel() * t.element_size()].view(t.dtype).view(t.shape)
+        out = torch.full((rows + 300, n_out), 7.0, dtype=torch.bfloat16, device=DEV)
+        run_product(dict(o, **tail), None, 1, 0, act, out[:rows])
+        assert (f64(out[rows:]) == 7).all()
+        outs.append(out[:rows].clone())
+    assert torch.equal(outs[0], outs[1])
+    check_product(o, None, 1, 1, 0, act, outs[0], 7.0)
+
+
 def test_row_offsets_past_32_bits():
     """Rows and outputs of more than 2^31 and 2^32 bytes: the last block against its own product."""
     say("case: product, long buffers")

@@ -128,7 +128,7 @@ def test_product_refusals(lib):
         assert product(lib, **bad) == EINVAL, bad
     for bad in (dict(R=65, E=65), dict(E=5), dict(E=4098), dict(S=9), dict(N=12), dict(D=24),
                 dict(D=65552), dict(N=24, act=1), dict(N=1 << 16, D=1 << 15), dict(n=1 << 31),
-                dict(q=at((1 << 24) + 8)), dict(w=at((4 << 24) + 8)), dict(sw=at((6 << 24) + 8)),
+                dict(n=(1 << 29) + 1), dict(q=at((1 << 24) + 8)), dict(w=at((4 << 24) + 8)), dict(sw=at((6 << 24) + 8)),
                 dict(out=at((8 << 24) + 8))):
         assert product(lib, **bad) == EGEOM, bad
     one = dict(R=1, E=1, S=0, sw=null, ss=null)
