@@ -124,6 +124,13 @@ __device__ __forceinline__ float pr_swiglu(float gate, float up) {
 // over all banks.
 constexpr int kPtDepth = 128;
 
+// Rows are D bytes apart, so that workgroups at the same step, of whichever channels, ask the same
+// few memory channels where D is a multiple of a high power of two.  They begin at different steps
+// instead: part `i` of `n` of the way through those before the last, which keeps its place (the
+// rest of the depth is cut off there).  (8192 rows of 32 instances, 4096 channels, depth 4096: 166
+// -> 147 us; 1024 rows 120 -> 105; 16 rows of one, 16384 channels 17 -> 14; depth 7168 the same.)
+__device__ __forceinline__ int pt_first(int i, int n, int steps) { return i % n * (steps - 1) / n; }
+
 __device__ __forceinline__ i32x4 pt_span(const void* p, int64_t bytes) {
   const uint64_t u = reinterpret_cast<uint64_t>(p);
   return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)u),
@@ -201,9 +208,11 @@ __global__ __launch_bounds__(kWC* kWR* kGroups* kWave) void pr_ring_kernel(PrArg
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
   const int rounds = (a.D + kPtDepth * kGroups - 1) / (kPtDepth * kGroups);
   const int fetch_lane = pt_fetch_lane(lane, a.D);
+  int turn = pt_first((int)(id / n_tiles), 16, rounds);  // of the rounds before the last
   // loads past the depth go past the span's end: the same number is on the way at every step
   auto fetch = [&](int round) {
-    const int step = round * kGroups + group;
+    const int step = (round < rounds - 1 ? turn : round) * kGroups + group;
+    turn = turn + 1 < rounds - 1 ? turn + 1 : 0;
     const bool inside = step * kPtDepth < a.D;
     const int off = inside ? fetch_lane : kPrFar, more = inside ? step * kPtDepth : 0;
     const uint32_t to = base + (round % kStages * kGroups + group) * kStage;
@@ -388,6 +397,10 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
   const uint32_t base = __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds);
 
+  const int steps = (a.D + kPtDepth - 1) / kPtDepth;
+  // the XCDs at different steps, unless it is one instance whose rows and weights they share (8192
+  // rows, 4096 channels, depth 7168: 172 us, else 177)
+  const int first = a.offset ? pt_first((int)blockIdx.x, 8, steps) : 0;
   // a wave fills 32 rows of both operands' buffers, 8 by 8
   const int fetch = pt_fetch_lane(lane, a.D);
   int w_fetch = fetch;                                   // of another's channels nothing
@@ -395,14 +408,14 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
     const uint32_t to = base + (step % 2) * kPtBuf + wave * 4096 + (i % 4) * 1024;
     const int r = wave * 32 + i % 4 * 8, f = r % 128 / 16;
     const int ch = t.c0 + (kGlu ? r / 128 * 64 + f / 2 * 16 + r % 16 + f % 2 * a.n_out : r);
-    const int more = step * kPtDepth;
+    const int from = step + first < steps - 1 ? step + first : step + first - (steps - 1);
+    const int more = (step < steps - 1 ? from : step) * kPtDepth;
     if (i < 4) pt_fetch(t.ws, to, w_fetch, (ch < a.N ? ch : 0) * a.D + more);
     else pt_fetch(t.qs, to + 2 * kPtBuf, fetch, (r < t.n_rows ? r : 0) * a.D + more);
   };
   // The two waves of a SIMD (w and w + 4) differ in channels and in rows, so that half of a tile's
   // rows, or half of its channels, is work for every SIMD.
   const int w_half = wave / 4, w_wave = w_half * 128, q_wave = (wave + 2 * w_half) % 4 * 64;
-  const int steps = (a.D + kPtDepth - 1) / kPtDepth;
   // scales of the wave's channels (SwiGLU: gates, then ups) and rows, then the first two steps
   auto begin = [&](const PtTile& t, int odd) {
     const uint32_t to = base + kPtTurn + wave * 4096 + kPtScales + odd * kPtScaleBytes;
