@@ -250,10 +250,11 @@ __global__ __launch_bounds__(kWC* kWR* kGroups* kWave) void pr_ring_kernel(PrArg
       for (int r = 0; r < kRB; ++r)
         acc[c][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[h][c], x[h][r], acc[c][r], 0, 0, 0);
   };
-  // own reads of the last step are done and own loads of the next have landed; then everyone's
+  // own reads of the last step are done and own loads of the next have landed; then everyone's (a
+  // wave by itself has only its own)
   auto meet = [&]() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((kStages - 2) * kLoads) : "memory");
-    __builtin_amdgcn_s_barrier();
+    if constexpr (kTeam > 1) __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
 #pragma unroll
@@ -631,28 +632,30 @@ static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
 // Which tile.  Each form's time is a chip load of workgroups (`resident` a CU) times the steps of
 // the depth, at what a step was measured to take with one workgroup a CU (`one`) and with all
 // (`all`), plus what a load takes beside its steps (`load`: first loads, results; us).  Half a tile is
-// left over in every instance.  The form that comes out least is taken; over 120 shapes of every
-// kind its measured time is 1.03 times the best form's on the average.  Rows past an instance's are
-// loads that bring nothing, but not for nothing: a form is weighed from `mean` rows an instance on
-// (13 rows of 34 instances, 5840 channels, depth 5360: 75 us by 64 x 32, 89 by 128 x 64; 64 rows in
-// each of 32, depth 4096: 130 us by 128 x 64, 151 by 128 x 128).
+// left over in every instance.  The two forms of a wave a step take their time by the weights that
+// they stream, and are weighed while each workgroup has a CU to itself.  The form that comes out
+// least is taken.  Rows past an instance's are loads that bring nothing, but not for nothing: a form
+// is weighed from `mean` rows an instance on (4096 channels, depth 4096, 72 rows in each of 32:
+// 113 us by 128 x 128, 144 by 128 x 64; 50 rows of 14, most of them in few: 88 us by 128 x 64, 107 by
+// 128 x 128; 13 rows of 34, 5840 channels, depth 5360: 75 us by 64 x 32, 89 by 128 x 64).
 // Measured, one instance, 4096 channels, depth 7168, us:
-//   rows            1    64   128   256   512  1024  2048   8192 (8192 channels, depth 8192)
-//   taken         9.6  13.1  16.6  20.9  28.3  38.4  62.0    378
-//   next larger  13.0  16.4  21.0  28.0  38.2  54.7  80.4
-//   next smaller    -  22.0  18.9  30.1  38.1  53.3  76.2
+//   rows            1    64   128   256   512  1024  8192 (8192 channels, depth 8192)
+//   taken         8.0  12.1  15.5  20.3  27.9  38.5   378
+//   next larger   9.3  16.0  20.5  27.8  37.5  53.5
+//   next smaller    -  17.8  19.4  27.6  38.5  55.2
 struct PrForm {
   int ch, rows, mean, resident;
   float one, all, load;
 };
 enum { kPrLarge, kPr128x128, kPr128x128Deep, kPr64x128, kPr128x64, kPr64x64, kPr64x32Deep,
-       kPr64x32, kPr32x32, kPr32x32Deep, kPrForms };
+       kPr64x32, kPr32x32, kPr32x16, kPr16x16, kPrForms };
 constexpr PrForm kPrForm[kPrForms] = {
-    {256, 256, 96, 1, 1.50f, 1.50f, 5}, {128, 128, 80, 2, 0.93f, 1.09f, 8},
+    {256, 256, 96, 1, 1.50f, 1.50f, 5}, {128, 128, 64, 2, 0.93f, 1.09f, 8},
     {128, 128, 80, 1, 0.66f, 0.66f, 5}, {64, 128, 80, 1, 0.47f, 0.47f, 4},
     {128, 64, 24, 2, 0.60f, 0.87f, 6},  {64, 64, 24, 1, 0.34f, 0.34f, 3},
     {64, 32, 0, 1, 0.27f, 0.27f, 2},    {64, 32, 0, 3, 0.32f, 0.65f, 5},
-    {32, 32, 0, 2, 0.20f, 0.31f, 3},    {32, 32, 0, 1, 0.36f, 0.36f, 1}};
+    {32, 32, 0, 2, 0.20f, 0.31f, 3},    {32, 16, 0, 1, 0.055f, 0.14f, 2.2f},
+    {16, 16, 0, 1, 0.054f, 0.09f, 0.5f}};
 
 template <bool kGlu>
 static int pr_form(const PrArgs& a) {
@@ -665,14 +668,15 @@ static int pr_form(const PrArgs& a) {
   float least = 0.0f;
   for (int i = 0; i < kPrForms; ++i) {
     const PrForm& f = kPrForm[i];
-    if ((i == kPrLarge && !fits) || a.rows < f.mean * used) continue;
+    if ((i == kPrLarge && !fits) || a.rows < f.mean * used || (kGlu && f.ch < 32)) continue;
     const int wide = kGlu ? f.ch / 2 : f.ch;
-    const int64_t groups = (a.n_out + wide - 1) / wide *
-                           std::max(used, (a.rows + f.rows - 1) / f.rows + used / 2);
+    const int64_t cols = (a.n_out + wide - 1) / wide;
+    const int64_t groups = cols * std::max(used, (a.rows + f.rows - 1) / f.rows + used / 2);
     const float loads = (float)groups / (256.0f * f.resident);
     float us = f.load / 2 + steps * f.one;               // at most one workgroup a CU
-    if (i == kPr32x32Deep && groups <= 128) {
-      us = 1.0f + steps * 0.14f;                         // half the CUs: memory is not yet full
+    if (i >= kPr32x16) {                                 // a wave a step: by the weights it reads
+      if (groups > 256) continue;
+      us = f.load + steps * (f.one + f.all * (float)(cols * used) / 256.0f);
     } else if (i == kPrLarge) {                          // a last round of halves
       const int64_t last = groups % 256;
       us = (float)(groups / 256) + (last > 128 ? 1.0f : last > 0 ? 0.6f : 0.0f);
@@ -698,7 +702,9 @@ static uep_status pr_run(const PrArgs& a, hipStream_t s) {
     case kPr64x64: return pr_ring<64, 64, 2, 2, 2, 4, kGlu>(a, s);
     case kPr64x32Deep: return pr_ring<64, 32, 2, 2, 2, 5, kGlu>(a, s);
     case kPr64x32: return pr_ring<64, 32, 2, 2, 1, 4, kGlu>(a, s);
-    case kPr32x32Deep: return pr_ring<32, 32, 1, 2, 2, 8, kGlu>(a, s);
+    case kPr32x16: return pr_ring<32, 16, 1, 1, 8, 3, kGlu>(a, s);
+    case kPr16x16:
+      if constexpr (!kGlu) return pr_ring<16, 16, 1, 1, 8, 4, kGlu>(a, s);
     default: return pr_ring<32, 32, 1, 2, 1, 8, kGlu>(a, s);
   }
 }

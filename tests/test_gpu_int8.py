@@ -229,6 +229,8 @@ SHAPES = [
     (1000, 1, 4, 0, 1040, 4112), (250, 1, 1, 0, 4080, 4112),       # 64 x 128, 64 x 64
     (1100, 4, 16, 1, 2064, 528), (120, 1, 1, 0, 4080, 4112),       # 128 x 64, 64 x 32 (depth in 2)
     (60, 4, 16, 1, 2064, 528), (60, 1, 1, 0, 4080, 4112),          # 64 x 32, 32 x 32
+    (30, 1, 1, 0, 4080, 4112), (16, 1, 1, 0, 4080, 7184),          # 32 x 16; 16 x 16, SwiGLU 32 x 16
+    (40, 2, 8, 1, 272, 4112),          # the same, several instances, a ragged last round of steps
     (3, 1, 1, 0, 1 << 20, 16),         # very wide
 ]
 
