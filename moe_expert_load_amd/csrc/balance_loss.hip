@@ -575,10 +575,18 @@ static int bl_lanes_of(int E, int size) {
   return l;
 }
 
+// Blocks to aim at.  Where each leaves sums to be joined, four for every CU, or two where the scores
+// take less than the memory (fp32) and a block has no more than 256 KiB to read (262144 tokens of
+// 128 fp32 logits 32.7 -> 30.1 us, 32768 15.6 -> 13.5; of 262144 x 256 it would be 49.6 -> 52.5, in
+// bf16 33.8 -> 39.8).  In the gradient sixteen, so that one block's start is behind another's
+// stream (262144 x 256 bf16 sigmoid, added to others, with 4, 8 and 16: 104, 91 and 84 us).
+constexpr int kBlGradBlocks = 4096;
+static int bl_sum_blocks(int64_t n_tok, int E, int size) {
+  return size == 4 && n_tok * E * size <= 512ll << 18 ? 512 : 1024;
+}
+
 // Tokens of a chunk: a token for every group of lanes until there are about `blocks` blocks, then
-// more.  Four for every CU where each leaves sums to be joined, else sixteen, so that one block's
-// start is behind another's stream (the gradient above with 4, 8 and 16: 104, 91 and 84 us).
-constexpr int kBlSumBlocks = 1024, kBlGradBlocks = 4096;
+// more.
 static int bl_chunk_tokens(int64_t n_tok, int E, int size, int blocks) {
   const int groups = kBlThreads / bl_lanes_of(E, size);
   int passes = 1;
@@ -616,7 +624,8 @@ static void bl_sum(const BlCall& c, const BlChunks& ch) {
 
 template <typename T, bool kSig, int kL, int kNV, bool kVec>
 static uep_status bl_forward(const BlCall& c) {
-  const int size = bl_chunk_tokens(c.n_tok, c.E, sizeof(T), kBlSumBlocks);
+  const int size =
+      bl_chunk_tokens(c.n_tok, c.E, sizeof(T), bl_sum_blocks(c.n_tok, c.E, sizeof(T)));
   const int len = c.n_tok / c.n_seq, most = std::min(4 * kBlThreads / kL, kBlMaxChunk);
   // short sequences: a block each, up to four passes, and no second launch
   if (!c.offset && len <= std::max(size, most)) {
@@ -714,8 +723,8 @@ static size_t bl_align(size_t n) { return (n + 255) / 256 * 256; }
 
 // Layout of the workspace; chunks for the smaller of the two dtypes' sizes.
 static size_t bl_workspace(char* ws, int64_t n_tok, int64_t n_seq, int E, BlPartial* p) {
-  const int64_t size = std::min(bl_chunk_tokens(n_tok, E, 4, kBlSumBlocks),
-                                bl_chunk_tokens(n_tok, E, 2, kBlSumBlocks));
+  const int64_t size = std::min(bl_chunk_tokens(n_tok, E, 4, bl_sum_blocks(n_tok, E, 4)),
+                                bl_chunk_tokens(n_tok, E, 2, bl_sum_blocks(n_tok, E, 2)));
   const size_t chunks = (size_t)(n_tok / size + n_seq);
   const size_t row = bl_align(chunks * bl_pitch(E) * 4), tok = bl_align(chunks * 4);
   // sliced only with kBlSliced chunks a sequence and more
