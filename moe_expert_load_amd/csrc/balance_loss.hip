@@ -91,7 +91,7 @@ __device__ __forceinline__ BlChunk bl_chunk(const BlChunks& c, int b) {
   return k;
 }
 
-// Calls f(token of the chunk, slot, id) for every id of the chunk in [0, E); true if one is
+// Calls f(token of the chunk, id) for every id of the chunk in [0, E); true if one is
 // neither that nor -1.  k_magic = ceil(2^32 / K), exact for the at most 2^17 ids of a chunk.
 template <typename F>
 __device__ __forceinline__ bool bl_ids(const int32_t* ids, const BlChunk& c, int E, int K,
@@ -105,10 +105,10 @@ __device__ __forceinline__ bool bl_ids(const int32_t* ids, const BlChunk& c, int
     for (int u = 0; u < 4; ++u) e[u] = i0 + u * step < n ? p[i0 + u * step] : -1;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * step, t = K == 1 ? i : (int)__umulhi(i, k_magic);
+      const int i = i0 + u * step;
       const bool in = e[u] >= 0 && e[u] < E;
       bad |= !in && e[u] != -1;
-      if (in) f(t, i - t * K, e[u]);
+      if (in) f(K == 1 ? i : (int)__umulhi(i, k_magic), e[u]);
     }
   }
   return bad;
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(kBlThreads) void bl_sum_kernel(
   for (int t = threadIdx.x; t < n_tok; t += blockDim.x) live[t] = 0;
   if (threadIdx.x == 0) present = 0;
   __syncthreads();
-  const bool bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int, int e) {
+  const bool bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int e) {
     live[t] = 1;
     atomicAdd(&hist[e], 1);
   });
@@ -462,9 +462,10 @@ __global__ __launch_bounds__(kWave) void bl_loss_kernel(BlPartial part, int slic
   if (threadIdx.x == 0) loss[g] = bl_loss(dot, E, K, tokens[g]);
 }
 
-// dl_e = f p_e ((c_e - c_0) - sum_j p_j (c_j - c_0)) [(1 - s_e)].  c_0 is the count of the
-// token's first expert, mostly its most likely one: where one expert takes nearly all of p the
-// difference then keeps its digits.  Counts enter as floats (exact below 2^24).
+// dl_e = f p_e ((c_e - c_0) - sum_j p_j (c_j - c_0)) [(1 - s_e)].  c_0 is the integer next to
+// sum_j p_j c_j: differences of counts are exact and the sum is at most about half, so that the
+// result keeps its digits where one expert takes nearly all of p, and where the chosen ones take
+// next to nothing.  Counts enter as floats (exact below 2^24).
 template <typename T, bool kSig, bool kAdd, int kL, int kNV, bool kVec>
 __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const float* __restrict__ dloss, const T* __restrict__ logits,
@@ -473,7 +474,6 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const T* add, T* dlogits, int32_t* err) {
   typedef BlRow<T, kL, kNV, kVec> Row;
   __shared__ float c_lds[kL * Row::kPer];
-  __shared__ int16_t head[kBlMaxChunk];           // a token's first id, -1 if that slot is empty
   __shared__ uint8_t live[kBlMaxChunk];
   const int lane = threadIdx.x % kL, group = threadIdx.x / kL, groups = blockDim.x / kL;
   if (chunks.offset && blockIdx.x == 0)
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
   };
   constexpr bool kAhead = Row::kPer <= 16;
   if (kAhead) fetch(group);
-  for (int t = threadIdx.x; t < n_tok; t += blockDim.x) live[t] = 0, head[t] = -1;
+  for (int t = threadIdx.x; t < n_tok; t += blockDim.x) live[t] = 0;
   if (inside)
     for (int e = threadIdx.x; e < E; e += blockDim.x)
       c_lds[e] = (float)counts[(int64_t)c.seq * E + e];
@@ -502,10 +502,7 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
   if (inside) {
     const double n = tokens[c.seq];
     f = n > 0.0 ? dloss[c.seq] * (float)(E / (K * n * n)) : 0.0f;
-    bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int slot, int e) {
-      live[t] = 1;
-      if (slot == 0) head[t] = (int16_t)e;
-    });
+    bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int) { live[t] = 1; });
   }
   __syncthreads();
   float cnt[Row::kPer];
@@ -520,14 +517,16 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     if (!kAhead) fetch(t);
     const Row row = next, base = next_base;
     if (kAhead) fetch(t + groups);
-    const int h0 = t < n_tok ? head[t] : -1;
     const bool on = t < n_tok && live[t];
-    const float c0 = h0 >= 0 ? c_lds[h0] : 0.0f;
     float s[Row::kPer], rest[Row::kPer], out[Row::kPer];
     bool bad = false;
     const float share = bl_scores<kSig, kSig, kL>(row, s, rest, bad);
     bad_logit |= bad && on;                       // an absent token may hold anything
     float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Row::kPer; ++i) dot = fmaf(s[i], cnt[i], dot);
+    const float c0 = rintf(bl_lanes_sum<kL>(dot) * share);
+    dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {
       out[i] = cnt[i] - c0;

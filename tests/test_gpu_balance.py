@@ -288,6 +288,21 @@ def test_a_sure_expert_keeps_its_gradient():
     assert (np.abs(host(d) - ref) <= 400 * EPS * np.abs(ref)).all() and (ref[..., 0] != 0).all()
 
 
+@pytest.mark.parametrize("score", [U.GATE_SOFTMAX, U.GATE_SIGMOID])
+def test_one_token_of_many_experts(score):
+    """Where the chosen expert has a small part of p the others' gradients are products of two
+    small parts: -f p_e p_h (1 - s_e), three factors that are each as near as a score."""
+    g = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.randn(1, 12, 4096, generator=g, device=DEV)
+    ids = torch.randint(0, 4096, (1, 12, 1), generator=g, device=DEV, dtype=torch.int32)
+    _, counts, _, tokens = U.balance_loss(x, ids, 12, score=score)
+    d = host(U.balance_loss_grad(torch.ones(12, device=DEV), x, ids, counts, tokens, score=score))
+    ref = O.balance_loss_grad([1.0] * 12, host(x), host(ids), host(counts), host(tokens), 12, None,
+                              score)
+    rel = (4 * spread(host(x), score) + 160) * EPS
+    assert (np.abs(d - ref) <= (3 * rel + 16 * EPS) * np.abs(ref)).all()
+
+
 def test_unaligned_rows_and_streams():
     """Tensors that start anywhere, on a stream of their own, without a caller's workspace."""
     flat = torch.randn(1 + 300 * 40, device=DEV)
