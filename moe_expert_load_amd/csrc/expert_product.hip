@@ -142,23 +142,23 @@ __device__ __forceinline__ i32x4 pt_span(const void* p, int64_t bytes) {
 // `lds` on.  Written by hand because the compiler has every later read of LDS wait for them.
 // `off` is checked against what `more` leaves of the span, so that `more` has to lie inside:
 // rows that a tile does not have are fetched as its first ones, and count for nothing.
+// The scalars may come from vector instructions (a spilled one by v_readlane), which the load may
+// follow no sooner than five wait states later; the compiler sees to that for its own loads only.
 __device__ __forceinline__ void pt_fetch(i32x4 span, uint32_t lds, int off, int more) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
+      "s_nop 4\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
-      : "s"(lds), "v"(off), "s"(span), "s"(more)
-      : "memory", "m0");
+      : "{m0}"(lds), "v"(off), "s"(span), "s"(more)
+      : "memory");
 }
 __device__ __forceinline__ void pt_fetch4(i32x4 span, uint32_t lds, int off, int more) {
   asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
+      "s_nop 4\n\t"
       "buffer_load_dword %1, %2, %3 offen lds"
       :
-      : "s"(lds), "v"(off), "s"(span), "s"(more)
-      : "memory", "m0");
+      : "{m0}"(lds), "v"(off), "s"(span), "s"(more)
+      : "memory");
 }
 
 // Lane's part of 8 rows that one load brings, and of 16 rows that one read takes (first half of the
