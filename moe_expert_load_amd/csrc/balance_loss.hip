@@ -465,7 +465,8 @@ __global__ __launch_bounds__(kWave) void bl_loss_kernel(BlPartial part, int slic
 // dl_e = f p_e ((c_e - c_0) - sum_j p_j (c_j - c_0)) [(1 - s_e)].  c_0 is the integer next to
 // sum_j p_j c_j: differences of counts are exact and the sum is at most about half, so that the
 // result keeps its digits where one expert takes nearly all of p, and where the chosen ones take
-// next to nothing.  Counts enter as floats (exact below 2^24).
+// next to nothing.  Counts enter as floats (exact below 2^24).  The factor that makes the scores
+// sum to one goes up to 2^126 and meets the scores first: p and what follows stay in range.
 template <typename T, bool kSig, bool kAdd, int kL, int kNV, bool kVec>
 __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const float* __restrict__ dloss, const T* __restrict__ logits,
@@ -524,19 +525,22 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     bad_logit |= bad && on;                       // an absent token may hold anything
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < Row::kPer; ++i) dot = fmaf(s[i], cnt[i], dot);
-    const float c0 = rintf(bl_lanes_sum<kL>(dot) * share);
+    for (int i = 0; i < Row::kPer; ++i) {
+      s[i] *= share;
+      dot = fmaf(s[i], cnt[i], dot);
+    }
+    const float c0 = rintf(bl_lanes_sum<kL>(dot));
     dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {
       out[i] = cnt[i] - c0;
       dot = fmaf(s[i], out[i], dot);
     }
-    dot = bl_lanes_sum<kL>(dot) * share;
-    const float h = on && share > 0.0f ? f * share : 0.0f;
+    dot = bl_lanes_sum<kL>(dot);
+    const float h = on && share > 0.0f ? f : 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {
-      float d = h * s[i] * (out[i] - dot);
+      float d = s[i] * (out[i] - dot) * h;
       if constexpr (kSig) d *= rest[i];
       if constexpr (kAdd) d += base.at(i);
       out[i] = d;
