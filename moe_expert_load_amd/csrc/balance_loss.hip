@@ -463,10 +463,15 @@ __global__ __launch_bounds__(kWave) void bl_loss_kernel(BlPartial part, int slic
 }
 
 // dl_e = f p_e ((c_e - c_0) - sum_j p_j (c_j - c_0)) [(1 - s_e)].  c_0 is the integer next to
-// sum_j p_j c_j: differences of counts are exact and the sum is at most about half, so that the
-// result keeps its digits where one expert takes nearly all of p, and where the chosen ones take
-// next to nothing.  Counts enter as floats (exact below 2^24).  The factor that makes the scores
+// sum_j p_j c_j: the sum is at most about half, so that the result keeps its digits where one
+// expert takes nearly all of p, and where the chosen ones take next to nothing.  Counts are
+// subtracted as integers, the first expert's before c_0 is looked for (a whole group's counts are
+// past 2^24, and what tells them apart are their last digits).  The factor that makes the scores
 // sum to one goes up to 2^126 and meets the scores first: p and what follows stay in range.
+__device__ __forceinline__ int32_t bl_minus(int32_t a, int32_t b) {     // wraps
+  return (int32_t)((uint32_t)a - (uint32_t)b);
+}
+
 template <typename T, bool kSig, bool kAdd, int kL, int kNV, bool kVec>
 __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const float* __restrict__ dloss, const T* __restrict__ logits,
@@ -474,7 +479,7 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     const int32_t* __restrict__ tokens, BlChunks chunks, int E, int K, uint32_t k_magic,
     const T* add, T* dlogits, int32_t* err) {
   typedef BlRow<T, kL, kNV, kVec> Row;
-  __shared__ float c_lds[kL * Row::kPer];
+  __shared__ int32_t c_lds[kL * Row::kPer];
   __shared__ uint8_t live[kBlMaxChunk];
   const int lane = threadIdx.x % kL, group = threadIdx.x / kL, groups = blockDim.x / kL;
   if (chunks.offset && blockIdx.x == 0)
@@ -494,9 +499,11 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
   constexpr bool kAhead = Row::kPer <= 16;
   if (kAhead) fetch(group);
   for (int t = threadIdx.x; t < n_tok; t += blockDim.x) live[t] = 0;
-  if (inside)
-    for (int e = threadIdx.x; e < E; e += blockDim.x)
-      c_lds[e] = (float)counts[(int64_t)c.seq * E + e];
+  if (inside) {
+    const int32_t* row = counts + (int64_t)c.seq * E;
+    const int32_t some = row[0];
+    for (int e = threadIdx.x; e < E; e += blockDim.x) c_lds[e] = bl_minus(row[e], some);
+  }
   __syncthreads();
   bool bad_id = false;
   float f = 0.0f;
@@ -506,11 +513,11 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
     bad_id = bl_ids(ids, c, E, K, k_magic, [&](int t, int) { live[t] = 1; });
   }
   __syncthreads();
-  float cnt[Row::kPer];
+  int32_t cnt[Row::kPer];
 #pragma unroll
   for (int i = 0; i < Row::kPer; ++i) {
     const int e = Row::expert(lane, i);
-    cnt[i] = inside && e < E ? c_lds[e] : 0.0f;
+    cnt[i] = inside && e < E ? c_lds[e] : 0;
   }
   bool bad_logit = false;
   for (int t0 = 0; t0 < n_tok; t0 += groups) {
@@ -527,13 +534,14 @@ __global__ __launch_bounds__(kBlThreads) void bl_grad_kernel(
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {
       s[i] *= share;
-      dot = fmaf(s[i], cnt[i], dot);
+      dot = fmaf(s[i], (float)cnt[i], dot);
     }
-    const float c0 = rintf(bl_lanes_sum<kL>(dot));
+    // the largest floats that are int32
+    const int32_t c0 = (int32_t)rintf(fminf(fmaxf(bl_lanes_sum<kL>(dot), -0x1p31f), 0x1.fffffep30f));
     dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < Row::kPer; ++i) {
-      out[i] = cnt[i] - c0;
+      out[i] = (float)bl_minus(cnt[i], c0);
       dot = fmaf(s[i], out[i], dot);
     }
     dot = bl_lanes_sum<kL>(dot);

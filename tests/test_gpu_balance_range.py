@@ -72,3 +72,42 @@ def test_scores_at_the_bottom_of_their_range(left, dloss, dtype):
                                 host(tokens), 3, None, 1)
     check(d, ref, room, dtype)
     assert int(host(err)[0]) == 0 and (ref != 0).any() == (len(left) > 1)
+
+
+@pytest.mark.parametrize("score", [U.GATE_SOFTMAX, U.GATE_SIGMOID])
+@pytest.mark.parametrize("E,K", [(2, 1), (16, 8), (60, 16), (1500, 40)])
+@pytest.mark.parametrize("near", [1, 3000, 1 << 20])
+def test_counts_past_24_bits(E, K, near, score):
+    """Counts of a whole group, far past 2^24 and near each other: what tells them apart are their
+    differences, and those are exact."""
+    say("case: large counts", E, K, near, score)
+    rng = np.random.default_rng(E + near)
+    n = min(1 << 26, (1 << 30) // K)
+    near = min(near, K * n // E - 1)
+    counts = (K * n // E + rng.integers(-near, near + 1, (2, E))).astype(np.int32)
+    x = to_dev(rng.normal(size=(1, 60, E)) * 2, torch.float32)
+    ids = to_dev(rng.integers(0, E, (1, 60, K)))
+    tokens, dloss = np.array([n, n - 5], np.int32), np.float32([1e9, -3e8])
+    d = U.balance_loss_grad(to_dev(dloss, torch.float32), x, ids, to_dev(counts), to_dev(tokens),
+                            score=score)
+    ref, room = oracle_and_room(dloss, host(x).astype(np.float64), host(ids), counts, tokens, 2, None,
+                                score)
+    check(d, ref, room)
+
+
+@pytest.mark.parametrize("score", [U.GATE_SOFTMAX, U.GATE_SIGMOID])
+def test_two_busy_experts_of_many(score):
+    """Two experts with nearly all ids and nearly all of p, the others with none: their counts
+    differ by one, and that is what their gradients are made of."""
+    E = 64
+    x = torch.full((1, 8, E), -30.0, device=DEV)
+    x[..., 7] = x[..., 50] = 0.5
+    ids = torch.tensor([7, 50], dtype=torch.int32, device=DEV).expand(1, 8, 2).contiguous()
+    counts = np.zeros((1, E), np.int32)
+    counts[0, 7], counts[0, 50] = (1 << 30) - 1, 1 << 30
+    tokens = np.array([1 << 30], np.int32)
+    d = U.balance_loss_grad(torch.full((1,), 1e18, device=DEV), x, ids, to_dev(counts),
+                            to_dev(tokens), score=score)
+    ref, room = oracle_and_room(np.float32([1e18]), host(x).astype(np.float64), host(ids), counts,
+                                tokens, 1, None, score)
+    check(d, ref, room)
