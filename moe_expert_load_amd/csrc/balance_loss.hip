@@ -14,15 +14,12 @@
 #include "common.h"
 #include "logits.h"
 #include "numeric.h"
+#include "rules.h"
 
 namespace uep {
 
 constexpr int kBlMaxE = 4096;
 constexpr int kBlMaxSeq = 65535;      // blocks of the second launch
-constexpr int kBlMaxChunk = 2048;     // tokens of a chunk
-
-constexpr int kBlThreads = 256;
-constexpr int kBlSliced = 128;        // chunks of a sequence from which its experts are sliced
 constexpr int kBlSliceWide = 4;
 
 // How the tokens fall into chunks of at most `size` tokens of one sequence each.  Equal
@@ -575,35 +572,6 @@ struct BlCall {
   int32_t* err;
   hipStream_t stream;
 };
-
-// Lanes of a token: as few as hold the experts with 16 each (above 1024 experts 64 each).  With 32
-// a lane the sigmoid's gradient takes 226 registers and two waves a SIMD (262144 tokens of 256
-// bf16 logits, added to others: 110 us against 104).
-static int bl_lanes_of(int E, int size) {
-  if (E * size < 16) return 8;
-  int l = 2;
-  while (l < 64 && l * 16 < E) l *= 2;
-  return l;
-}
-
-// Blocks to aim at.  Where each leaves sums to be joined, four for every CU, or two where the scores
-// take less than the memory (fp32) and a block has no more than 256 KiB to read (262144 tokens of
-// 128 fp32 logits 32.7 -> 30.1 us, 32768 15.6 -> 13.5; of 262144 x 256 it would be 49.6 -> 52.5, in
-// bf16 33.8 -> 39.8).  In the gradient sixteen, so that one block's start is behind another's
-// stream (262144 x 256 bf16 sigmoid, added to others, with 4, 8 and 16: 104, 91 and 84 us).
-constexpr int kBlGradBlocks = 4096;
-static int bl_sum_blocks(int64_t n_tok, int E, int size) {
-  return size == 4 && n_tok * E * size <= 512ll << 18 ? 512 : 1024;
-}
-
-// Tokens of a chunk: a token for every group of lanes until there are about `blocks` blocks, then
-// more.
-static int bl_chunk_tokens(int64_t n_tok, int E, int size, int blocks) {
-  const int groups = kBlThreads / bl_lanes_of(E, size);
-  int passes = 1;
-  while (groups * passes * 2 <= kBlMaxChunk && n_tok > (int64_t)groups * passes * blocks) passes *= 2;
-  return groups * passes;
-}
 
 static int64_t bl_n_chunks(const BlChunks& c) {
   if (!c.offset) return (int64_t)c.n_seq * c.per;

@@ -9,6 +9,7 @@
 
 #include "common.h"
 #include "numeric.h"
+#include "rules.h"
 
 namespace uep {
 
@@ -122,7 +123,6 @@ __device__ __forceinline__ float pr_swiglu(float gate, float up) {
 // the LDS with them (buffer loads into LDS).  A step's rows are 128 bytes in eight slots of 16;
 // slot s of row r holds bytes 16 (s ^ r % 8), so that the 16 rows that a wave reads together spread
 // over all banks.
-constexpr int kPtDepth = 128;
 
 // Rows are D bytes apart, so that workgroups at the same step, of whichever channels, ask the same
 // few memory channels where D is a multiple of a high power of two.  They begin at different steps
@@ -338,12 +338,11 @@ __global__ __launch_bounds__(kWC* kWR* kGroups* kWave) void pr_ring_kernel(PrArg
 // takes tile after tile: the next one's first two steps are under way while this one's results go
 // out.  Beside the buffers each wave has 4 KiB of LDS of its own: 2 to turn results into whole
 // lines, and the scales of this tile and the next.
-constexpr int kPtSide = 256, kPtThreads = 512;
+constexpr int kPtThreads = 512;
 constexpr int kPtBuf = kPtSide * kPtDepth;          // one buffer of one operand
 constexpr int kPtTurn = 4 * kPtBuf;                 // the waves' own parts
 constexpr int kPtScales = 2048, kPtScaleBytes = 768;
 constexpr int kPtBand = 8;
-constexpr int kPtMostOut = 1 << 21;                 // a tile's outputs are one span
 
 // What a workgroup knows of a tile.
 struct PtTile {
@@ -592,18 +591,12 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
   }
 }
 
-// Tiles of `side` rows are at most so many, whatever the table: every instance that has rows at
-// all leaves side - 1 of its last one empty.
-static int64_t pr_most_tiles(const PrArgs& a, int side) {
-  return (a.rows + std::min<int64_t>(a.n_inst, a.rows) * (side - 1)) / side;
-}
-
 // Launches of fewer than 2^32 threads each, over ranges of tiles.
 template <int kCh, int kRows, int kWC, int kWR, int kGroups, int kStages, bool kGlu>
 static uep_status pr_ring(const PrArgs& a, hipStream_t s) {
   constexpr int kWide = kGlu ? kCh / 2 : kCh, kThreads = kWC * kWR * kGroups * kWave;
   const int cols = (a.n_out + kWide - 1) / kWide;
-  const int64_t tiles = pr_most_tiles(a, kRows);
+  const int64_t tiles = pr_most_tiles(a.rows, a.n_inst, kRows);
   const int64_t most = ((1ll << 32) - 1) / kThreads / cols;
   for (int64_t t = 0; t < tiles; t += most) {
     const int n = (int)std::min(tiles - t, most);
@@ -615,12 +608,11 @@ static uep_status pr_ring(const PrArgs& a, hipStream_t s) {
 }
 
 // One workgroup for every CU; the tiles' number is known on the device only.
-constexpr int kPtGroups = 256;
 template <bool kGlu>
 static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   constexpr int kWide = kGlu ? kPtSide / 2 : kPtSide;
   const int cols = (a.n_out + kWide - 1) / kWide;
-  const int64_t tiles = pr_most_tiles(a, kPtSide);
+  const int64_t tiles = pr_most_tiles(a.rows, a.n_inst, kPtSide);
   // twice the tiles: a tile may be two workgroups' work
   hipLaunchKernelGGL((pr_tile_kernel<kGlu>),
                      dim3((unsigned)std::min<int64_t>(2 * tiles * cols, kPtGroups)),
@@ -629,71 +621,9 @@ static uep_status pr_tiles_of(const PrArgs& a, hipStream_t s) {
   return UEP_OK;
 }
 
-// Which tile.  Each form's time is a chip load of workgroups (`resident` a CU) times the steps of
-// the depth, at what a step was measured to take with one workgroup a CU (`one`) and with all
-// (`all`), plus what a load takes beside its steps (`load`: first loads, results; us).  Half a tile is
-// left over in every instance.  The two forms of a wave a step take their time by the weights that
-// they stream, and are weighed while each workgroup has a CU to itself.  The form that comes out
-// least is taken.  Rows past an instance's are loads that bring nothing, but not for nothing: a form
-// is weighed from `mean` rows an instance on (4096 channels, depth 4096, 72 rows in each of 32:
-// 113 us by 128 x 128, 144 by 128 x 64; 50 rows of 14, most of them in few: 88 us by 128 x 64, 107 by
-// 128 x 128; 13 rows of 34, 5840 channels, depth 5360: 75 us by 64 x 32, 89 by 128 x 64).
-// Measured, one instance, 4096 channels, depth 7168, us:
-//   rows            1    64   128   256   512  1024  8192 (8192 channels, depth 8192)
-//   taken         8.0  12.1  15.5  20.3  27.9  38.5   378
-//   next larger   9.3  16.0  20.5  27.8  37.5  53.5
-//   next smaller    -  17.8  19.4  27.6  38.5  55.2
-struct PrForm {
-  int ch, rows, mean, resident;
-  float one, all, load;
-};
-enum { kPrLarge, kPr128x128, kPr128x128Deep, kPr64x128, kPr128x64, kPr64x64, kPr64x32Deep,
-       kPr64x32, kPr32x32, kPr32x16, kPr16x16, kPrForms };
-constexpr PrForm kPrForm[kPrForms] = {
-    {256, 256, 96, 1, 1.50f, 1.50f, 5}, {128, 128, 64, 2, 0.93f, 1.09f, 8},
-    {128, 128, 80, 1, 0.66f, 0.66f, 5}, {64, 128, 80, 1, 0.47f, 0.47f, 4},
-    {128, 64, 24, 2, 0.60f, 0.87f, 6},  {64, 64, 24, 1, 0.34f, 0.34f, 3},
-    {64, 32, 0, 1, 0.27f, 0.27f, 2},    {64, 32, 0, 3, 0.32f, 0.65f, 5},
-    {32, 32, 0, 2, 0.20f, 0.31f, 3},    {32, 16, 0, 1, 0.055f, 0.14f, 2.2f},
-    {16, 16, 0, 1, 0.054f, 0.09f, 0.5f}};
-
-template <bool kGlu>
-static int pr_form(const PrArgs& a) {
-  const int64_t used = std::min<int64_t>(a.n_inst, a.rows);
-  const float steps = (float)((a.D + kPtDepth - 1) / kPtDepth);
-  // ids of tiles and offsets in a tile's outputs are 32-bit in the large kernel
-  const int64_t ids = pr_most_tiles(a, kPtSide) * (a.n_out / (kPtSide / 2) + 1ll);
-  const bool fits = a.n_out <= kPtMostOut && ids < (1ll << 31) - kPtGroups;
-  int best = kPr32x32;
-  float least = 0.0f;
-  for (int i = 0; i < kPrForms; ++i) {
-    const PrForm& f = kPrForm[i];
-    if ((i == kPrLarge && !fits) || a.rows < f.mean * used || (kGlu && f.ch < 32)) continue;
-    const int wide = kGlu ? f.ch / 2 : f.ch;
-    const int64_t cols = (a.n_out + wide - 1) / wide;
-    const int64_t groups = cols * std::max(used, (a.rows + f.rows - 1) / f.rows + used / 2);
-    const float loads = (float)groups / (256.0f * f.resident);
-    float us = f.load / 2 + steps * f.one;               // at most one workgroup a CU
-    if (i >= kPr32x16) {                                 // a wave a step: by the weights it reads
-      if (groups > 256) continue;
-      us = f.load + steps * (f.one + f.all * (float)(cols * used) / 256.0f);
-    } else if (i == kPrLarge) {                          // a last round of halves
-      const int64_t last = groups % 256;
-      us = (float)(groups / 256) + (last > 128 ? 1.0f : last > 0 ? 0.6f : 0.0f);
-      us *= steps * f.one + f.load;
-    } else if (f.resident == 1) {
-      us = (float)((groups + 255) / 256) * (steps * f.one + f.load);
-    } else if (groups > 256) {
-      us = std::max(us, loads * (steps * f.all + f.load));
-    }
-    if (least == 0.0f || us < least) least = us, best = i;
-  }
-  return best;
-}
-
 template <bool kGlu>
 static uep_status pr_run(const PrArgs& a, hipStream_t s) {
-  switch (pr_form<kGlu>(a)) {
+  switch (pr_form(a.rows, a.n_inst, a.n_out, a.D, kGlu)) {
     case kPrLarge: return pr_tiles_of<kGlu>(a, s);
     case kPr128x128: return pr_ring<128, 128, 4, 2, 1, 2, kGlu>(a, s);
     case kPr128x128Deep: return pr_ring<128, 128, 4, 2, 1, 4, kGlu>(a, s);
