@@ -734,7 +734,7 @@ uep_status uep_permute_quant(const uint16_t* x, const int32_t* dest_row, int32_t
  *   UEP_PRODUCT_PLAIN    out[p][n] = bf16(y[p][n])                                      n < N
  *   UEP_PRODUCT_SWIGLU   out[p][n] = bf16(silu(y[p][n]) y[p][N/2 + n])                n < N/2
  * with silu(g) = g / (1 + exp(-g)) (hardware exp2 and reciprocal, each within a unit in the last
- * place) and w those of the row's instance i = r * (E/R + S) + j: main r*E/R + j for j < E/R,
+ * place; 0 for gates below -174) and w those of the row's instance i = r * (E/R + S) + j: main r*E/R + j for j < E/R,
  * slot (r, j - E/R) otherwise.  S = 0 and R = 1: one matrix per expert; E = 1 then: a plain
  * product of all rows (a shared expert).
  *

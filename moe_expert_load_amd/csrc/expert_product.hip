@@ -113,9 +113,25 @@ __device__ __forceinline__ void pr_check_offsets(const PrArgs& a) {
 __device__ __forceinline__ float pr_scaled(int acc, float w_scale, float q_scale) {
   return (float)acc * w_scale * q_scale;
 }
-// gate / (1 + e^-gate) * up; exp2's argument rounded once, hardware exp2 and reciprocal
-__device__ __forceinline__ float pr_swiglu(float gate, float up) {
-  return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * gate)) * up;
+// gate / (1 + e^-gate) * up; exp2's argument rounded once, hardware exp2 and reciprocal.  Below -87 the
+// reciprocal leaves its range (it is 0 from -87.3 on), not the result if the up value is large: such
+// gates take e^gate by halves, one to each side.  Where the wave has any: for all of them 32768 rows
+// of 32 instances, 4096 x 7168, take 832 us instead of 825.
+__device__ __forceinline__ void pr_swiglu(float (&gate)[4], const float (&up)[4]) {
+  const bool far = fminf(fminf(gate[0], gate[1]), fminf(gate[2], gate[3])) < -87.0f;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = gate[i] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * gate[i])) * up[i];
+  if (ballot(far)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float half = __builtin_amdgcn_exp2f(0.72134752f * gate[i]);
+      if (gate[i] < -87.0f) y[i] = gate[i] * half * (up[i] * half);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) gate[i] = y[i];
 }
 
 // ---------------------------------------------------------------------------------------
@@ -315,13 +331,13 @@ __global__ __launch_bounds__(kWC* kWR* kGroups* kWave) void pr_ring_kernel(PrArg
     for (int c = 0; c < kCB; c += kGlu ? 2 : 1) {
       const int ch = c0 + (w_wave + 16 * c) / (kGlu ? 2 : 1) + lane / 16 * 4;
       if (ch >= a.n_out) continue;
-      float y[4];
+      float y[4], up[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         y[i] = pr_scaled(acc[c][r][i], w_scale[ch + i], q_scale);
-        if constexpr (kGlu)
-          y[i] = pr_swiglu(y[i], pr_scaled(acc[c + 1][r][i], w_scale[a.n_out + ch + i], q_scale));
+        if constexpr (kGlu) up[i] = pr_scaled(acc[c + 1][r][i], w_scale[a.n_out + ch + i], q_scale);
       }
+      if constexpr (kGlu) pr_swiglu(y, up);
       *reinterpret_cast<uint2*>(a.out + (tile.row0 + row) * a.n_out + ch) =
           uint2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
     }
@@ -564,9 +580,10 @@ __global__ __launch_bounds__(kPtThreads, 2) void pr_tile_kernel(PrArgs a, int co
           for (int i = 0; i < 4; ++i) y[i] = pr_scaled(acc[f][j][i], s[i], q_scale);
           if constexpr (kGlu) {
             const f32x4 s_up = *reinterpret_cast<const f32x4*>(scales + 64 + at);
+            float up[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              y[i] = pr_swiglu(y[i], pr_scaled(acc[f + 1][j][i], s_up[i], q_scale));
+            for (int i = 0; i < 4; ++i) up[i] = pr_scaled(acc[f + 1][j][i], s_up[i], q_scale);
+            pr_swiglu(y, up);
           }
           const int piece = (2 * o + l / 32) ^ l % 8;
           *reinterpret_cast<uint2*>(own + l % 16 * 128 + piece * 16 + l / 16 % 2 * 8) =
