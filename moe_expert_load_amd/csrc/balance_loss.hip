@@ -20,7 +20,7 @@ namespace uep {
 
 constexpr int kBlMaxE = 4096;
 constexpr int kBlMaxSeq = 65535;      // blocks of the second launch
-constexpr int kBlSliceWide = 4;
+constexpr int kBlSliceWide = 4;       // threads of a joining block for a slice of the experts
 
 // How the tokens fall into chunks of at most `size` tokens of one sequence each.  Equal
 // sequences have `per` chunks each.  Otherwise chunk numbers go by offset[g] / size + g, which
@@ -620,15 +620,12 @@ static uep_status bl_forward(const BlCall& c) {
   const BlChunks ch = bl_chunks(c.offset, c.n_tok, c.n_seq, size, false);
   bl_sum<T, kSig, kL, kNV, kVec, false>(c, ch);
   UEP_CHECK_LAUNCH();
-  // as many rows of threads as a sequence has chunks on the average; from 128 on the experts go to
-  // several blocks (1024 chunks of one sequence, 128 experts: 16.4 us by one block, 8.9 and 3.9 by eight)
+  // as many rows of threads as a sequence has chunks on the average
   const int64_t mean = bl_n_chunks(ch) / c.n_seq;
-  int wide = 16, slices = 1;
-  while (wide < 256 && 4 * wide < c.E) wide *= 2;
-  if (mean >= kBlSliced) {
-    wide = kBlSliceWide;
-    slices = (c.E + 4 * wide - 1) / (4 * wide);
-  }
+  int wide = kBlSliceWide, slices = 1;
+  if (bl_sliced(mean, c.E)) slices = (c.E + 4 * wide - 1) / (4 * wide);
+  else
+    while (wide < 256 && 4 * wide < c.E) wide *= 2;
   int threads = std::max(wide, kWave);
   while (threads < kBlJoin && threads / wide < mean) threads *= 2;
   hipLaunchKernelGGL(bl_join_kernel, dim3((unsigned)c.n_seq, slices), dim3(threads), 0, c.stream,
@@ -710,9 +707,10 @@ static size_t bl_workspace(char* ws, int64_t n_tok, int64_t n_seq, int E, BlPart
                                 bl_chunk_tokens(n_tok, E, 2, bl_sum_blocks(n_tok, E, 2)));
   const size_t chunks = (size_t)(n_tok / size + n_seq);
   const size_t row = bl_align(chunks * bl_pitch(E) * 4), tok = bl_align(chunks * 4);
-  // sliced only with kBlSliced chunks a sequence and more
+  // sliced: no more sequences than fill the rule's mean
   const size_t slices = (E + 4 * kBlSliceWide - 1) / (4 * kBlSliceWide);
-  const size_t sliced = std::min<size_t>(n_seq, chunks / kBlSliced + 1) * slices * sizeof(double);
+  const size_t most = std::min<size_t>(n_seq, chunks * E / kBlSliced + 1);
+  const size_t sliced = most * slices * sizeof(double);
   if (p) {
     p->loss = reinterpret_cast<double*>(ws + 2 * row + tok);
     p->prob = reinterpret_cast<float*>(ws);

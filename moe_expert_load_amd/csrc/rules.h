@@ -11,7 +11,6 @@ namespace uep {
 // ------------------------------------------------------------------------- balance loss
 constexpr int kBlThreads = 256;
 constexpr int kBlMaxChunk = 2048;     // tokens of a chunk
-constexpr int kBlSliced = 128;        // chunks of a sequence from which its experts are sliced
 
 // Lanes of a token: as few as hold the experts with 16 each (above 1024 experts 64 each).  With 32
 // a lane the sigmoid's gradient takes 226 registers and two waves a SIMD (262144 tokens of 256
@@ -23,10 +22,13 @@ static inline int bl_lanes_of(int E, int size) {
   return l;
 }
 
-// Blocks to aim at.  Where each leaves sums to be joined, four for every CU, or two where the scores
-// take less than the memory (fp32) and a block has no more than 256 KiB to read (262144 tokens of
-// 128 fp32 logits 32.7 -> 30.1 us, 32768 15.6 -> 13.5; of 262144 x 256 it would be 49.6 -> 52.5, in
-// bf16 33.8 -> 39.8).  In the gradient sixteen, so that one block's start is behind another's
+// Blocks to aim at.  Where each leaves sums to be joined, four for every CU, or two for fp32 logits
+// (half as many scores to a byte, of either kind) while a block has no more than 256 KiB to read.  One
+// loss, us a call, by two and by four: 65536 x 128 19.5 and 21.1 (sigmoid 19.9 and 21.3), 262144 x 128
+// 40.1 and 40.7 (41.0 and 41.4), 131072 x 256 38.5 and 40.4; past it 393216 x 128 61.5 and 52.2 (63.6 and
+// 52.8), 524288 x 128 64.3 and 64.1, 262144 x 256 61.0 and 62.8.  Chunks are powers of two: where 512
+// blocks come out as 384, as for 393216 x 32, two are the slower ones below it too, 26.6 and 24.9.
+// bf16 (262144 x 256) 39.8 and 33.8 of kernel.  In the gradient sixteen, so that one block's start is behind another's
 // stream (262144 x 256 bf16 sigmoid, added to others, with 4, 8 and 16: 104, 91 and 84 us).
 constexpr int kBlGradBlocks = 4096;
 static inline int bl_sum_blocks(int64_t n_tok, int E, int size) {
@@ -41,6 +43,14 @@ static inline int bl_chunk_tokens(int64_t n_tok, int E, int size, int blocks) {
   while (groups * passes * 2 <= kBlMaxChunk && n_tok > (int64_t)groups * passes * blocks) passes *= 2;
   return groups * passes;
 }
+
+// Whether several blocks join a sequence of `mean` chunks, each for some of its experts; their parts
+// of the loss take a launch of their own then.  One loss, us by one block and by several: 128
+// experts, 128 chunks 11.9 and 14.9, 500 chunks 16.3 and 15.0; 1000 experts, 32 chunks 12.1 and 14.5, 64
+// 15.2 and 14.9, 128 21.4 and 14.9; 4096 experts, 17 chunks 23.9 and 15.5.  (64 experts, 500 chunks
+// are on the wrong side: 17.3 and 15.8.)
+constexpr int64_t kBlSliced = 50000;
+static inline bool bl_sliced(int64_t mean, int E) { return mean * E >= kBlSliced; }
 
 // ---------------------------------------------------------------------- expert product
 constexpr int kPtDepth = 128;                       // a step of the depth

@@ -25,7 +25,7 @@ int chunk(int64_t n_tok, int E, int size, int grad) {
   return uep::bl_chunk_tokens(n_tok, E, size,
                               grad ? uep::kBlGradBlocks : uep::bl_sum_blocks(n_tok, E, size));
 }
-int sliced() { return uep::kBlSliced; }
+int sliced(int64_t mean, int E) { return uep::bl_sliced(mean, E); }
 int threads() { return uep::kBlThreads; }
 }
 """ % len(FORMS)
@@ -56,5 +56,6 @@ def chunk(n_tok, E, size, grad=False):
     return n, n * _lib().lanes(E, size) // _lib().threads()
 
 
-def sliced():
-    return _lib().sliced()
+def sliced(mean, E):
+    """Whether several blocks join a sequence of so many chunks on the average."""
+    return bool(_lib().sliced(ctypes.c_int64(mean), E))
