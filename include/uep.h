@@ -749,6 +749,8 @@ uep_status uep_permute_quant(const uint16_t* x, const int32_t* dest_row, int32_t
  *   out [rows][N or N/2] bf16 bits  out   not overlapping an input (UEP_EINVAL)
  *   err                       out  optional; UEP_ERR_OFFSET: a table that falls or leaves
  *                                  [0, rows]
+ * How the work is cut goes by `rows` and the number of instances, on the host: a buffer with many
+ * more rows than its table names takes longer than one of the table's size.
  * q, weights and out 16-byte aligned.  D % 16 == 0, D <= 65536, N % 8 == 0 (SwiGLU: 16),
  * N*D < 2^31, S <= 8, rows <= 2^29; otherwise UEP_EGEOM.
  * ------------------------------------------------------------------------- */

@@ -143,8 +143,8 @@ __device__ __forceinline__ void pr_swiglu(float (&gate)[4], const float (&up)[4]
 // Rows are D bytes apart, so that workgroups at the same step, of whichever channels, ask the same
 // few memory channels where D is a multiple of a high power of two.  They begin at different steps
 // instead: part `i` of `n` of the way through those before the last, which keeps its place (the
-// rest of the depth is cut off there).  (8192 rows of 32 instances, 4096 channels, depth 4096: 166
-// -> 147 us; 1024 rows 120 -> 105; 16 rows of one, 16384 channels 17 -> 14; depth 7168 the same.)
+// rest of the depth is cut off there).  (8192 rows of 32 instances, 4096 channels, depth 4096: 164
+// -> 148 us; 1024 rows 123 -> 105; 4096 rows of 4 95 -> 85; depth 7168 the same.)
 __device__ __forceinline__ int pt_first(int i, int n, int steps) { return i % n * (steps - 1) / n; }
 
 __device__ __forceinline__ i32x4 pt_span(const void* p, int64_t bytes) {
